@@ -313,7 +313,9 @@ def _encode(x, signed):
     e = torch.where(r > 0, torch.frexp(r).exponent - 1, -126)
     z = torch.clamp((-1 - e) // 3, 0, bits - 1)           # leading zeros of the code
     low = torch.exp2((bits - 1 - z).float())              # its leading one
-    c = torch.round((r * torch.exp2((bits + 2 + 2 * z).float()) - low) * np.float32(1 / 7).item()) + low - 1
+    # the interval's straight line, c = ((8^(z+1) r - 1) / 7) low + low - 1, with its slope and offset in 32 bits
+    slope = torch.exp2((bits + 2 + 2 * z).float()) * np.float32(1 / 7).item()
+    c = torch.round(r * slope + (low * np.float32(6 / 7).item() - 1))
     if signed:
         c = c + 128 * (blocks < 0)
     else:  # a positive second moment never becomes zero
