@@ -2,6 +2,7 @@
 optimizer update per touched row, as a C-ABI CUDA library (include/tbe.h) with a thin
 ctypes binding.  Nothing here computes on the CPU; the library must be built
 (``bwd_tbe_fwd_gb300.build.build()``) and a CUDA device must be present to run it."""
+from .dense import DenseAdamW, GradNorm, LayerNorm  # noqa: F401
 from .tbe import (  # noqa: F401
     BWD_STAGES,
     EXPORTED,

@@ -1,0 +1,163 @@
+// dense_common.cuh -- what the kernels of the dense side (tbe_dense.h) share: vectors of V elements
+// of a storage type, type dispatch on the host, and small reductions.
+#pragma once
+
+#include "tbe_dense.h"
+#include "tbe_internal.cuh"
+
+namespace tbe {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// V consecutive elements of storage type T as they lie in memory (a multiple of 4 bytes, or one
+// element), so that a row waiting in registers takes no more of them than its bytes.
+template <typename T, int V>
+struct Pack {
+  static constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+
+  // p is aligned to kBytes, or to 16 where that is less
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kBytes == 2) {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (kBytes == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      static_assert(kBytes % 16 == 0, "");
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kBytes == 2) {
+      *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+    } else if constexpr (kBytes == 4) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
+
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (std::is_same<T, float>::value) {
+      return __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+    } else {
+      return __half2float(__ushort_as_half(static_cast<unsigned short>((i & 1) ? w[i >> 1] >> 16 : w[i >> 1])));
+    }
+  }
+
+  // Round to nearest even.
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+    if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(f[i]);
+    } else if constexpr (V == 1) {
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+      else w[0] = __half_as_ushort(__float2half_rn(f[0]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+          w[i] = *reinterpret_cast<uint32_t*>(&h);
+        } else {
+          __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+          w[i] = *reinterpret_cast<uint32_t*>(&h);
+        }
+      }
+    }
+  }
+};
+
+// One element of a buffer whose type is only known at run time (weights, read once for many rows).
+__device__ __forceinline__ float load_any(const void* p, int type, int64_t i) {
+  if (type == TBE_F32) return static_cast<const float*>(p)[i];
+  if (type == TBE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v) {
+  if (type == TBE_F32) static_cast<float*>(p)[i] = v;
+  else if (type == TBE_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// Sum over the L lanes (a power of two, aligned) that a thread is one of.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+template <typename T> struct TypeTag { using type = T; };
+
+// Calls f with the type tag of a tbe_dtype.
+template <typename F>
+auto with_type(int dtype, F&& f) {
+  if (dtype == TBE_F32) return f(TypeTag<float>());
+  if (dtype == TBE_F16) return f(TypeTag<__half>());
+  return f(TypeTag<__nv_bfloat16>());
+}
+
+inline int dtype_bytes(int dtype) { return dtype == TBE_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == TBE_F32 || dtype == TBE_F16 || dtype == TBE_BF16; }
+inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// ------------------------------------------------------------------------------------------
+// Layer norm
+// ------------------------------------------------------------------------------------------
+// The validated problem, and what the kernels get of it.
+struct NormArgs {
+  int64_t rows, x_stride, y_stride, dx_stride;
+  const int32_t* col_offsets;   // device, or NULL: segment s starts at s * width
+  int segments, width, cols;    // width: the widest segment; cols: their sum
+  int wtype;
+  float eps;
+};
+
+tbe_status launch_norm_forward(const NormArgs& a, int xtype, int ytype, int vec, const void* x, const void* weight,
+                               const void* bias, void* y, float* mean, float* rstd, const DeviceInfo& dev,
+                               cudaStream_t s);
+// Row slots of the backward's sums over rows: each leaves one partial row of dweight and dbias.
+int norm_backward_slots(const NormArgs& a, const DeviceInfo& dev);
+tbe_status launch_norm_backward(const NormArgs& a, int xtype, int ytype, int vec, const void* dy, const void* x,
+                                const float* mean, const float* rstd, const void* weight, void* dx, void* dweight,
+                                void* dbias, float* partial, const DeviceInfo& dev, cudaStream_t s);
+
+// First column and width of segment s.  Both are clamped into the row, and to multiples of V, so that col_offsets that disagree with
+// the host's widths give wrong sums but no access outside a row and none that is misaligned.
+template <int V>
+__device__ __forceinline__ void segment_span(const NormArgs& a, int s, int* col, int* width) {
+  if (a.col_offsets == nullptr) {
+    *col = s * a.width;
+    *width = a.width;
+    return;
+  }
+  int c0 = min(max(__ldg(a.col_offsets + s), 0), a.cols), c1 = min(max(__ldg(a.col_offsets + s + 1), c0), a.cols);
+  c0 -= c0 % V;
+  int w = min(c1 - c0, a.width);
+  w -= w % V;
+  *col = c0;
+  *width = w;
+}
+
+}  // namespace tbe

@@ -1,0 +1,669 @@
+// k_adamw.cu -- one AdamW step of many tensors (tbe_adamw_update), the values of its 8-bit states
+// (tbe_adamw_state_values) and the global norm of many gradients (tbe_grad_norm).
+//
+// Each element is read and written once; all three are bound by DRAM.  A thread takes 8 consecutive
+// elements: 16 bytes of a 16-bit type, 32 of fp32, 8 of codes; a warp then takes one block of the 8-bit
+// states, whose scale needs one reduction over the warp and no shared memory.
+#include <cmath>
+
+#include "k_tensor_list.cuh"
+
+namespace tbe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 8;
+constexpr int kStep = kThreads * kVec;     // elements of a CTA's pass over its chunk
+constexpr int kScalar = 0xff;              // AdamEntry.head: the tensor's buffers share no vector alignment
+static_assert(TBE_Q8_BLOCK == 32 * kVec, "a warp takes one block");
+
+struct AdamEntry {
+  void* p;
+  const void* g;
+  float* master;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  int64_t n;
+  float lr_scale, decay;
+  int32_t head;   // elements before the first aligned vector, or kScalar (8-bit states: 0 or kScalar)
+  int32_t pad;
+};
+
+struct AdamScalars {
+  float beta1, beta2, one_minus_beta1, one_minus_beta2, log_beta1, log_beta2, eps, lr;
+  const float* clip;
+  int64_t* step;
+  uint32_t* ticket;
+  int advance;    // the call's last launch increments the step
+};
+
+template <int CAP> using AdamList = TensorList<AdamEntry, CAP>;
+constexpr int kLargeAdam = 360;
+static_assert(sizeof(AdamList<kLargeAdam>) + sizeof(AdamScalars) <= 32764, "kernel parameters");
+
+// What a step multiplies by, the same for every element of a tensor.
+struct AdamFactors {
+  float coef, beta1, beta2, omb1, omb2, step_size, inv_sqrt_bc2, eps, decay;
+};
+
+// The products and sums of the moments are rounded one by one (no fused multiply-add): the moments
+// are then the same in any program that evaluates the formulas in fp32, and so are their 8-bit codes.
+__device__ __forceinline__ void adam_element(const AdamFactors& f, float grad, float& p, float& m, float& v) {
+  const float g = __fmul_rn(grad, f.coef);
+  m = __fadd_rn(__fmul_rn(m, f.beta1), __fmul_rn(g, f.omb1));
+  v = __fadd_rn(__fmul_rn(v, f.beta2), __fmul_rn(__fmul_rn(g, g), f.omb2));
+  float root;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));  // within 1 ulp: far inside p's rounding
+  const float denom = fmaf(root, f.inv_sqrt_bc2, f.eps);
+  p = fmaf(-f.decay, p, p) - __fdividef(f.step_size * m, denom);
+}
+
+// 1 - beta^t, without the cancellation of small t.
+__device__ __forceinline__ float bias_correction(float log_beta, int64_t t) {
+  return -expm1f(static_cast<float>(t) * log_beta);
+}
+
+// False when the gradients' norm says that the step is to be left out.
+__device__ __forceinline__ bool adam_factors(const AdamScalars& s, float lr_scale, float decay, AdamFactors* f) {
+  f->coef = 1.f;
+  if (s.clip != nullptr) {
+    if (!isfinite(s.clip[0])) return false;
+    f->coef = s.clip[1];
+  }
+  const int64_t t = *s.step + 1;
+  const float lr = s.lr * lr_scale;
+  f->beta1 = s.beta1, f->beta2 = s.beta2, f->omb1 = s.one_minus_beta1, f->omb2 = s.one_minus_beta2;
+  f->step_size = lr / bias_correction(s.log_beta1, t);
+  f->inv_sqrt_bc2 = __frsqrt_rn(bias_correction(s.log_beta2, t));
+  f->eps = s.eps;
+  f->decay = lr * decay;
+  return true;
+}
+
+__device__ __forceinline__ void advance_step(const AdamScalars& s) {
+  // every CTA has read the step before the last one to arrive changes it
+  if (last_cta(s.ticket) && s.advance && threadIdx.x == 0) *s.step += 1;
+}
+
+// 8 elements at p (aligned), or the first `n` of them one by one.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&f)[kVec]) {
+  if (vec && n >= kVec) {
+    Pack<T, kVec> v;
+    v.load(p);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] = v.get(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      Pack<T, 1> v;
+      v.zero();
+      if (i < n) v.load(p + i);
+      f[i] = v.get(0);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&f)[kVec]) {
+  if (vec && n >= kVec) {
+    Pack<T, kVec> v;
+    v.set(f);
+    v.store(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (i < n) {
+        Pack<T, 1> v;
+        const float one[1] = {f[i]};
+        v.set(one);
+        v.store(p + i);
+      }
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// 32-bit states
+// ------------------------------------------------------------------------------------------
+template <typename P, typename G, bool MASTER>
+__device__ __forceinline__ void adam_step_at(const AdamEntry& e, const AdamFactors& f, int64_t at, int n, bool vec) {
+  float p[kVec], g[kVec], m[kVec], v[kVec];
+  load8(static_cast<const G*>(e.g) + at, n, vec, g);
+  load8(static_cast<const float*>(e.m) + at, n, vec, m);
+  load8(static_cast<const float*>(e.v) + at, n, vec, v);
+  if constexpr (MASTER) load8(e.master + at, n, vec, p);
+  else load8(static_cast<const P*>(e.p) + at, n, vec, p);
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) adam_element(f, g[i], p[i], m[i], v[i]);
+  if constexpr (MASTER) store8(e.master + at, n, vec, p);
+  store8(static_cast<P*>(e.p) + at, n, vec, p);
+  store8(static_cast<float*>(e.m) + at, n, vec, m);
+  store8(static_cast<float*>(e.v) + at, n, vec, v);
+}
+
+template <typename P, typename G, bool MASTER, int CAP>
+__global__ void __launch_bounds__(kThreads)
+    adamw_kernel(const __grid_constant__ AdamList<CAP> list, const __grid_constant__ AdamScalars s) {
+  if (blockIdx.x < list.first[list.count]) {
+    const int t = tensor_of_chunk(list, blockIdx.x);
+    const AdamEntry& e = list.e[t];
+    AdamFactors f;
+    if (!adam_factors(s, e.lr_scale, e.decay, &f)) return;  // in every CTA alike
+    const bool vec = e.head != kScalar;
+    const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[t]) * list.chunk_elems;
+    const int64_t end = min(begin + list.chunk_elems, e.n);
+    if (vec) {
+      // vectors start `head` elements in; the elements before belong to the first chunk's first thread
+      if (begin == 0 && threadIdx.x == 0 && e.head > 0)
+        adam_step_at<P, G, MASTER>(e, f, 0, static_cast<int>(min(static_cast<int64_t>(e.head), e.n)), false);
+      const int64_t stop = min(end + e.head, e.n);
+      for (int64_t at = begin + e.head + threadIdx.x * kVec; at < stop; at += kStep)
+        adam_step_at<P, G, MASTER>(e, f, at, static_cast<int>(min(static_cast<int64_t>(kVec), stop - at)), true);
+    } else {
+      for (int64_t at = begin + threadIdx.x; at < end; at += kThreads) adam_step_at<P, G, MASTER>(e, f, at, 1, false);
+    }
+  } else if (s.clip != nullptr && !isfinite(s.clip[0])) {
+    return;  // no tensor has an element, and the step is left out
+  }
+  advance_step(s);
+}
+
+// ------------------------------------------------------------------------------------------
+// 8-bit states
+// ------------------------------------------------------------------------------------------
+// Scales below this (whose reciprocals would leave fp32) count as zero.
+constexpr float kQ8Least = 0x1p-120f;
+
+// Code of magnitude r in [0, 1] with BITS bits: z leading zeros by the power of 8 that r lies below, then
+// the interval's straight line, rounded to the nearest integer by the addition of 1.5 * 2^23.
+template <int BITS>
+__device__ __forceinline__ uint32_t q8_encode(float r) {
+  const int e = static_cast<int>(__float_as_uint(r) >> 23);
+  const int z = max(min(((126 - e) * 0x5556) >> 16, BITS - 1), 0);  // (126 - e) / 3
+  const float slope = __uint_as_float(__float_as_uint(1.f / 7.f) + (static_cast<uint32_t>(BITS + 2 + 2 * z) << 23));
+  const float low = __uint_as_float(static_cast<uint32_t>(127 + BITS - 1 - z) << 23);
+  const float offset = __fadd_rn(__fmul_rn(low, 6.f / 7.f), -1.f);
+  return __float_as_uint(__fadd_rn(__fadd_rn(__fmul_rn(r, slope), offset), 12582912.f)) & 0xffu;
+}
+
+// The values of two codes (the low 8 bits of each half of `pair`), in units of the scale: with c the
+// code, low its leading one, (7 c + 7 - 6 low) low^2 2^(-3 BITS); every step is exact in fp16.
+template <int BITS>
+__device__ __forceinline__ __half2 q8_decode2(uint32_t pair) {
+  const uint32_t magic = pair | 0x64006400u;  // 1024 + c
+  const __half2 c = __hadd2(*reinterpret_cast<const __half2*>(&magic), __float2half2_rn(-1024.f));
+  uint32_t low_bits = *reinterpret_cast<const uint32_t*>(&c) & 0x7c007c00u;
+  const __half2 low = *reinterpret_cast<const __half2*>(&low_bits);
+  // BITS = 8: q = 7 c + 7 - 6 low, times (low 2^-12)^2; BITS = 7: q / 2, times (low 2^-10)^2
+  constexpr float k = BITS == 8 ? 1.f : 0.5f;
+  const __half2 q = __hfma2(low, __float2half2_rn(-6.f * k), __hfma2(c, __float2half2_rn(7.f * k), __float2half2_rn(7.f * k)));
+  const __half2 lows = __hmul2(low, __float2half2_rn(BITS == 8 ? 0x1p-12f : 0x1p-10f));
+  return __hmul2(__hmul2(q, lows), lows);
+}
+
+// 8 codes in two words -> fp32; SIGNED: the top bit is the sign.
+template <bool SIGNED>
+__device__ __forceinline__ void q8_values(uint2 codes, float scale, float (&f)[kVec]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w = h ? codes.y : codes.x;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t pair = __byte_perm(w, 0, k ? 0x4342 : 0x4140);  // two codes, each in a half
+      __half2 d = q8_decode2<SIGNED ? 7 : 8>(SIGNED ? pair & 0x007f007fu : pair);
+      if (SIGNED) {
+        uint32_t b = *reinterpret_cast<uint32_t*>(&d) | ((pair & 0x00800080u) << 8);
+        d = *reinterpret_cast<__half2*>(&b);
+      }
+      const float2 v = __half22float2(d);
+      f[4 * h + 2 * k] = __fmul_rn(v.x, scale);
+      f[4 * h + 2 * k + 1] = __fmul_rn(v.y, scale);
+    }
+  }
+}
+
+__device__ __forceinline__ uint2 load_codes(const void* base, int64_t at, int n, bool vec) {
+  const uint8_t* p = static_cast<const uint8_t*>(base) + at;
+  if (vec && n >= kVec) return *reinterpret_cast<const uint2*>(p);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kVec; ++i)
+    if (i < n) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_codes(void* base, int64_t at, int n, bool vec, uint2 c) {
+  uint8_t* p = static_cast<uint8_t*>(base) + at;
+  if (vec && n >= kVec) {
+    *reinterpret_cast<uint2*>(p) = c;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kVec; ++i)
+    if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i % 4)));
+}
+
+// Codes of a warp's block, 8 values to a lane, and its scale.  Magnitudes are compared as integers, which
+// orders them and puts NaN above infinity: a block with either gets it as its scale.
+template <bool SIGNED>
+__device__ __forceinline__ uint2 q8_block(const float (&f)[kVec], float* scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+  float a = __uint_as_float(__reduce_max_sync(kFull, top));
+  if (a < kQ8Least) a = 0.f;
+  const float inv = a > 0.f ? __fdiv_rn(1.f, a) : 0.f;
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const float r = __fmul_rn(fabsf(f[i]), inv);
+    uint32_t c = q8_encode<SIGNED ? 7 : 8>(r);
+    if (SIGNED) c |= (__float_as_uint(f[i]) >> 24) & 0x80u;
+    else if (r > 0.f) c = max(c, 1u);
+    w[i / 4] |= c << (8 * (i % 4));
+  }
+  *scale = a;
+  return make_uint2(w[0], w[1]);
+}
+
+template <typename P, typename G, bool MASTER, int CAP>
+__global__ void __launch_bounds__(kThreads)
+    adamw_q8_kernel(const __grid_constant__ AdamList<CAP> list, const __grid_constant__ AdamScalars s) {
+  if (blockIdx.x < list.first[list.count]) {
+    const int t = tensor_of_chunk(list, blockIdx.x);
+    const AdamEntry& e = list.e[t];
+    AdamFactors f;
+    if (!adam_factors(s, e.lr_scale, e.decay, &f)) return;  // in every CTA alike
+    const bool vec = e.head != kScalar;
+    const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[t]) * list.chunk_elems;
+    const int64_t end = min(begin + list.chunk_elems, e.n);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int64_t block = begin + warp * TBE_Q8_BLOCK; block < end; block += kStep) {
+      const int64_t at = block + lane * kVec;
+      const int n = static_cast<int>(min(max(e.n - at, int64_t(0)), static_cast<int64_t>(kVec)));
+      float p[kVec], g[kVec], m[kVec], v[kVec];
+      const uint2 mc = load_codes(e.m, at, n, vec), vc = load_codes(e.v, at, n, vec);
+      load8(static_cast<const G*>(e.g) + at, n, vec, g);
+      if constexpr (MASTER) load8(e.master + at, n, vec, p);
+      else load8(static_cast<const P*>(e.p) + at, n, vec, p);
+      q8_values<true>(mc, e.ms[block / TBE_Q8_BLOCK], m);
+      q8_values<false>(vc, e.vs[block / TBE_Q8_BLOCK], v);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        adam_element(f, g[i], p[i], m[i], v[i]);
+        if (i >= n) m[i] = v[i] = 0.f;  // past the tensor's end: no part of the block's scale
+      }
+      if constexpr (MASTER) store8(e.master + at, n, vec, p);
+      store8(static_cast<P*>(e.p) + at, n, vec, p);
+      float a, b;
+      store_codes(e.m, at, n, vec, q8_block<true>(m, &a));
+      store_codes(e.v, at, n, vec, q8_block<false>(v, &b));
+      if (lane == 0) {
+        e.ms[block / TBE_Q8_BLOCK] = a;
+        e.vs[block / TBE_Q8_BLOCK] = b;
+      }
+    }
+  } else if (s.clip != nullptr && !isfinite(s.clip[0])) {
+    return;
+  }
+  advance_step(s);
+}
+
+// ------------------------------------------------------------------------------------------
+// Values of the 8-bit states
+// ------------------------------------------------------------------------------------------
+struct ValuesEntry {
+  const void* m;
+  const void* v;
+  const float* ms;
+  const float* vs;
+  float* m_out;
+  float* v_out;
+  int64_t n;
+  int32_t vec;
+  int32_t pad;
+};
+constexpr int kLargeValues = 480;
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) q8_values_kernel(const __grid_constant__ TensorList<ValuesEntry, CAP> list) {
+  const int t = tensor_of_chunk(list, blockIdx.x);
+  const ValuesEntry& e = list.e[t];
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[t]) * list.chunk_elems;
+  const int64_t end = min(begin + list.chunk_elems, e.n);
+  for (int64_t at = begin + threadIdx.x * kVec; at < end; at += kStep) {
+    const int n = static_cast<int>(min(end - at, static_cast<int64_t>(kVec)));
+    float f[kVec];
+    if (e.m_out != nullptr) {
+      q8_values<true>(load_codes(e.m, at, n, e.vec), e.ms[at / TBE_Q8_BLOCK], f);
+      store8(e.m_out + at, n, e.vec, f);
+    }
+    if (e.v_out != nullptr) {
+      q8_values<false>(load_codes(e.v, at, n, e.vec), e.vs[at / TBE_Q8_BLOCK], f);
+      store8(e.v_out + at, n, e.vec, f);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Gradient norm
+// ------------------------------------------------------------------------------------------
+struct NormEntry {
+  const void* g;
+  int64_t n;
+};
+constexpr int kLargeNorm = 1500;
+static_assert(sizeof(TensorList<NormEntry, kLargeNorm>) + 64 <= 32764, "kernel parameters");
+
+constexpr int kNormMaxGrid = 4096;
+struct NormWs {
+  uint32_t ticket;
+  uint32_t pad;
+  double earlier;                 // the squares of the call's earlier launches
+  double partial[kNormMaxGrid];   // of this launch's CTAs
+};
+
+template <typename G, int CAP>
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_kernel(const __grid_constant__ TensorList<NormEntry, CAP> list, NormWs* ws, int first, int last,
+                     float max_norm, float* out) {
+  double sum = 0.0;
+  for (uint32_t chunk = blockIdx.x; chunk < list.first[list.count]; chunk += gridDim.x) {
+    const int t = tensor_of_chunk(list, chunk);
+    const G* g = static_cast<const G*>(list.e[t].g);
+    const int64_t n = list.e[t].n, begin = static_cast<int64_t>(chunk - list.first[t]) * list.chunk_elems;
+    const int64_t end = min(begin + list.chunk_elems, n);
+    // elements before the first 16-byte boundary, whole vectors, the rest
+    const int64_t head = min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(g + begin) % 16) % 16 / sizeof(G)), end - begin);
+    float q = 0.f;
+    if (threadIdx.x < head) {
+      Pack<G, 1> v;
+      v.load(g + begin + threadIdx.x);
+      q = v.get(0) * v.get(0);
+    }
+    constexpr int N = 16 / sizeof(G);
+    const int64_t vectors = (end - begin - head) / N;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < vectors; i += kThreads) {
+      Pack<G, N> v;
+      v.load(g + begin + head + i * N);
+#pragma unroll
+      for (int k = 0; k < N; ++k) q = fmaf(v.get(k), v.get(k), q);
+    }
+    const int64_t tail = begin + head + vectors * N + threadIdx.x;
+    if (tail < end) {
+      Pack<G, 1> v;
+      v.load(g + tail);
+      q = fmaf(v.get(0), v.get(0), q);
+    }
+    sum += static_cast<double>(q);
+  }
+  __shared__ double part[kThreads / 32];
+  auto block_sum = [&](double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    double total = 0.0;
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) total += part[k];
+    return total;
+  };
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) ws->partial[blockIdx.x] = sum;
+  if (!last_cta(&ws->ticket)) return;
+  sum = 0.0;
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += kThreads) sum += __ldcg(&ws->partial[i]);
+  sum = block_sum(sum);
+  if (threadIdx.x != 0) return;
+  if (!first) sum += ws->earlier;
+  if (!last) {
+    ws->earlier = sum;
+    return;
+  }
+  const float norm = static_cast<float>(sqrt(sum));
+  out[0] = norm;
+  const float coef = __fdiv_rn(max_norm, norm + 1e-6f);
+  out[1] = coef > 1.f ? 1.f : coef;
+}
+
+// ------------------------------------------------------------------------------------------
+// Host
+// ------------------------------------------------------------------------------------------
+// Elements of a chunk: 4 passes of a CTA, or one while that leaves SMs without work.
+uint32_t chunk_elems(int64_t total, const DeviceInfo& dev) {
+  return total / (4 * kStep) >= 4 * static_cast<int64_t>(dev.sms) ? 4 * kStep : kStep;
+}
+
+// Splits the tensors into launches of at most the list's capacity and at most 2^31 - 1 chunks; fill(i, entry)
+// describes tensor i, go(list, first, last) launches.
+template <typename Entry, int LARGE, typename Numel, typename Fill, typename Go>
+tbe_status for_lists(int count, uint32_t chunk, Numel&& numel, Fill&& fill, Go&& go) {
+  int at = 0;
+  bool first = true;
+  do {
+    auto part = [&](auto& list, int cap) {
+      list.chunk_elems = chunk;
+      int k = 0;
+      int64_t chunks = 0;
+      while (k < cap && at < count) {
+        const int64_t more = (numel(at) + chunk - 1) / chunk;
+        if (chunks + more > INT32_MAX) break;
+        list.first[k] = static_cast<uint32_t>(chunks);
+        fill(at, &list.e[k]);
+        chunks += more;
+        ++k;
+        ++at;
+      }
+      list.count = k;
+      list.first[k] = static_cast<uint32_t>(chunks);
+      const tbe_status st = go(list, first, at >= count);
+      first = false;
+      return st;
+    };
+    tbe_status st;
+    if (count - at <= kSmallList) {
+      TensorList<Entry, kSmallList> list;
+      st = part(list, kSmallList);
+    } else {
+      TensorList<Entry, LARGE> list;
+      st = part(list, LARGE);
+    }
+    if (st != TBE_OK) return st;
+  } while (at < count);
+  return TBE_OK;
+}
+
+constexpr int64_t kMaxNumel = int64_t(1) << 40;  // one tensor's chunks fit a launch
+
+// Elements before the first at which every buffer is aligned for vectors of 8, or kScalar.
+int vector_head(const tbe_dense_tensor& d, int pdtype, int gdtype) {
+  auto congruent = [](const void* p, int size, int head) {
+    return (reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(head) * size) % 16 == 0;
+  };
+  for (int head = 0; head < kVec; ++head) {
+    if (congruent(d.param, dtype_bytes(pdtype), head) && congruent(d.grad, dtype_bytes(gdtype), head) &&
+        congruent(d.exp_avg, 4, head) && congruent(d.exp_avg_sq, 4, head) && congruent(d.master, 4, d.master ? head : 0))
+      return head;
+  }
+  return kScalar;
+}
+
+tbe_status check_adamw(const tbe_adamw_problem* p, bool values_only) {
+  if (p == nullptr || p->count < 0 || (p->count > 0 && p->tensors == nullptr)) return TBE_ERR_INVALID_ARG;
+  if (!dtype_ok(p->pdtype) || !dtype_ok(p->gdtype)) return TBE_ERR_UNSUPPORTED;
+  if (p->states != TBE_STATE_F32 && p->states != TBE_STATE_Q8) return TBE_ERR_INVALID_ARG;
+  if (!(p->beta1 >= 0 && p->beta1 < 1 && p->beta2 >= 0 && p->beta2 < 1)) return TBE_ERR_INVALID_ARG;
+  if (!(p->eps >= 0) || std::isinf(p->eps)) return TBE_ERR_INVALID_ARG;
+  const bool q8 = p->states == TBE_STATE_Q8;
+  bool master = false, plain = false;
+  for (int i = 0; i < p->count; ++i) {
+    const tbe_dense_tensor& d = p->tensors[i];
+    if (d.numel < 0) return TBE_ERR_INVALID_ARG;
+    if (d.numel > kMaxNumel) return TBE_ERR_UNSUPPORTED;
+    if (d.numel == 0) continue;
+    if (d.exp_avg == nullptr || d.exp_avg_sq == nullptr) return TBE_ERR_INVALID_ARG;
+    if (q8 && (d.exp_avg_scale == nullptr || d.exp_avg_sq_scale == nullptr || !is_aligned(d.exp_avg_scale, 4) ||
+               !is_aligned(d.exp_avg_sq_scale, 4)))
+      return TBE_ERR_INVALID_ARG;
+    if (values_only) continue;
+    if (d.param == nullptr || d.grad == nullptr || !is_aligned(d.param, dtype_bytes(p->pdtype)) ||
+        !is_aligned(d.grad, dtype_bytes(p->gdtype)) || !is_aligned(d.master, 4))
+      return TBE_ERR_INVALID_ARG;
+    if (!q8 && (!is_aligned(d.exp_avg, 4) || !is_aligned(d.exp_avg_sq, 4))) return TBE_ERR_INVALID_ARG;
+    if (!std::isfinite(d.lr_scale) || !std::isfinite(d.weight_decay)) return TBE_ERR_INVALID_ARG;
+    (d.master != nullptr ? master : plain) = true;
+  }
+  if (master && (plain || p->pdtype == TBE_F32)) return TBE_ERR_UNSUPPORTED;  // all tensors or none, 16-bit params
+  return TBE_OK;
+}
+
+template <typename P, typename G, bool MASTER>
+tbe_status launch_adamw(const tbe_adamw_problem& prob, AdamScalars sc, const DeviceInfo& dev, cudaStream_t s) {
+  int64_t total = 0;
+  for (int i = 0; i < prob.count; ++i) total += prob.tensors[i].numel;
+  const bool q8 = prob.states == TBE_STATE_Q8;
+  return for_lists<AdamEntry, kLargeAdam>(
+      prob.count, chunk_elems(total, dev), [&](int i) { return prob.tensors[i].numel; },
+      [&](int i, AdamEntry* e) {
+        const tbe_dense_tensor& d = prob.tensors[i];
+        int head = d.numel == 0 ? 0 : kScalar;
+        if (d.numel > 0 && q8) {
+          if (is_aligned(d.param, 16) && is_aligned(d.grad, 16) && is_aligned(d.master, 16) && is_aligned(d.exp_avg, 8) &&
+              is_aligned(d.exp_avg_sq, 8))
+            head = 0;
+        } else if (d.numel > 0) {
+          head = vector_head(d, prob.pdtype, prob.gdtype);
+        }
+        *e = AdamEntry{d.param,         d.grad,  d.master,   d.exp_avg,      d.exp_avg_sq, d.exp_avg_scale,
+                       d.exp_avg_sq_scale, d.numel, d.lr_scale, d.weight_decay, head,         0};
+      },
+      [&](auto& list, bool, bool last) {
+        constexpr int CAP = static_cast<int>(sizeof(list.e) / sizeof(list.e[0]));
+        const uint32_t chunks = list.first[list.count];
+        sc.advance = last;
+        const unsigned grid = chunks > 0 ? chunks : 1;
+        if (q8) adamw_q8_kernel<P, G, MASTER, CAP><<<grid, kThreads, 0, s>>>(list, sc);
+        else adamw_kernel<P, G, MASTER, CAP><<<grid, kThreads, 0, s>>>(list, sc);
+        note_launch();
+        return cuda_status(cudaGetLastError());
+      });
+}
+
+}  // namespace
+}  // namespace tbe
+
+using namespace tbe;
+
+extern "C" {
+
+size_t tbe_grad_norm_workspace_size(void) { return sizeof(NormWs); }
+
+tbe_status tbe_grad_norm(int32_t count, const void* const* grads, const int64_t* numels, tbe_dtype dtype, float max_norm,
+                         float* out, void* ws, size_t ws_bytes, void* stream) {
+  if (count < 0 || (count > 0 && (grads == nullptr || numels == nullptr)) || out == nullptr || !is_aligned(out, 4))
+    return TBE_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype)) return TBE_ERR_UNSUPPORTED;
+  if (!(max_norm >= 0)) return TBE_ERR_INVALID_ARG;
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    if (numels[i] < 0) return TBE_ERR_INVALID_ARG;
+    if (numels[i] > kMaxNumel) return TBE_ERR_UNSUPPORTED;
+    if (numels[i] > 0 && (grads[i] == nullptr || !is_aligned(grads[i], dtype_bytes(dtype)))) return TBE_ERR_INVALID_ARG;
+    total += numels[i];
+  }
+  if (ws == nullptr || ws_bytes < sizeof(NormWs)) return TBE_ERR_WORKSPACE;
+  if (!is_aligned(ws, 16)) return TBE_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  const tbe_status st = device_info(&dev);
+  if (st != TBE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return with_type(dtype, [&](auto tag) {
+    using G = typename decltype(tag)::type;
+    return for_lists<NormEntry, kLargeNorm>(
+        count, chunk_elems(total, dev), [&](int i) { return numels[i]; },
+        [&](int i, NormEntry* e) { *e = NormEntry{grads[i], numels[i]}; },
+        [&](auto& list, bool first, bool last) {
+          constexpr int CAP = static_cast<int>(sizeof(list.e) / sizeof(list.e[0]));
+          const int64_t chunks = list.first[list.count];
+          const int grid = persistent_grid(grad_norm_kernel<G, CAP>, kThreads, 0, dev, chunks < kNormMaxGrid ? chunks : kNormMaxGrid);
+          grad_norm_kernel<G, CAP><<<grid, kThreads, 0, s>>>(list, static_cast<NormWs*>(ws), first, last, max_norm, out);
+          note_launch();
+          return cuda_status(cudaGetLastError());
+        });
+  });
+}
+
+size_t tbe_adamw_workspace_size(void) { return 16; }
+
+tbe_status tbe_adamw_update(const tbe_adamw_problem* prob, float lr, const float* clip, int64_t* step, void* ws,
+                            size_t ws_bytes, void* stream) {
+  tbe_status st = check_adamw(prob, false);
+  if (st != TBE_OK) return st;
+  if (!std::isfinite(lr) || step == nullptr || !is_aligned(step, 8) || !is_aligned(clip, 4)) return TBE_ERR_INVALID_ARG;
+  if (ws == nullptr || ws_bytes < tbe_adamw_workspace_size()) return TBE_ERR_WORKSPACE;
+  if (!is_aligned(ws, 16)) return TBE_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != TBE_OK) return st;
+  AdamScalars sc;
+  sc.beta1 = static_cast<float>(prob->beta1);
+  sc.beta2 = static_cast<float>(prob->beta2);
+  sc.one_minus_beta1 = static_cast<float>(1.0 - prob->beta1);
+  sc.one_minus_beta2 = static_cast<float>(1.0 - prob->beta2);
+  sc.log_beta1 = static_cast<float>(std::log(prob->beta1));  // beta = 0: -infinity, whose correction is 1
+  sc.log_beta2 = static_cast<float>(std::log(prob->beta2));
+  sc.eps = prob->eps;
+  sc.lr = lr;
+  sc.clip = clip;
+  sc.step = step;
+  sc.ticket = static_cast<uint32_t*>(ws);
+  sc.advance = 0;
+  bool master = false;
+  for (int i = 0; i < prob->count; ++i) master = master || (prob->tensors[i].numel > 0 && prob->tensors[i].master != nullptr);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return with_type(prob->pdtype, [&](auto pt) {
+    return with_type(prob->gdtype, [&](auto gt) {
+      using P = typename decltype(pt)::type;
+      using G = typename decltype(gt)::type;
+      if constexpr (sizeof(P) == 2)
+        if (master) return launch_adamw<P, G, true>(*prob, sc, dev, s);
+      return launch_adamw<P, G, false>(*prob, sc, dev, s);
+    });
+  });
+}
+
+tbe_status tbe_adamw_state_values(const tbe_adamw_problem* prob, float* const* exp_avg_values,
+                                  float* const* exp_avg_sq_values, void* stream) {
+  tbe_status st = check_adamw(prob, true);
+  if (st != TBE_OK) return st;
+  if (prob->states != TBE_STATE_Q8) return TBE_ERR_INVALID_ARG;
+  int64_t total = 0;
+  for (int i = 0; i < prob->count; ++i) {
+    if (prob->tensors[i].numel == 0) continue;
+    total += prob->tensors[i].numel;
+    if (exp_avg_values != nullptr && !is_aligned(exp_avg_values[i], 4)) return TBE_ERR_INVALID_ARG;
+    if (exp_avg_sq_values != nullptr && !is_aligned(exp_avg_sq_values[i], 4)) return TBE_ERR_INVALID_ARG;
+  }
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != TBE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return for_lists<ValuesEntry, kLargeValues>(
+      prob->count, chunk_elems(total, dev), [&](int i) { return prob->tensors[i].numel; },
+      [&](int i, ValuesEntry* e) {
+        const tbe_dense_tensor& d = prob->tensors[i];
+        float* m = exp_avg_values != nullptr ? exp_avg_values[i] : nullptr;
+        float* v = exp_avg_sq_values != nullptr ? exp_avg_sq_values[i] : nullptr;
+        const bool vec = is_aligned(d.exp_avg, 8) && is_aligned(d.exp_avg_sq, 8) && is_aligned(m, 16) && is_aligned(v, 16);
+        *e = ValuesEntry{d.exp_avg, d.exp_avg_sq, d.exp_avg_scale, d.exp_avg_sq_scale, m, v, d.numel, vec, 0};
+      },
+      [&](auto& list, bool, bool) {
+        constexpr int CAP = static_cast<int>(sizeof(list.e) / sizeof(list.e[0]));
+        const uint32_t chunks = list.first[list.count];
+        if (chunks == 0) return TBE_OK;
+        q8_values_kernel<CAP><<<chunks, kThreads, 0, s>>>(list);
+        note_launch();
+        return cuda_status(cudaGetLastError());
+      });
+}
+
+}  // extern "C"

@@ -43,6 +43,9 @@ EXPORTED = (
     "tbe_backward_update", "tbe_backward_metadata", "tbe_status_string", "tbe_version",
     "tbe_last_cuda_error", "tbe_backward_update_noalloc", "tbe_backward_prepare", "tbe_psw_gradient",
     "tbe_bounds_check_offsets", "tbe_selftest_wait_timeout",
+    "tbe_layer_norm_forward", "tbe_layer_norm_backward_workspace_size", "tbe_layer_norm_backward",
+    "tbe_grad_norm_workspace_size", "tbe_grad_norm", "tbe_adamw_workspace_size", "tbe_adamw_update",
+    "tbe_adamw_state_values",
 )
 TBE_STATIC_SCRATCH_BYTES = 64 * 1024 * 1024
 
