@@ -100,6 +100,40 @@ __device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v)
   else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
+// V weights from column c on (1 or 0 where there are none), with vector loads where the buffer allows.
+template <int V>
+__device__ __forceinline__ void load_weights(const void* p, int type, int64_t c, float none, float (&f)[V]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = none;
+  } else if (V > 1 && type == TBE_F32 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    Pack<float, V> v;
+    v.load(static_cast<const float*>(p) + c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = v.get(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = load_any(p, type, c + i);
+  }
+}
+
+// Asynchronous copy of one thread's BYTES (8, or a multiple of 16) into its own place in shared memory; the thread
+// that copied them is the only one to read them, after async_wait, so no barrier is needed.
+template <int BYTES>
+__device__ __forceinline__ void async_copy(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 8) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  } else {
+    static_assert(BYTES == 16, "");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  }
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // Sum over the L lanes (a power of two, aligned) that a thread is one of.
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {

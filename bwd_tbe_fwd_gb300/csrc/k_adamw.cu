@@ -48,16 +48,25 @@ struct AdamFactors {
   float coef, beta1, beta2, omb1, omb2, step_size, inv_sqrt_bc2, eps, decay;
 };
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The products and sums of the moments are rounded one by one (no fused multiply-add): the moments
 // are then the same in any program that evaluates the formulas in fp32, and so are their 8-bit codes.
+// The root and the reciprocal are the hardware's (within 2^-22 together, far inside p's rounding),
+// in the forms without subnormals, one instruction each: a root counts as at least 2^-63, which matters only where
+// eps is smaller still.
 __device__ __forceinline__ void adam_element(const AdamFactors& f, float grad, float& p, float& m, float& v) {
   const float g = __fmul_rn(grad, f.coef);
   m = __fadd_rn(__fmul_rn(m, f.beta1), __fmul_rn(g, f.omb1));
   v = __fadd_rn(__fmul_rn(v, f.beta2), __fmul_rn(__fmul_rn(g, g), f.omb2));
-  float root;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));  // within 1 ulp: far inside p's rounding
-  const float denom = fmaf(root, f.inv_sqrt_bc2, f.eps);
-  p = fmaf(-f.decay, p, p) - __fdividef(f.step_size * m, denom);
+  float root, inv;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(max_nan(v, 0x1p-126f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(root, f.inv_sqrt_bc2, f.eps)));
+  p = fmaf(-f.step_size, m * inv, fmaf(-f.decay, p, p));
 }
 
 // 1 - beta^t, without the cancellation of small t.
@@ -175,16 +184,30 @@ __global__ void __launch_bounds__(kThreads)
 // Scales below this (whose reciprocals would leave fp32) count as zero.
 constexpr float kQ8Least = 0x1p-120f;
 
-// Code of magnitude r in [0, 1] with BITS bits: z leading zeros by the power of 8 that r lies below, then
-// the interval's straight line, rounded to the nearest integer by the addition of 1.5 * 2^23.
-template <int BITS>
-__device__ __forceinline__ uint32_t q8_encode(float r) {
-  const int e = static_cast<int>(__float_as_uint(r) >> 23);
-  const int z = max(min(((126 - e) * 0x5556) >> 16, BITS - 1), 0);  // (126 - e) / 3
-  const float slope = __uint_as_float(__float_as_uint(1.f / 7.f) + (static_cast<uint32_t>(BITS + 2 + 2 * z) << 23));
-  const float low = __uint_as_float(static_cast<uint32_t>(127 + BITS - 1 - z) << 23);
-  const float offset = __fadd_rn(__fmul_rn(low, 6.f / 7.f), -1.f);
-  return __float_as_uint(__fadd_rn(__fadd_rn(__fmul_rn(r, slope), offset), 12582912.f)) & 0xffu;
+// The code of a magnitude r in [0, 1] is the nearest integer to slope * r + offset: with z the code's leading zeros (r
+// lies between 8^-(z+1) and 8^-z) and low its leading one, the line of that interval is
+// ((8^(z+1) r - 1) / 7) low + low - 1.  z follows from r's exponent; slope and offset come from a table by it, in
+// shared memory (12 instructions an element less than computing them; few exponents occur in a block, and equal
+// ones are one access).
+struct Q8Lines {
+  float2 line[2][256];  // of the first moment (7 bits of magnitude), of the second (8)
+};
+
+__device__ __forceinline__ void q8_fill(Q8Lines& t) {
+  for (int i = threadIdx.x; i < 512; i += kThreads) {
+    const int bits = 7 + (i >> 8), e = i & 255;
+    const int z = max(min((126 - e) / 3, bits - 1), 0);
+    const float low = __uint_as_float(static_cast<uint32_t>(127 + bits - 1 - z) << 23);
+    const float slope = __uint_as_float(__float_as_uint(1.f / 7.f) + (static_cast<uint32_t>(bits + 2 + 2 * z) << 23));
+    t.line[i >> 8][e] = make_float2(slope, __fadd_rn(__fmul_rn(low, 6.f / 7.f), -1.f));
+  }
+  __syncthreads();
+}
+
+// The code in the low byte: adding 1.5 * 2^23 rounds to the nearest integer.
+__device__ __forceinline__ uint32_t q8_encode(const float2 (&line)[256], float r) {
+  const float2 l = line[__float_as_uint(r) >> 23];
+  return __float_as_uint(__fadd_rn(__fadd_rn(__fmul_rn(r, l.x), l.y), 12582912.f));
 }
 
 // The values of two codes (the low 8 bits of each half of `pair`), in units of the scale: with c the
@@ -243,24 +266,38 @@ __device__ __forceinline__ void store_codes(void* base, int64_t at, int n, bool 
     if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i % 4)));
 }
 
-// Codes of a warp's block, 8 values to a lane, and its scale.  Magnitudes are compared as integers, which
-// orders them and puts NaN above infinity: a block with either gets it as its scale.
+// Codes of a warp's block, 8 values to a lane, and its scale.  A block with a NaN or an infinity gets it as its
+// scale.  Magnitudes are compared across the warp as integers, which orders them and puts NaN on top.
 template <bool SIGNED>
-__device__ __forceinline__ uint2 q8_block(const float (&f)[kVec], float* scale) {
-  uint32_t top = 0;
+__device__ __forceinline__ uint2 q8_block(const float2 (&line)[256], const float (&f)[kVec], float* scale) {
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
-  float a = __uint_as_float(__reduce_max_sync(kFull, top));
+  for (int i = 0; i < kVec; ++i) top = max_nan(top, fabsf(f[i]));
+  float a = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
   if (a < kQ8Least) a = 0.f;
   const float inv = a > 0.f ? __fdiv_rn(1.f, a) : 0.f;
-  uint32_t w[2] = {0, 0};
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const float r = __fmul_rn(fabsf(f[i]), inv);
-    uint32_t c = q8_encode<SIGNED ? 7 : 8>(r);
-    if (SIGNED) c |= (__float_as_uint(f[i]) >> 24) & 0x80u;
-    else if (r > 0.f) c = max(c, 1u);
-    w[i / 4] |= c << (8 * (i % 4));
+  for (int h = 0; h < 2; ++h) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = q8_encode(line, __fmul_rn(fabsf(f[4 * h + i]), inv));
+    w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    if (SIGNED) {
+      uint32_t s[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = __float_as_uint(f[4 * h + i]);
+      w[h] |= __byte_perm(__byte_perm(s[0], s[1], 0x0073), __byte_perm(s[2], s[3], 0x0073), 0x5410) & 0x80808080u;
+    }
+  }
+  if (!SIGNED) {
+    // a positive second moment gets code 1 at least; bytes of zero are rare
+    auto has_zero = [](uint32_t v) { return (v - 0x01010101u) & ~v & 0x80808080u; };
+    if (has_zero(w[0]) | has_zero(w[1])) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (!(w[i / 4] >> (8 * (i % 4)) & 0xffu) && __fmul_rn(f[i], inv) > 0.f) w[i / 4] |= 1u << (8 * (i % 4));
+    }
   }
   *scale = a;
   return make_uint2(w[0], w[1]);
@@ -269,6 +306,8 @@ __device__ __forceinline__ uint2 q8_block(const float (&f)[kVec], float* scale) 
 template <typename P, typename G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads)
     adamw_q8_kernel(const __grid_constant__ AdamList<CAP> list, const __grid_constant__ AdamScalars s) {
+  __shared__ Q8Lines lines;
+  q8_fill(lines);
   if (blockIdx.x < list.first[list.count]) {
     const int t = tensor_of_chunk(list, blockIdx.x);
     const AdamEntry& e = list.e[t];
@@ -289,15 +328,17 @@ __global__ void __launch_bounds__(kThreads)
       q8_values<true>(mc, e.ms[block / TBE_Q8_BLOCK], m);
       q8_values<false>(vc, e.vs[block / TBE_Q8_BLOCK], v);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        adam_element(f, g[i], p[i], m[i], v[i]);
-        if (i >= n) m[i] = v[i] = 0.f;  // past the tensor's end: no part of the block's scale
+      for (int i = 0; i < kVec; ++i) adam_element(f, g[i], p[i], m[i], v[i]);
+      if (n < kVec) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          if (i >= n) m[i] = v[i] = 0.f;  // past the tensor's end: no part of the block's scale
       }
       if constexpr (MASTER) store8(e.master + at, n, vec, p);
       store8(static_cast<P*>(e.p) + at, n, vec, p);
       float a, b;
-      store_codes(e.m, at, n, vec, q8_block<true>(m, &a));
-      store_codes(e.v, at, n, vec, q8_block<false>(v, &b));
+      store_codes(e.m, at, n, vec, q8_block<true>(lines.line[0], m, &a));
+      store_codes(e.v, at, n, vec, q8_block<false>(lines.line[1], v, &b));
       if (lane == 0) {
         e.ms[block / TBE_Q8_BLOCK] = a;
         e.vs[block / TBE_Q8_BLOCK] = b;

@@ -4,16 +4,10 @@
 // One pass reads x and dy once, writes dx and keeps each column's sums of dy * xhat and dy in registers
 // over the rows that a CTA takes (its slot); the slots' sums meet in a second kernel, in a fixed
 // order.  The bound is DRAM; the partial rows add 16 bytes a column and slot to it.
-#include "dense_common.cuh"
+#include "norm_rows.cuh"
 
 namespace tbe {
 namespace {
-
-constexpr int kRowThreads = 256;
-// Widest segment that a warp keeps in its registers (x, dy, the weight and the two sums of each column).
-template <int V> constexpr int kRowMax = V == 1 ? 128 : V == 4 ? 512 : 512;
-constexpr int kWideElems = 16;                    // elements of a row to a thread of a wide row
-constexpr int kWideMax = 512 * kWideElems;        // wider rows take two kernels
 
 // Where the sums of a slot go: to its row of the partial sums, or, with a single slot, out.
 struct SumsOut {
@@ -21,6 +15,7 @@ struct SumsOut {
   int64_t slots;
   void* dweight;
   void* dbias;
+  __device__ __forceinline__ bool wanted() const { return partial != nullptr || dweight != nullptr || dbias != nullptr; }
   __device__ __forceinline__ void put(const NormArgs& a, int64_t slot, int c, float dw, float db) const {
     if (partial != nullptr) {
       partial[slot * a.cols + c] = dw;
@@ -41,241 +36,178 @@ struct RowIn {
   void* dx;
 };
 
-// L lanes to a row, J vectors of V elements to a lane, U rows at a time.
-template <typename X, typename Y, int V, int L, int J, int U>
-__device__ __forceinline__ void rows_body(const NormArgs& a, int seg, int col0, int width, int64_t row0, int64_t row1,
-                                          const RowIn& in, const SumsOut& out, int64_t slot, float* smem) {
-  constexpr int kGroups = kRowThreads / L;
-  const X* x = static_cast<const X*>(in.x);
-  const Y* dy = static_cast<const Y*>(in.dy);
-  X* dx = static_cast<X*>(in.dx);
-  const int lane = threadIdx.x % L, group = threadIdx.x / L;
-  bool has[J];
+template <int L, int T>
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* part) {
+  if constexpr (L <= 32) {
+    return make_float2(lanes_sum<L>(v.x), lanes_sum<L>(v.y));
+  } else {
+    v = make_float2(lanes_sum<32>(v.x), lanes_sum<32>(v.y));
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    const float2 p = threadIdx.x % 32 < T / 32 ? part[threadIdx.x % 32] : make_float2(0.f, 0.f);
+    return make_float2(lanes_sum<32>(p.x), lanes_sum<32>(p.y));
+  }
+}
+
+template <typename X, typename Y, int V, int L, int T>
+__device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g, const SumsOut& out, int64_t slot, int seg,
+                                              int col0, int width, const RowWalk& walk, char* smem) {
+  constexpr int J = kPer / V;
+  __shared__ float2 part[2][T / 32];
+  const int lane = threadIdx.x % L;
+  bool in[J];
   float w[J][V], dw[J][V], db[J][V];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int c = (j * L + lane) * V;
-    has[j] = c < width;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[j][i] = has[j] && in.weight != nullptr ? load_any(in.weight, a.wtype, col0 + c + i) : 1.f;
-      dw[j][i] = db[j][i] = 0.f;
+  for (int j = 0; j < J; ++j) in[j] = (j * L + lane) * V < width;
+  const RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, smem);
+  const RowReader<Y, V, L, T> dy(g.dy, a.y_stride, col0 + lane * V, smem + kStages * stage_bytes<X, V>(T));
+  for (int k = 0; k < kStages - 1; ++k) {
+    const int64_t r = walk.first + k * walk.step;
+    if (r < walk.end) {
+      x.copy(k, r, in);
+      dy.copy(k, r, in);
     }
+    async_commit();
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    load_weights<V>(g.weight, a.wtype, in[j] ? col0 + (j * L + lane) * V : col0, 1.f, w[j]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[j][i] = db[j][i] = 0.f;
   }
   const float inv_n = 1.f / static_cast<float>(width);
-  for (int64_t base = row0; base < row1; base += kGroups * U) {
-    Pack<X, V> vx[U][J];
-    Pack<Y, V> vy[U][J];
-    float mu[U], rs[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = base + u * kGroups + group;
-      mu[u] = rs[u] = 0.f;
-      if (r < row1) {
-        mu[u] = in.mean[r * a.segments + seg];
-        rs[u] = in.rstd[r * a.segments + seg];
-      }
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        vx[u][j].zero();
-        vy[u][j].zero();
-        if (r < row1 && has[j]) {
-          vx[u][j].load(x + r * a.x_stride + col0 + (j * L + lane) * V);
-          vy[u][j].load(dy + r * a.y_stride + col0 + (j * L + lane) * V);
-        }
-      }
-    }
-    float c1[U], c2[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      c1[u] = c2[u] = 0.f;
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d = vy[u][j].get(i), xh = (vx[u][j].get(i) - mu[u]) * rs[u], h = d * w[j][i];
-          c1[u] += h;
-          c2[u] = fmaf(h, xh, c2[u]);
-          dw[j][i] = fmaf(d, xh, dw[j][i]);
-          db[j][i] += d;
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      c1[u] = lanes_sum<L>(c1[u]) * inv_n;
-      c2[u] = lanes_sum<L>(c2[u]) * inv_n;
-    }
-    if (dx != nullptr) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t r = base + u * kGroups + group;
-        if (r >= row1) continue;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          if (!has[j]) continue;
-          float f[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float xh = (vx[u][j].get(i) - mu[u]) * rs[u];
-            f[i] = rs[u] * (fmaf(vy[u][j].get(i), w[j][i], -c1[u]) - xh * c2[u]);
-          }
-          Pack<X, V> o;
-          o.set(f);
-          o.store(dx + r * a.dx_stride + col0 + (j * L + lane) * V);
-        }
-      }
-    }
+  float mu = 0.f, rs = 0.f;  // of the row to come
+  if (walk.first < walk.end) {
+    mu = g.mean[walk.first * a.segments + seg];
+    rs = g.rstd[walk.first * a.segments + seg];
   }
-  if (out.partial == nullptr && out.dweight == nullptr && out.dbias == nullptr) return;
-  // the groups of a warp, then the warps (kGroups / kSub rows of sums), one after the other
-  constexpr int kSub = 32 / L, kWarps = kRowThreads / 32, kSpan = L * J * V;
-  const int warp = threadIdx.x / 32;
-#pragma unroll
-  for (int j = 0; j < J; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int o = 16; o >= L; o >>= 1) {
-        dw[j][i] += __shfl_xor_sync(kFull, dw[j][i], o);
-        db[j][i] += __shfl_xor_sync(kFull, db[j][i], o);
-      }
-  (void)kSub;
-  float* sw = smem;
-  float* sb = smem + kWarps * kSpan;
-  if ((threadIdx.x & 31) < L) {
+  int stage = 0;
+  for (int64_t k = 0; k < walk.count; ++k) {
+    const int64_t r = walk.first + k * walk.step, ahead = r + (kStages - 1) * walk.step;
+    if (ahead < walk.end) {
+      x.copy(stage == 0 ? kStages - 1 : stage - 1, ahead, in);
+      dy.copy(stage == 0 ? kStages - 1 : stage - 1, ahead, in);
+    }
+    async_commit();
+    async_wait<kStages - 1>();
+    const bool valid = r < walk.end;
+    float xh[J][V], h[J][V];
+    x.read(stage, r, valid, in, xh);
+    dy.read(stage, r, valid, in, h);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
+    float2 c = make_float2(0.f, 0.f);
+    const float m = valid ? mu : 0.f, q = valid ? rs : 0.f;
+    if (r + walk.step < walk.end) {
+      mu = g.mean[(r + walk.step) * a.segments + seg];
+      rs = g.rstd[(r + walk.step) * a.segments + seg];
+    }
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = (j * L + lane) * V + i;
-        sw[warp * kSpan + c] = dw[j][i];
-        sb[warp * kSpan + c] = db[j][i];
+        const float d = h[j][i];
+        xh[j][i] = in[j] ? (xh[j][i] - m) * q : 0.f;
+        dw[j][i] = fmaf(d, xh[j][i], dw[j][i]);
+        db[j][i] += d;
+        h[j][i] = d * w[j][i];
+        c.x += h[j][i];
+        c.y = fmaf(h[j][i], xh[j][i], c.y);
       }
-  }
-  __syncthreads();
-  for (int c = threadIdx.x; c < width; c += kRowThreads) {
-    float tw = 0.f, tb = 0.f;
+    if (g.dx == nullptr) continue;
+    c = row_sum2<L, T>(c, part[k & 1]);  // the next row's sums go to the other buffer: one barrier a row
+    if (!valid) continue;
+    const float c1 = c.x * inv_n * q, c2 = c.y * inv_n * q;
+    X* dx = static_cast<X*>(g.dx) + r * a.dx_stride + col0 + lane * V;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      tw += sw[k * kSpan + c];
-      tb += sb[k * kSpan + c];
+    for (int j = 0; j < J; ++j) {
+      if (!in[j]) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[j][i] = fmaf(-xh[j][i], c2, fmaf(h[j][i], q, -c1));
+      Pack<X, V> o;
+      o.set(h[j]);
+      o.store(dx + j * L * V);
     }
-    out.put(a, slot, col0 + c, tw, tb);
   }
+  if (!out.wanted()) return;
+  if constexpr (L > 32) {  // each thread owns its columns
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (in[j]) out.put(a, slot, col0 + (j * L + lane) * V + i, dw[j][i], db[j][i]);
+  } else {  // the T / L groups of the CTA hold the same columns: [groups][kPer * L] sums in shared memory, added in order
+    async_wait<0>();
+    __syncthreads();  // every thread is done with the stages
+    float* sums = reinterpret_cast<float*>(smem);
+    constexpr int kSpan = kPer * L;
+    auto combine = [&](const float (&v)[J][V], int pass) {
+      float* mine = sums + pass * T * kPer + (threadIdx.x / L) * kSpan;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        Pack<float, V> o;
+        o.set(v[j]);
+        o.store(mine + (j * L + lane) * V);
+      }
+    };
+    combine(dw, 0);
+    combine(db, 1);
+    __syncthreads();
+    for (int c = threadIdx.x; c < width; c += T) {
+      float tw = 0.f, tb = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < T / L; ++k) {
+        tw += sums[k * kSpan + c];
+        tb += sums[T * kPer + k * kSpan + c];
+      }
+      out.put(a, slot, col0 + c, tw, tb);
+    }
+  }
+}
+
+// Shared memory of a CTA: the stages, and then, where groups share columns, their sums.
+template <typename X, typename Y, int V>
+constexpr int backward_smem(int T, bool groups) {
+  const int stages = kStages * (stage_bytes<X, V>(T) + stage_bytes<Y, V>(T));
+  const int sums = groups ? 2 * T * kPer * static_cast<int>(sizeof(float)) : 0;
+  return stages > sums ? stages : sums;
 }
 
 // A CTA takes one segment of a slot's rows, with lanes to a row by the segment's own width.
 template <typename X, typename Y, int V>
-__global__ void __launch_bounds__(kRowThreads)
-    norm_backward_rows_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RowIn in,
+__global__ void __launch_bounds__(kGroupThreads, 4)
+    norm_backward_rows_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RowIn g,
                               const __grid_constant__ SumsOut out) {
-  constexpr int kMaxJ = kRowMax<V> / (32 * V);
-  __shared__ float smem[2 * (kRowThreads / 32) * 32 * kMaxJ * V];
+  extern __shared__ __align__(16) char smem[];
+  constexpr int T = kGroupThreads;
   const int seg = blockIdx.x % a.segments;
   const int64_t slot = blockIdx.x / a.segments;
   const int64_t per = (a.rows + out.slots - 1) / out.slots;
   const int64_t row0 = min(slot * per, a.rows), row1 = min(row0 + per, a.rows);
   int col0, width;
   segment_span<V>(a, seg, &col0, &width);
-#define TBE_BODY(L, J, U) rows_body<X, Y, V, L, J, U>(a, seg, col0, width, row0, row1, in, out, slot, smem)
-  if (V > 1 && width <= 8 * V) TBE_BODY(8, 1, 4);
-  else if (V > 1 && width <= 16 * V) TBE_BODY(16, 1, 4);
-  else if (width <= 32 * V) TBE_BODY(32, 1, 4);
-  else if (kMaxJ == 2 || width <= 64 * V) TBE_BODY(32, 2, 2);
-  else if constexpr (kMaxJ > 2) TBE_BODY(32, 4, 1);
-#undef TBE_BODY
+  auto go = [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value;
+    const RowWalk walk{row0 + threadIdx.x / L, T / L, row1, (row1 - row0 + T / L - 1) / (T / L)};
+    backward_rows<X, Y, V, L, T>(a, g, out, slot, seg, col0, width, walk, smem);
+  };
+  if (V > 1 && width <= row_capacity(4)) go(std::integral_constant<int, 4>());
+  else if (V > 1 && width <= row_capacity(8)) go(std::integral_constant<int, 8>());
+  else if (V > 1 && width <= row_capacity(16)) go(std::integral_constant<int, 16>());
+  else go(std::integral_constant<int, 32>());
 }
 
-// One CTA to a row (segment) of up to T * J * V columns, over the rows of its slot; each thread owns
-// its columns' sums.
+// A CTA of T threads to a row, over every slots-th row.
 template <typename X, typename Y, int V, int T>
-__global__ void __launch_bounds__(T)
-    norm_backward_wide_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RowIn in,
+__global__ void __launch_bounds__(T, 512 / T)
+    norm_backward_wide_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RowIn g,
                               const __grid_constant__ SumsOut out) {
-  constexpr int J = kWideElems / V;
-  __shared__ float2 part[2][T / 32];
-  const X* x = static_cast<const X*>(in.x);
-  const Y* dy = static_cast<const Y*>(in.dy);
-  X* dx = static_cast<X*>(in.dx);
+  extern __shared__ __align__(16) char smem[];
   const int seg = blockIdx.x % a.segments;
   const int64_t slot = blockIdx.x / a.segments;
   int col0, width;
   segment_span<V>(a, seg, &col0, &width);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  bool has[J];
-  float w[J][V], dw[J][V], db[J][V];
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int c = (j * T + threadIdx.x) * V;
-    has[j] = c < width;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[j][i] = has[j] && in.weight != nullptr ? load_any(in.weight, a.wtype, col0 + c + i) : 1.f;
-      dw[j][i] = db[j][i] = 0.f;
-    }
-  }
-  const float inv_n = 1.f / static_cast<float>(width);
-  Pack<X, V> vx[J];
-  Pack<Y, V> vy[J];
-  float mu = 0.f, rs = 0.f;
-  auto fetch = [&](int64_t r) {
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      vx[j].zero();
-      vy[j].zero();
-      if (r < a.rows && has[j]) {
-        vx[j].load(x + r * a.x_stride + col0 + (j * T + threadIdx.x) * V);
-        vy[j].load(dy + r * a.y_stride + col0 + (j * T + threadIdx.x) * V);
-      }
-    }
-    if (r < a.rows) {
-      mu = in.mean[r * a.segments + seg];
-      rs = in.rstd[r * a.segments + seg];
-    }
-  };
-  int buf = 0;
-  for (int64_t r = slot; r < a.rows; r += out.slots, buf ^= 1) {
-    fetch(r);
-    float c1 = 0.f, c2 = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float d = vy[j].get(i), xh = (vx[j].get(i) - mu) * rs, h = d * w[j][i];
-        c1 += h;
-        c2 = fmaf(h, xh, c2);
-        if (has[j]) dw[j][i] = fmaf(d, xh, dw[j][i]);
-        db[j][i] += d;
-      }
-    c1 = lanes_sum<32>(c1);
-    c2 = lanes_sum<32>(c2);
-    if (lane == 0) part[buf][warp] = make_float2(c1, c2);
-    __syncthreads();  // the next row writes the other buffer
-    const float2 p = lane < T / 32 ? part[buf][lane] : make_float2(0.f, 0.f);
-    c1 = lanes_sum<32>(p.x) * inv_n;
-    c2 = lanes_sum<32>(p.y) * inv_n;
-    if (dx != nullptr) {
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        if (!has[j]) continue;
-        float f[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xh = (vx[j].get(i) - mu) * rs;
-          f[i] = rs * (fmaf(vy[j].get(i), w[j][i], -c1) - xh * c2);
-        }
-        Pack<X, V> o;
-        o.set(f);
-        o.store(dx + r * a.dx_stride + col0 + (j * T + threadIdx.x) * V);
-      }
-    }
-  }
-  if (out.partial == nullptr && out.dweight == nullptr && out.dbias == nullptr) return;
-#pragma unroll
-  for (int j = 0; j < J; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (has[j]) out.put(a, slot, col0 + (j * T + threadIdx.x) * V + i, dw[j][i], db[j][i]);
+  const RowWalk walk{slot, out.slots, a.rows, (a.rows - slot + out.slots - 1) / out.slots};
+  backward_rows<X, Y, V, T, T>(a, g, out, slot, seg, col0, width, walk, smem);
 }
 
 // Rows wider than a CTA's registers.  First the columns' sums: a thread to a column, down the rows of
@@ -334,9 +266,11 @@ __global__ void __launch_bounds__(1024)
       Pack<Y, V> vy;
       vx.load(xr + c);
       vy.load(yr + c);
+      float w[V];
+      load_weights<V>(in.weight, a.wtype, col0 + c, 1.f, w);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float h = vy.get(i) * (in.weight != nullptr ? load_any(in.weight, a.wtype, col0 + c + i) : 1.f);
+        const float h = vy.get(i) * w[i];
         c1 += h;
         c2 = fmaf(h, (vx.get(i) - mu) * rs, c2);
       }
@@ -353,12 +287,10 @@ __global__ void __launch_bounds__(1024)
       Pack<Y, V> vy;
       vx.load(xr + c);
       vy.load(yr + c);
-      float f[V];
+      float w[V], f[V];
+      load_weights<V>(in.weight, a.wtype, col0 + c, 1.f, w);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float w = in.weight != nullptr ? load_any(in.weight, a.wtype, col0 + c + i) : 1.f;
-        f[i] = rs * (fmaf(vy.get(i), w, -c1) - (vx.get(i) - mu) * rs * c2);
-      }
+      for (int i = 0; i < V; ++i) f[i] = rs * (fmaf(vy.get(i), w[i], -c1) - (vx.get(i) - mu) * rs * c2);
       Pack<X, V> o;
       o.set(f);
       o.store(dr + c);
@@ -392,19 +324,27 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+constexpr int kWideMax = row_capacity(512);  // wider rows take two kernels
+
 template <typename X, typename Y, int V>
 tbe_status launch(const NormArgs& a, const RowIn& in, SumsOut out, const DeviceInfo& dev, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(out.slots * a.segments);
-  if (a.width <= kRowMax<V>) {
-    norm_backward_rows_kernel<X, Y, V><<<grid, kRowThreads, 0, s>>>(a, in, out);
-  } else if (a.width <= 64 * kWideElems) {
-    norm_backward_wide_kernel<X, Y, V, 64><<<grid, 64, 0, s>>>(a, in, out);
-  } else if (a.width <= 128 * kWideElems) {
-    norm_backward_wide_kernel<X, Y, V, 128><<<grid, 128, 0, s>>>(a, in, out);
-  } else if (a.width <= 256 * kWideElems) {
-    norm_backward_wide_kernel<X, Y, V, 256><<<grid, 256, 0, s>>>(a, in, out);
+  cudaError_t bad = cudaSuccess;
+  auto go = [&](auto kernel, int threads, bool groups) {
+    const int smem = backward_smem<X, Y, V>(threads, groups);
+    if (smem > kPlainSmem) bad = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (bad == cudaSuccess) kernel<<<grid, threads, smem, s>>>(a, in, out);
+  };
+  if (a.width <= row_capacity(32)) {
+    go(norm_backward_rows_kernel<X, Y, V>, kGroupThreads, true);
+  } else if (a.width <= row_capacity(64)) {
+    go(norm_backward_wide_kernel<X, Y, V, 64>, 64, false);
+  } else if (a.width <= row_capacity(128)) {
+    go(norm_backward_wide_kernel<X, Y, V, 128>, 128, false);
+  } else if (a.width <= row_capacity(256)) {
+    go(norm_backward_wide_kernel<X, Y, V, 256>, 256, false);
   } else if (a.width <= kWideMax) {
-    norm_backward_wide_kernel<X, Y, V, 512><<<grid, 512, 0, s>>>(a, in, out);
+    go(norm_backward_wide_kernel<X, Y, V, 512>, 512, false);
   } else {
     if (out.dweight != nullptr || out.dbias != nullptr) {
       const int64_t tiles = (a.width + 255) / 256;
@@ -421,6 +361,7 @@ tbe_status launch(const NormArgs& a, const RowIn& in, SumsOut out, const DeviceI
     }
     return cuda_status(cudaGetLastError());
   }
+  if (bad != cudaSuccess) return cuda_status(bad);
   note_launch();
   return cuda_status(cudaGetLastError());
 }
@@ -428,15 +369,17 @@ tbe_status launch(const NormArgs& a, const RowIn& in, SumsOut out, const DeviceI
 }  // namespace
 
 int norm_backward_slots(const NormArgs& a, const DeviceInfo& dev) {
-  // rows by warps: about 16 CTAs to an SM, no fewer than 32 rows to a slot; rows by CTAs: two to four to an SM;
-  // wider still: enough that 256-column tiles fill the SMs four times
+  // By parts of warps: two waves of four CTAs to an SM, no fewer than 32 rows to a slot.  By CTAs: one wave of 512
+  // threads to an SM.  Wider still: enough that 256-column tiles fill the SMs four times.
   int64_t want, least;
-  if (a.width <= 512) {
-    want = static_cast<int64_t>(dev.sms) * 16 / a.segments;
+  if (a.width <= row_capacity(32)) {
+    want = static_cast<int64_t>(dev.sms) * 8 / a.segments;
     least = 32;
   } else if (a.width <= kWideMax) {
-    want = static_cast<int64_t>(dev.sms) * (a.width <= 2048 ? 4 : 2) / a.segments;
-    least = 4;
+    int threads = 64;
+    while (row_capacity(threads) < a.width) threads *= 2;
+    want = static_cast<int64_t>(dev.sms) * (512 / threads) / a.segments;
+    least = 1;
   } else {
     want = static_cast<int64_t>(dev.sms) * 4 / (static_cast<int64_t>(a.segments) * ((a.width + 255) / 256));
     least = 16;

@@ -1,275 +1,203 @@
 // k_norm_forward.cu -- layer norm over the segments of a row (tbe_layer_norm_forward).
 //
 // Every element is read once and written once; the bound is DRAM.  The mean and the sum of squared
-// deviations are taken in that order over the row held in registers, so no cancellation of
+// deviations are taken one after the other over the row held in registers: no cancellation of
 // E[x^2] - mean^2 and no second read.
-#include "dense_common.cuh"
+#include "norm_rows.cuh"
 
 namespace tbe {
 namespace {
 
-constexpr int kRowThreads = 256;
-// Widest segment that a warp keeps in its registers.
-template <int V> constexpr int kRowMax = V == 1 ? 256 : 128 * V;
+struct ForwardArgs {
+  const void* x;
+  const void* weight;
+  const void* bias;
+  void* y;
+  float* mean;
+  float* rstd;
+};
 
-// L lanes to a row, J vectors of V elements to a lane, U rows at a time: U * J loads in flight.
-template <typename X, typename Y, int V, int L, int J, int U>
-__device__ __forceinline__ void rows_body(const NormArgs& a, int seg, int col0, int width, int64_t row0, int64_t row1,
-                                          const X* x, const void* weight, const void* bias, Y* y, float* mean,
-                                          float* rstd) {
-  constexpr int kGroups = kRowThreads / L;
-  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+template <typename X, typename Y, int V, int L, int T>
+__device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArgs& g, int seg, int col0, int width,
+                                             const RowWalk& walk, char* smem) {
+  constexpr int J = kPer / V;
+  __shared__ float part[2][T / 32];
+  const int lane = threadIdx.x % L;
   bool in[J];
   float w[J][V], b[J][V];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int c = (j * L + lane) * V;
-    in[j] = c < width;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[j][i] = in[j] && weight != nullptr ? load_any(weight, a.wtype, col0 + c + i) : 1.f;
-      b[j][i] = in[j] && bias != nullptr ? load_any(bias, a.wtype, col0 + c + i) : 0.f;
-    }
+  for (int j = 0; j < J; ++j) in[j] = (j * L + lane) * V < width;
+  const RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, smem);
+  for (int k = 0; k < kStages - 1; ++k) {
+    const int64_t r = walk.first + k * walk.step;
+    if (r < walk.end) x.copy(k, r, in);
+    async_commit();
   }
-  const float inv_n = 1.f / static_cast<float>(width);
-  for (int64_t base = row0; base < row1; base += kGroups * U) {
-    Pack<X, V> v[U][J];
-    float mu[U], rs[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = base + u * kGroups + group;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        v[u][j].zero();
-        if (r < row1 && in[j]) v[u][j].load(x + r * a.x_stride + col0 + (j * L + lane) * V);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float s = 0.f;
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) s += v[u][j].get(i);
-      mu[u] = lanes_sum<L>(s) * inv_n;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float s = 0.f;
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d = v[u][j].get(i) - mu[u];
-          if (in[j]) s = fmaf(d, d, s);
-        }
-      rs[u] = __frsqrt_rn(fmaf(lanes_sum<L>(s), inv_n, a.eps));
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = base + u * kGroups + group;
-      if (r >= row1) continue;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        if (!in[j]) continue;
-        float f[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = fmaf((v[u][j].get(i) - mu[u]) * rs[u], w[j][i], b[j][i]);
-        Pack<Y, V> o;
-        o.set(f);
-        o.store(y + r * a.y_stride + col0 + (j * L + lane) * V);
-      }
-      if (mean != nullptr && lane == 0) {
-        mean[r * a.segments + seg] = mu[u];
-        rstd[r * a.segments + seg] = rs[u];
-      }
-    }
-  }
-}
-
-// A CTA takes one segment of rows_tile rows; neighbouring CTAs take neighbouring segments of the
-// same rows, so what is in flight at one time is a band of whole rows.  The lanes to a row follow
-// the segment's own width: the tables of one launch may be of different widths.
-template <typename X, typename Y, int V>
-__global__ void __launch_bounds__(kRowThreads)
-    norm_rows_kernel(const __grid_constant__ NormArgs a, int64_t rows_tile, const X* x, const void* weight,
-                     const void* bias, Y* y, float* mean, float* rstd) {
-  const int seg = blockIdx.x % a.segments;
-  const int64_t row0 = (blockIdx.x / a.segments) * rows_tile;
-  const int64_t row1 = min(row0 + rows_tile, a.rows);
-  int col0, width;
-  segment_span<V>(a, seg, &col0, &width);
-#define TBE_BODY(L, J, U) \
-  rows_body<X, Y, V, L, J, U>(a, seg, col0, width, row0, row1, x, weight, bias, y, mean, rstd)
-  if (V > 1 && width <= 8 * V) TBE_BODY(8, 1, 4);
-  else if (V > 1 && width <= 16 * V) TBE_BODY(16, 1, 4);
-  else if (width <= 32 * V) TBE_BODY(32, 1, 4);
-  else if (width <= 64 * V) TBE_BODY(32, 2, 2);
-  else if (V > 1 || width <= 128 * V) TBE_BODY(32, 4, 1);
-  else TBE_BODY(32, 8, 1);
-#undef TBE_BODY
-}
-
-// One CTA to a row (segment) of up to blockDim.x * J * V elements.
-template <typename X, typename Y, int V, int J, int T>
-__global__ void __launch_bounds__(T)
-    norm_wide_kernel(const __grid_constant__ NormArgs a, int64_t row_slots, const X* x, const void* weight,
-                     const void* bias, Y* y, float* mean, float* rstd) {
-  __shared__ float part[2][32];
-  const int seg = blockIdx.x % a.segments;
-  int col0, width;
-  segment_span<V>(a, seg, &col0, &width);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto block_sum = [&](float s, float* buf) {
-    s = lanes_sum<32>(s);
-    if (lane == 0) buf[warp] = s;
-    __syncthreads();
-    return lanes_sum<32>(lane < T / 32 ? buf[lane] : 0.f);
-  };
-  bool in[J];
-  float w[J][V], b[J][V];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int c = (j * T + threadIdx.x) * V;
-    in[j] = c < width;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[j][i] = in[j] && weight != nullptr ? load_any(weight, a.wtype, col0 + c + i) : 1.f;
-      b[j][i] = in[j] && bias != nullptr ? load_any(bias, a.wtype, col0 + c + i) : 0.f;
-    }
+    const int c = in[j] ? col0 + (j * L + lane) * V : col0;
+    load_weights<V>(g.weight, a.wtype, c, 1.f, w[j]);
+    load_weights<V>(g.bias, a.wtype, c, 0.f, b[j]);
   }
   const float inv_n = 1.f / static_cast<float>(width);
-  for (int64_t r = blockIdx.x / a.segments; r < a.rows; r += row_slots) {
-    Pack<X, V> v[J];
+  int stage = 0;
+  for (int64_t k = 0; k < walk.count; ++k) {
+    const int64_t r = walk.first + k * walk.step, ahead = r + (kStages - 1) * walk.step;
+    if (ahead < walk.end) x.copy(stage == 0 ? kStages - 1 : stage - 1, ahead, in);
+    async_commit();
+    async_wait<kStages - 1>();
+    const bool valid = r < walk.end;
+    float f[J][V];
+    x.read(stage, r, valid, in, f);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
     float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      v[j].zero();
-      if (in[j]) v[j].load(x + r * a.x_stride + col0 + (j * T + threadIdx.x) * V);
-    }
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) s += v[j].get(i);
-    const float mu = block_sum(s, part[0]) * inv_n;
+      for (int i = 0; i < V; ++i) s += f[j][i];
+    const float mu = row_sum<L, T>(s, part[0]) * inv_n;
     s = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float d = v[j].get(i) - mu;
-        if (in[j]) s = fmaf(d, d, s);
+        f[j][i] = in[j] ? f[j][i] - mu : 0.f;
+        s = fmaf(f[j][i], f[j][i], s);
       }
-    // the barrier inside also keeps the next row's first sums behind this row's reads of part[0]
-    const float rs = __frsqrt_rn(fmaf(block_sum(s, part[1]), inv_n, a.eps));
+    const float rs = __frsqrt_rn(fmaf(row_sum<L, T>(s, part[1]), inv_n, a.eps));
+    if (!valid) continue;
+    Y* y = static_cast<Y*>(g.y) + r * a.y_stride + col0 + lane * V;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       if (!in[j]) continue;
-      float f[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = fmaf((v[j].get(i) - mu) * rs, w[j][i], b[j][i]);
+      for (int i = 0; i < V; ++i) f[j][i] = fmaf(f[j][i] * rs, w[j][i], b[j][i]);
       Pack<Y, V> o;
-      o.set(f);
-      o.store(y + r * a.y_stride + col0 + (j * T + threadIdx.x) * V);
+      o.set(f[j]);
+      o.store(y + j * L * V);
     }
-    if (mean != nullptr && threadIdx.x == 0) {
-      mean[r * a.segments + seg] = mu;
-      rstd[r * a.segments + seg] = rs;
+    if (g.mean != nullptr && lane == 0) {
+      g.mean[r * a.segments + seg] = mu;
+      g.rstd[r * a.segments + seg] = rs;
     }
   }
 }
 
-// Rows wider than the registers of a CTA: three passes over the row, the second and third from the
-// caches.
+// A CTA takes one segment of `tile` rows; neighbouring CTAs take neighbouring segments of the same rows, so what is
+// in flight at one time is a band of whole rows.  The lanes to a row follow the segment's own width: the tables of one
+// launch may be of different widths.
+template <typename X, typename Y, int V>
+__global__ void __launch_bounds__(kGroupThreads, 6)
+    norm_rows_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ ForwardArgs g, int64_t tile) {
+  extern __shared__ __align__(16) char smem[];
+  constexpr int T = kGroupThreads;
+  const int seg = blockIdx.x % a.segments;
+  const int64_t row0 = (blockIdx.x / a.segments) * tile, row1 = min(row0 + tile, a.rows);
+  int col0, width;
+  segment_span<V>(a, seg, &col0, &width);
+  auto go = [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value;
+    const RowWalk walk{row0 + threadIdx.x / L, T / L, row1, (row1 - row0 + T / L - 1) / (T / L)};
+    forward_rows<X, Y, V, L, T>(a, g, seg, col0, width, walk, smem);
+  };
+  if (V > 1 && width <= row_capacity(4)) go(std::integral_constant<int, 4>());
+  else if (V > 1 && width <= row_capacity(8)) go(std::integral_constant<int, 8>());
+  else if (V > 1 && width <= row_capacity(16)) go(std::integral_constant<int, 16>());
+  else go(std::integral_constant<int, 32>());
+}
+
+// A CTA of T threads to a row, over every slots-th row.
+template <typename X, typename Y, int V, int T>
+__global__ void __launch_bounds__(T, T <= 256 ? 768 / T : 1)
+    norm_wide_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ ForwardArgs g, int64_t slots) {
+  extern __shared__ __align__(16) char smem[];
+  const int seg = blockIdx.x % a.segments;
+  const int64_t slot = blockIdx.x / a.segments;
+  int col0, width;
+  segment_span<V>(a, seg, &col0, &width);
+  const RowWalk walk{slot, slots, a.rows, (a.rows - slot + slots - 1) / slots};
+  forward_rows<X, Y, V, T, T>(a, g, seg, col0, width, walk, smem);
+}
+
+// Rows wider than the registers of a CTA: three passes over the row, the second and third from the caches.
 template <typename X, typename Y, int V>
 __global__ void __launch_bounds__(1024)
-    norm_long_kernel(const __grid_constant__ NormArgs a, int64_t row_slots, const X* x, const void* weight,
-                     const void* bias, Y* y, float* mean, float* rstd) {
+    norm_long_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ ForwardArgs g, int64_t slots) {
   __shared__ float part[2][32];
   const int seg = blockIdx.x % a.segments;
   int col0, width;
   segment_span<V>(a, seg, &col0, &width);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto block_sum = [&](float s, float* buf) {
-    s = lanes_sum<32>(s);
-    if (lane == 0) buf[warp] = s;
-    __syncthreads();
-    return lanes_sum<32>(buf[lane]);
-  };
   const float inv_n = 1.f / static_cast<float>(width);
-  for (int64_t r = blockIdx.x / a.segments; r < a.rows; r += row_slots) {
-    const X* xr = x + r * a.x_stride + col0;
+  for (int64_t r = blockIdx.x / a.segments; r < a.rows; r += slots) {
+    const X* x = static_cast<const X*>(g.x) + r * a.x_stride + col0;
+    Y* y = static_cast<Y*>(g.y) + r * a.y_stride + col0;
     float s = 0.f;
 #pragma unroll 4
     for (int c = threadIdx.x * V; c < width; c += 1024 * V) {
       Pack<X, V> v;
-      v.load(xr + c);
+      v.load(x + c);
 #pragma unroll
       for (int i = 0; i < V; ++i) s += v.get(i);
     }
-    const float mu = block_sum(s, part[0]) * inv_n;
+    const float mu = row_sum<1024, 1024>(s, part[0]) * inv_n;
     s = 0.f;
 #pragma unroll 4
     for (int c = threadIdx.x * V; c < width; c += 1024 * V) {
       Pack<X, V> v;
-      v.load(xr + c);
+      v.load(x + c);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float d = v.get(i) - mu;
         s = fmaf(d, d, s);
       }
     }
-    const float rs = __frsqrt_rn(fmaf(block_sum(s, part[1]), inv_n, a.eps));
+    const float rs = __frsqrt_rn(fmaf(row_sum<1024, 1024>(s, part[1]), inv_n, a.eps));
     for (int c = threadIdx.x * V; c < width; c += 1024 * V) {
       Pack<X, V> v;
-      v.load(xr + c);
-      float f[V];
+      v.load(x + c);
+      float w[V], b[V], f[V];
+      load_weights<V>(g.weight, a.wtype, col0 + c, 1.f, w);
+      load_weights<V>(g.bias, a.wtype, col0 + c, 0.f, b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float w = weight != nullptr ? load_any(weight, a.wtype, col0 + c + i) : 1.f;
-        const float b = bias != nullptr ? load_any(bias, a.wtype, col0 + c + i) : 0.f;
-        f[i] = fmaf((v.get(i) - mu) * rs, w, b);
-      }
+      for (int i = 0; i < V; ++i) f[i] = fmaf((v.get(i) - mu) * rs, w[i], b[i]);
       Pack<Y, V> o;
       o.set(f);
-      o.store(y + r * a.y_stride + col0 + c);
+      o.store(y + c);
     }
-    if (mean != nullptr && threadIdx.x == 0) {
-      mean[r * a.segments + seg] = mu;
-      rstd[r * a.segments + seg] = rs;
+    if (g.mean != nullptr && threadIdx.x == 0) {
+      g.mean[r * a.segments + seg] = mu;
+      g.rstd[r * a.segments + seg] = rs;
     }
   }
 }
 
 template <typename X, typename Y, int V>
-tbe_status launch(const NormArgs& a, const void* x, const void* weight, const void* bias, void* y, float* mean,
-                  float* rstd, const DeviceInfo& dev, cudaStream_t s) {
-  const X* xp = static_cast<const X*>(x);
-  Y* yp = static_cast<Y*>(y);
-  if (a.width <= kRowMax<V>) {
-    // about 16 CTAs to an SM, and no fewer rows to a CTA than its warps
-    const int64_t want = a.rows * a.segments / (static_cast<int64_t>(dev.sms) * 16);
-    int64_t tile = want < 8 ? 8 : want > 256 ? 256 : want / 8 * 8;
-    int64_t tiles = (a.rows + tile - 1) / tile;
-    while (tiles * a.segments > INT32_MAX) {
-      tile *= 2;
-      tiles = (a.rows + tile - 1) / tile;
-    }
-    const unsigned grid = static_cast<unsigned>(tiles * a.segments);
-    norm_rows_kernel<X, Y, V><<<grid, kRowThreads, 0, s>>>(a, tile, xp, weight, bias, yp, mean, rstd);
+tbe_status launch(const NormArgs& a, const ForwardArgs& g, const DeviceInfo& dev, cudaStream_t s) {
+  if (a.width <= row_capacity(32)) {
+    constexpr int T = kGroupThreads;
+    constexpr int smem = kStages * stage_bytes<X, V>(T);
+    // about 24 CTAs to an SM (4 waves), and no fewer rows to a CTA than one pass of its threads over the widest rows
+    const int64_t want = a.rows * a.segments / (static_cast<int64_t>(dev.sms) * 24);
+    int64_t tile = want < 16 ? 16 : want > 512 ? 512 : want / 16 * 16;
+    while ((a.rows + tile - 1) / tile * a.segments > INT32_MAX) tile *= 2;
+    const unsigned grid = static_cast<unsigned>((a.rows + tile - 1) / tile * a.segments);
+    norm_rows_kernel<X, Y, V><<<grid, T, smem, s>>>(a, g, tile);
   } else {
-    constexpr int J = 16 / V;
-    auto wide = [&](auto kernel, int threads) {
-      const int per_seg = persistent_grid(kernel, threads, 0, dev, INT32_MAX) / a.segments;
+    cudaError_t bad = cudaSuccess;
+    auto wide = [&](auto kernel, int threads, int smem) {
+      if (smem > kPlainSmem) bad = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (bad != cudaSuccess) return;
+      const int per_seg = persistent_grid(kernel, threads, smem, dev, INT32_MAX) / a.segments;
       const int64_t slots = per_seg < 1 ? 1 : per_seg < a.rows ? per_seg : a.rows;
-      kernel<<<static_cast<unsigned>(slots * a.segments), threads, 0, s>>>(a, slots, xp, weight, bias, yp, mean, rstd);
+      kernel<<<static_cast<unsigned>(slots * a.segments), threads, smem, s>>>(a, g, slots);
     };
-    if (a.width <= 64 * 16) wide(norm_wide_kernel<X, Y, V, J, 64>, 64);
-    else if (a.width <= 128 * 16) wide(norm_wide_kernel<X, Y, V, J, 128>, 128);
-    else if (a.width <= 256 * 16) wide(norm_wide_kernel<X, Y, V, J, 256>, 256);
-    else if (a.width <= 512 * 16) wide(norm_wide_kernel<X, Y, V, J, 512>, 512);
-    else if (a.width <= 1024 * 16) wide(norm_wide_kernel<X, Y, V, J, 1024>, 1024);
-    else wide(norm_long_kernel<X, Y, V>, 1024);
+    if (a.width <= row_capacity(64)) wide(norm_wide_kernel<X, Y, V, 64>, 64, kStages * stage_bytes<X, V>(64));
+    else if (a.width <= row_capacity(128)) wide(norm_wide_kernel<X, Y, V, 128>, 128, kStages * stage_bytes<X, V>(128));
+    else if (a.width <= row_capacity(256)) wide(norm_wide_kernel<X, Y, V, 256>, 256, kStages * stage_bytes<X, V>(256));
+    else if (a.width <= row_capacity(512)) wide(norm_wide_kernel<X, Y, V, 512>, 512, kStages * stage_bytes<X, V>(512));
+    else if (a.width <= row_capacity(1024)) wide(norm_wide_kernel<X, Y, V, 1024>, 1024, kStages * stage_bytes<X, V>(1024));
+    else wide(norm_long_kernel<X, Y, V>, 1024, 0);
+    if (bad != cudaSuccess) return cuda_status(bad);
   }
   note_launch();
   return cuda_status(cudaGetLastError());
@@ -280,6 +208,7 @@ tbe_status launch(const NormArgs& a, const void* x, const void* weight, const vo
 tbe_status launch_norm_forward(const NormArgs& a, int xtype, int ytype, int vec, const void* x, const void* weight,
                                const void* bias, void* y, float* mean, float* rstd, const DeviceInfo& dev,
                                cudaStream_t s) {
+  const ForwardArgs g{x, weight, bias, y, mean, rstd};
   return with_type(xtype, [&](auto xt) {
     return with_type(ytype, [&](auto yt) {
       using X = typename decltype(xt)::type;
@@ -288,9 +217,9 @@ tbe_status launch_norm_forward(const NormArgs& a, int xtype, int ytype, int vec,
         return TBE_ERR_UNSUPPORTED;
       } else {
         if constexpr (sizeof(X) == 2 && sizeof(Y) == 2)
-          if (vec >= 8) return launch<X, Y, 8>(a, x, weight, bias, y, mean, rstd, dev, s);
-        if (vec >= 4) return launch<X, Y, 4>(a, x, weight, bias, y, mean, rstd, dev, s);
-        return launch<X, Y, 1>(a, x, weight, bias, y, mean, rstd, dev, s);
+          if (vec >= 8) return launch<X, Y, 8>(a, g, dev, s);
+        if (vec >= 4) return launch<X, Y, 4>(a, g, dev, s);
+        return launch<X, Y, 1>(a, g, dev, s);
       }
     });
   });
