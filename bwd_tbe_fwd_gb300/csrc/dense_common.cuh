@@ -41,6 +41,25 @@ struct Pack {
     }
   }
 
+  // The first n elements one by one, zeros after them.
+  __device__ __forceinline__ void load_some(const T* p, int n) {
+    zero();
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 4) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (16 * (i % 2));
+      }
+  }
+  __device__ __forceinline__ void store_some(T* p, int n) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
+      }
+  }
+
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (kBytes == 2) {
       *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);

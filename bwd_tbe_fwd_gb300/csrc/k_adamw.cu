@@ -98,38 +98,23 @@ __device__ __forceinline__ void advance_step(const AdamScalars& s) {
 
 // 8 elements at p (aligned), or the first `n` of them one by one.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&f)[kVec]) {
-  if (vec && n >= kVec) {
-    Pack<T, kVec> v;
-    v.load(p);
+__device__ __forceinline__ Pack<T, kVec> load8(const T* p, int n, bool vec) {
+  Pack<T, kVec> v;
+  if (vec && n >= kVec) v.load(p);
+  else v.load_some(p, n);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const Pack<T, kVec>& v, float (&f)[kVec]) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) f[i] = v.get(i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      Pack<T, 1> v;
-      v.zero();
-      if (i < n) v.load(p + i);
-      f[i] = v.get(0);
-    }
-  }
+  for (int i = 0; i < kVec; ++i) f[i] = v.get(i);
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&f)[kVec]) {
-  if (vec && n >= kVec) {
-    Pack<T, kVec> v;
-    v.set(f);
-    v.store(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      if (i < n) {
-        Pack<T, 1> v;
-        const float one[1] = {f[i]};
-        v.set(one);
-        v.store(p + i);
-      }
-  }
+  Pack<T, kVec> v;
+  v.set(f);
+  if (vec && n >= kVec) v.store(p);
+  else v.store_some(p, n);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -138,11 +123,11 @@ __device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&f)[k
 template <typename P, typename G, bool MASTER>
 __device__ __forceinline__ void adam_step_at(const AdamEntry& e, const AdamFactors& f, int64_t at, int n, bool vec) {
   float p[kVec], g[kVec], m[kVec], v[kVec];
-  load8(static_cast<const G*>(e.g) + at, n, vec, g);
-  load8(static_cast<const float*>(e.m) + at, n, vec, m);
-  load8(static_cast<const float*>(e.v) + at, n, vec, v);
-  if constexpr (MASTER) load8(e.master + at, n, vec, p);
-  else load8(static_cast<const P*>(e.p) + at, n, vec, p);
+  unpack8(load8(static_cast<const G*>(e.g) + at, n, vec), g);
+  unpack8(load8(static_cast<const float*>(e.m) + at, n, vec), m);
+  unpack8(load8(static_cast<const float*>(e.v) + at, n, vec), v);
+  if constexpr (MASTER) unpack8(load8(e.master + at, n, vec), p);
+  else unpack8(load8(static_cast<const P*>(e.p) + at, n, vec), p);
 #pragma unroll
   for (int i = 0; i < kVec; ++i) adam_element(f, g[i], p[i], m[i], v[i]);
   if constexpr (MASTER) store8(e.master + at, n, vec, p);
@@ -275,7 +260,7 @@ __device__ __forceinline__ uint2 q8_block(const float2 (&line)[256], const float
   for (int i = 0; i < kVec; ++i) top = max_nan(top, fabsf(f[i]));
   float a = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
   if (a < kQ8Least) a = 0.f;
-  const float inv = a > 0.f ? __fdiv_rn(1.f, a) : 0.f;
+  const float inv = a > 0.f ? __frcp_rn(a) : 0.f;
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -316,17 +301,42 @@ __global__ void __launch_bounds__(kThreads)
     const bool vec = e.head != kScalar;
     const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[t]) * list.chunk_elems;
     const int64_t end = min(begin + list.chunk_elems, e.n);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int64_t block = begin + warp * TBE_Q8_BLOCK; block < end; block += kStep) {
+    const int lane = threadIdx.x % 32;
+    // A block as a lane has it.  The next block's loads are in flight while this one's codes are computed.
+    using Held = typename std::conditional<MASTER, float, P>::type;
+    struct Block {
+      uint2 m, v;
+      Pack<G, kVec> g;
+      Pack<Held, kVec> p;
+      float ms, vs;
+      int n;  // elements of the lane
+    };
+    const Held* held = MASTER ? reinterpret_cast<const Held*>(e.master) : static_cast<const Held*>(e.p);
+    auto load = [&](int64_t block) {
+      Block b;
       const int64_t at = block + lane * kVec;
-      const int n = static_cast<int>(min(max(e.n - at, int64_t(0)), static_cast<int64_t>(kVec)));
+      b.n = max(min(static_cast<int>(min(e.n - block, int64_t(TBE_Q8_BLOCK))) - lane * kVec, kVec), 0);
+      b.m = load_codes(e.m, at, b.n, vec);
+      b.v = load_codes(e.v, at, b.n, vec);
+      b.g = load8(static_cast<const G*>(e.g) + at, b.n, vec);
+      b.p = load8(held + at, b.n, vec);
+      b.ms = e.ms[block / TBE_Q8_BLOCK];
+      b.vs = e.vs[block / TBE_Q8_BLOCK];
+      return b;
+    };
+    int64_t block = begin + (threadIdx.x / 32) * TBE_Q8_BLOCK;
+    Block next;
+    if (block < end) next = load(block);
+    for (; block < end; block += kStep) {
+      const Block b = next;
+      if (block + kStep < end) next = load(block + kStep);
+      const int64_t at = block + lane * kVec;
+      const int n = b.n;
       float p[kVec], g[kVec], m[kVec], v[kVec];
-      const uint2 mc = load_codes(e.m, at, n, vec), vc = load_codes(e.v, at, n, vec);
-      load8(static_cast<const G*>(e.g) + at, n, vec, g);
-      if constexpr (MASTER) load8(e.master + at, n, vec, p);
-      else load8(static_cast<const P*>(e.p) + at, n, vec, p);
-      q8_values<true>(mc, e.ms[block / TBE_Q8_BLOCK], m);
-      q8_values<false>(vc, e.vs[block / TBE_Q8_BLOCK], v);
+      unpack8(b.g, g);
+      unpack8(b.p, p);
+      q8_values<true>(b.m, b.ms, m);
+      q8_values<false>(b.v, b.vs, v);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) adam_element(f, g[i], p[i], m[i], v[i]);
       if (n < kVec) {
@@ -336,12 +346,12 @@ __global__ void __launch_bounds__(kThreads)
       }
       if constexpr (MASTER) store8(e.master + at, n, vec, p);
       store8(static_cast<P*>(e.p) + at, n, vec, p);
-      float a, b;
-      store_codes(e.m, at, n, vec, q8_block<true>(lines.line[0], m, &a));
-      store_codes(e.v, at, n, vec, q8_block<false>(lines.line[1], v, &b));
+      float ms, vs;
+      store_codes(e.m, at, n, vec, q8_block<true>(lines.line[0], m, &ms));
+      store_codes(e.v, at, n, vec, q8_block<false>(lines.line[1], v, &vs));
       if (lane == 0) {
-        e.ms[block / TBE_Q8_BLOCK] = a;
-        e.vs[block / TBE_Q8_BLOCK] = b;
+        e.ms[block / TBE_Q8_BLOCK] = ms;
+        e.vs[block / TBE_Q8_BLOCK] = vs;
       }
     }
   } else if (s.clip != nullptr && !isfinite(s.clip[0])) {
@@ -471,9 +481,11 @@ __global__ void __launch_bounds__(kThreads)
 // ------------------------------------------------------------------------------------------
 // Host
 // ------------------------------------------------------------------------------------------
-// Elements of a chunk: 4 passes of a CTA, or one while that leaves SMs without work.
-uint32_t chunk_elems(int64_t total, const DeviceInfo& dev) {
-  return total / (4 * kStep) >= 4 * static_cast<int64_t>(dev.sms) ? 4 * kStep : kStep;
+// Elements of a chunk: up to `most` passes of a CTA (a power of two), fewer while that leaves less than 16 chunks to an SM.
+uint32_t chunk_elems(int64_t total, const DeviceInfo& dev, int most) {
+  int passes = 1;
+  while (passes < most && total / (2 * passes * kStep) >= 16 * static_cast<int64_t>(dev.sms)) passes *= 2;
+  return static_cast<uint32_t>(passes * kStep);
 }
 
 // Splits the tensors into launches of at most the list's capacity and at most 2^31 - 1 chunks; fill(i, entry)
@@ -565,7 +577,7 @@ tbe_status launch_adamw(const tbe_adamw_problem& prob, AdamScalars sc, const Dev
   for (int i = 0; i < prob.count; ++i) total += prob.tensors[i].numel;
   const bool q8 = prob.states == TBE_STATE_Q8;
   return for_lists<AdamEntry, kLargeAdam>(
-      prob.count, chunk_elems(total, dev), [&](int i) { return prob.tensors[i].numel; },
+      prob.count, chunk_elems(total, dev, q8 ? 16 : 4), [&](int i) { return prob.tensors[i].numel; },
       [&](int i, AdamEntry* e) {
         const tbe_dense_tensor& d = prob.tensors[i];
         int head = d.numel == 0 ? 0 : kScalar;
@@ -622,7 +634,7 @@ tbe_status tbe_grad_norm(int32_t count, const void* const* grads, const int64_t*
   return with_type(dtype, [&](auto tag) {
     using G = typename decltype(tag)::type;
     return for_lists<NormEntry, kLargeNorm>(
-        count, chunk_elems(total, dev), [&](int i) { return numels[i]; },
+        count, chunk_elems(total, dev, 4), [&](int i) { return numels[i]; },
         [&](int i, NormEntry* e) { *e = NormEntry{grads[i], numels[i]}; },
         [&](auto& list, bool first, bool last) {
           constexpr int CAP = static_cast<int>(sizeof(list.e) / sizeof(list.e[0]));
@@ -689,7 +701,7 @@ tbe_status tbe_adamw_state_values(const tbe_adamw_problem* prob, float* const* e
   if ((st = device_info(&dev)) != TBE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return for_lists<ValuesEntry, kLargeValues>(
-      prob->count, chunk_elems(total, dev), [&](int i) { return prob->tensors[i].numel; },
+      prob->count, chunk_elems(total, dev, 4), [&](int i) { return prob->tensors[i].numel; },
       [&](int i, ValuesEntry* e) {
         const tbe_dense_tensor& d = prob->tensors[i];
         float* m = exp_avg_values != nullptr ? exp_avg_values[i] : nullptr;

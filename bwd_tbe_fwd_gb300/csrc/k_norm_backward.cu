@@ -59,14 +59,11 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
   float w[J][V], dw[J][V], db[J][V];
 #pragma unroll
   for (int j = 0; j < J; ++j) in[j] = (j * L + lane) * V < width;
-  const RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, smem);
-  const RowReader<Y, V, L, T> dy(g.dy, a.y_stride, col0 + lane * V, smem + kStages * stage_bytes<X, V>(T));
+  RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, walk.first, walk.step, smem);
+  RowReader<Y, V, L, T> dy(g.dy, a.y_stride, col0 + lane * V, walk.first, walk.step, smem + kStages * stage_bytes<X, V>(T));
   for (int k = 0; k < kStages - 1; ++k) {
-    const int64_t r = walk.first + k * walk.step;
-    if (r < walk.end) {
-      x.copy(k, r, in);
-      dy.copy(k, r, in);
-    }
+    x.copy(k, walk.first + k * walk.step < walk.end, in);
+    dy.copy(k, walk.first + k * walk.step < walk.end, in);
     async_commit();
   }
 #pragma unroll
@@ -82,18 +79,18 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
     rs = g.rstd[walk.first * a.segments + seg];
   }
   int stage = 0;
-  for (int64_t k = 0; k < walk.count; ++k) {
-    const int64_t r = walk.first + k * walk.step, ahead = r + (kStages - 1) * walk.step;
-    if (ahead < walk.end) {
-      x.copy(stage == 0 ? kStages - 1 : stage - 1, ahead, in);
-      dy.copy(stage == 0 ? kStages - 1 : stage - 1, ahead, in);
-    }
+  int64_t r = walk.first;
+  X* dx = static_cast<X*>(g.dx) + r * a.dx_stride + col0 + lane * V;
+  for (int64_t k = 0; k < walk.count; ++k, r += walk.step, dx += walk.step * a.dx_stride) {
+    const bool more = r + (kStages - 1) * walk.step < walk.end;
+    x.copy(stage == 0 ? kStages - 1 : stage - 1, more, in);
+    dy.copy(stage == 0 ? kStages - 1 : stage - 1, more, in);
     async_commit();
     async_wait<kStages - 1>();
     const bool valid = r < walk.end;
     float xh[J][V], h[J][V];
-    x.read(stage, r, valid, in, xh);
-    dy.read(stage, r, valid, in, h);
+    x.read(stage, valid, in, xh);
+    dy.read(stage, valid, in, h);
     stage = stage == kStages - 1 ? 0 : stage + 1;
     float2 c = make_float2(0.f, 0.f);
     const float m = valid ? mu : 0.f, q = valid ? rs : 0.f;
@@ -106,7 +103,7 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float d = h[j][i];
-        xh[j][i] = in[j] ? (xh[j][i] - m) * q : 0.f;
+        xh[j][i] = (xh[j][i] - m) * q;  // times d = 0 outside the row
         dw[j][i] = fmaf(d, xh[j][i], dw[j][i]);
         db[j][i] += d;
         h[j][i] = d * w[j][i];
@@ -117,7 +114,6 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
     c = row_sum2<L, T>(c, part[k & 1]);  // the next row's sums go to the other buffer: one barrier a row
     if (!valid) continue;
     const float c1 = c.x * inv_n * q, c2 = c.y * inv_n * q;
-    X* dx = static_cast<X*>(g.dx) + r * a.dx_stride + col0 + lane * V;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       if (!in[j]) continue;

@@ -27,10 +27,9 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
   float w[J][V], b[J][V];
 #pragma unroll
   for (int j = 0; j < J; ++j) in[j] = (j * L + lane) * V < width;
-  const RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, smem);
+  RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, walk.first, walk.step, smem);
   for (int k = 0; k < kStages - 1; ++k) {
-    const int64_t r = walk.first + k * walk.step;
-    if (r < walk.end) x.copy(k, r, in);
+    x.copy(k, walk.first + k * walk.step < walk.end, in);
     async_commit();
   }
 #pragma unroll
@@ -41,14 +40,15 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
   }
   const float inv_n = 1.f / static_cast<float>(width);
   int stage = 0;
-  for (int64_t k = 0; k < walk.count; ++k) {
-    const int64_t r = walk.first + k * walk.step, ahead = r + (kStages - 1) * walk.step;
-    if (ahead < walk.end) x.copy(stage == 0 ? kStages - 1 : stage - 1, ahead, in);
+  int64_t r = walk.first;
+  Y* y = static_cast<Y*>(g.y) + r * a.y_stride + col0 + lane * V;
+  for (int64_t k = 0; k < walk.count; ++k, r += walk.step, y += walk.step * a.y_stride) {
+    x.copy(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * walk.step < walk.end, in);
     async_commit();
     async_wait<kStages - 1>();
     const bool valid = r < walk.end;
     float f[J][V];
-    x.read(stage, r, valid, in, f);
+    x.read(stage, valid, in, f);
     stage = stage == kStages - 1 ? 0 : stage + 1;
     float s = 0.f;
 #pragma unroll
@@ -66,7 +66,6 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
       }
     const float rs = __frsqrt_rn(fmaf(row_sum<L, T>(s, part[1]), inv_n, a.eps));
     if (!valid) continue;
-    Y* y = static_cast<Y*>(g.y) + r * a.y_stride + col0 + lane * V;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       if (!in[j]) continue;

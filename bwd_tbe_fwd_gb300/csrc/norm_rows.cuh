@@ -32,36 +32,40 @@ struct RowReader {
   static constexpr int J = kPer / V;
   static constexpr int kChunk = V * static_cast<int>(sizeof(E)) >= 16 ? 16 : V * static_cast<int>(sizeof(E));
   static constexpr int kChunks = V == 1 ? 1 : V * static_cast<int>(sizeof(E)) / kChunk;
-  const E* base;       // the thread's first element in row 0
-  int64_t stride;
+  const E* next;       // the thread's first element in the next row to copy (V = 1: to read)
+  int64_t step;        // from one of the thread's rows to the next
   uint32_t place;      // shared memory: the thread's first chunk of stage 0
 
-  __device__ __forceinline__ RowReader(const void* p, int64_t stride_, int col, char* smem)
-      : base(static_cast<const E*>(p) + col), stride(stride_), place(smem_u32(smem) + threadIdx.x * kChunk) {}
+  __device__ __forceinline__ RowReader(const void* p, int64_t stride, int col, int64_t first_row, int64_t row_step, char* smem)
+      : next(static_cast<const E*>(p) + first_row * stride + col), step(row_step * stride),
+        place(smem_u32(smem) + threadIdx.x * kChunk) {}
 
-  __device__ __forceinline__ void copy(int stage, int64_t row, const bool (&in)[J]) const {
+  // Begins the copy of the next row into a stage; `valid`: the row exists.
+  __device__ __forceinline__ void copy(int stage, bool valid, const bool (&in)[J]) {
     if constexpr (V > 1) {
-      const E* r = base + row * stride;
+      if (valid) {
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (in[j]) {
+        for (int j = 0; j < J; ++j)
+          if (in[j]) {
 #pragma unroll
-          for (int k = 0; k < kChunks; ++k)
-            async_copy<kChunk>(place + stage * stage_bytes<E, V>(T) + (j * kChunks + k) * T * kChunk,
-                               reinterpret_cast<const char*>(r + j * L * V) + k * kChunk);
-        }
+            for (int k = 0; k < kChunks; ++k)
+              async_copy<kChunk>(place + stage * stage_bytes<E, V>(T) + (j * kChunks + k) * T * kChunk,
+                                 reinterpret_cast<const char*>(next + j * L * V) + k * kChunk);
+          }
+      }
+      next += step;
     }
   }
 
-  // The thread's elements of a row (zero outside it).
-  __device__ __forceinline__ void read(int stage, int64_t row, bool valid, const bool (&in)[J], float (&f)[J][V]) const {
+  // The thread's elements of the row in a stage (zero outside it).
+  __device__ __forceinline__ void read(int stage, bool valid, const bool (&in)[J], float (&f)[J][V]) {
     Pack<E, V> v[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       v[j].zero();
       if (valid && in[j]) {
         if constexpr (V == 1) {
-          v[j].load(base + row * stride + j * L);
+          v[j].load(next + j * L);
         } else {
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) {
@@ -76,6 +80,7 @@ struct RowReader {
         }
       }
     }
+    if constexpr (V == 1) next += step;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
