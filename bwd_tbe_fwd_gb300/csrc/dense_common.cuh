@@ -107,6 +107,36 @@ struct Pack {
   }
 };
 
+// Two fp32 values in a register pair: one instruction for both.
+struct F2 {
+  uint64_t b;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ explicit F2(float both) : F2(both, both) {}
+  __device__ __forceinline__ void get(float& lo, float& hi) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(b));
+  }
+  __device__ __forceinline__ float lo() const { float x, y; get(x, y); return x; }
+  __device__ __forceinline__ float hi() const { float x, y; get(x, y); return y; }
+};
+__device__ __forceinline__ F2 operator*(F2 x, F2 y) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(x.b), "l"(y.b));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 x, F2 y) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(x.b), "l"(y.b));
+  return r;
+}
+// x y + z, rounded once.  A product that has to be rounded before it is added to something is fma2(x, y, -0) with a zero
+// that the compiler does not know: ptxas contracts mul.rn.f32x2 and add.rn.f32x2 into one operation.
+__device__ __forceinline__ F2 fma2(F2 x, F2 y, F2 z) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(x.b), "l"(y.b), "l"(z.b));
+  return r;
+}
+
 // One element of a buffer whose type is only known at run time (weights, read once for many rows).
 __device__ __forceinline__ float load_any(const void* p, int type, int64_t i) {
   if (type == TBE_F32) return static_cast<const float*>(p)[i];
@@ -136,12 +166,12 @@ __device__ __forceinline__ void load_weights(const void* p, int type, int64_t c,
   }
 }
 
-// Asynchronous copy of one thread's BYTES (8, or a multiple of 16) into its own place in shared memory; the thread
+// Asynchronous copy of one thread's BYTES (4, 8 or 16) into its own place in shared memory; the thread
 // that copied them is the only one to read them, after async_wait, so no barrier is needed.
 template <int BYTES>
 __device__ __forceinline__ void async_copy(uint32_t dst, const void* src) {
-  if constexpr (BYTES == 8) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  if constexpr (BYTES < 16) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
   } else {
     static_assert(BYTES == 16, "");
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -151,6 +181,19 @@ __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_g
 template <int PENDING>
 __device__ __forceinline__ void async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// What async_copy put there: BYTES / 4 words.
+template <int BYTES>
+__device__ __forceinline__ void shared_words(uint32_t src, uint32_t* w) {
+  if constexpr (BYTES == 4) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(src) : "memory");
+  } else if constexpr (BYTES == 8) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src) : "memory");
+  } else {
+    static_assert(BYTES == 16, "");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src) : "memory");
+  }
 }
 
 // Sum over the L lanes (a power of two, aligned) that a thread is one of.

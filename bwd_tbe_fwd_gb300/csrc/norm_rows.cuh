@@ -70,12 +70,7 @@ struct RowReader {
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) {
             const uint32_t at = place + stage * stage_bytes<E, V>(T) + (j * kChunks + k) * T * kChunk;
-            if constexpr (kChunk == 16)
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(v[j].w[4 * k]), "=r"(v[j].w[4 * k + 1]), "=r"(v[j].w[4 * k + 2]), "=r"(v[j].w[4 * k + 3])
-                           : "r"(at) : "memory");
-            else
-              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[j].w[0]), "=r"(v[j].w[1]) : "r"(at) : "memory");
+            shared_words<kChunk>(at, &v[j].w[(kChunk / 4) * k]);
           }
         }
       }

@@ -14,7 +14,7 @@ import math
 
 import torch
 
-from .tbe import _WDTYPE, TBE_OK, TBEError, _check, _stream, c_f32, c_i32, c_i64, load, vp
+from .tbe import _WDTYPE, TBE_OK, TBEError, _check, c_f32, c_i32, c_i64, load, vp
 
 TBE_STATE_F32, TBE_STATE_Q8 = 0, 1
 TBE_Q8_BLOCK = 256
@@ -67,9 +67,18 @@ def _device(device) -> torch.device:
     return dev
 
 
+# The current stream's handle without making a Stream object (which costs 2 to 4 us of a small call's 10).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _launch(device, fn, args, stream, what):
     """Calls the library with `device` current, on `stream` (default: the device's current one)."""
-    s = _stream(stream, device)
+    if stream is not None:
+        s = stream.cuda_stream
+    elif _current_raw_stream is not None and device.type == "cuda":
+        s = _current_raw_stream(device.index)
+    else:
+        s = torch.cuda.current_stream(device).cuda_stream
     if device.type == "cuda" and torch.cuda.current_device() == device.index:
         status = fn(*args, s)
     else:
@@ -88,9 +97,10 @@ def _empty(shape, dtype, device, stream):
 
 
 def _flat(t, name, dtype, numel, device):
-    if t.dtype != dtype:
+    """Address of a contiguous tensor of that type and size on that device."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.device != device or not t.is_contiguous():
+    if t.get_device() != (-1 if device.index is None else device.index) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous on {device}")
     if t.numel() != numel:
         raise ValueError(f"{name} must have {numel} elements")
@@ -110,6 +120,7 @@ class LayerNorm:
                  device="cuda"):
         self.lib = _bind(load())
         self.device = _device(device)
+        self._index = -1 if self.device.index is None else self.device.index
         self.widths = [int(w) for w in ([widths] if isinstance(widths, int) else widths)]
         self.cols = sum(self.widths)
         self.x_dtype, self.y_dtype, self.weight_dtype = x_dtype, y_dtype or x_dtype, weight_dtype
@@ -129,17 +140,19 @@ class LayerNorm:
 
     def _rows(self, t, name, dtype, rows=None):
         """Row stride of a [rows, cols] matrix."""
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}")
-        if t.dim() != 2 or t.shape[1] != self.cols or (rows is not None and t.shape[0] != rows):
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != self.cols or (rows is not None and shape[0] != rows):
             raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {self.cols}]")
-        if t.device != self.device or (self.cols > 1 and t.stride(1) != 1):
+        stride = t.stride()
+        if t.get_device() != self._index or (self.cols > 1 and stride[1] != 1):
             raise ValueError(f"{name} must be on {self.device} with contiguous columns")
-        if t.shape[0] <= 1:
+        if shape[0] <= 1:
             return self.cols
-        if t.stride(0) < self.cols:
+        if stride[0] < self.cols:
             raise ValueError(f"the rows of {name} overlap")
-        return t.stride(0)
+        return stride[0]
 
     def _param(self, t, name):
         return None if t is None else _flat(t, name, self.weight_dtype, self.cols, self.device)
@@ -241,7 +254,7 @@ class DenseAdamW:
         self.device = self.params[0].device if n else _device(device)
         q8 = {"f32": False, "q8": True}[states]
         self.states = states
-        numels = [p.numel() for p in self.params]
+        self._numels = numels = [p.numel() for p in self.params]
         self.master = None if master is None else list(master)
         if self.master is not None and n and self.params[0].dtype == torch.float32:
             raise TypeError("float32 params take no master")
@@ -322,11 +335,11 @@ class DenseAdamW:
         lists = []
         for given, name in ((exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq")):
             if given is None:
-                given = [_empty(p.numel(), torch.float32, self.device, stream) for p in self.params]
+                given = [_empty(n, torch.float32, self.device, stream) for n in self._numels]
             self._same_count(given, name)
-            for t, p in zip(given, self.params):
-                _flat(t, name, torch.float32, p.numel(), self.device)
-            lists.append(given)
-        _launch(self.device, self.lib.tbe_adamw_state_values,
-                (self._prob, _pointers(lists[0]), _pointers(lists[1])), stream, "tbe_adamw_state_values")
-        return lists[0], lists[1]
+            ptrs = (vp * max(1, len(given)))(*[_flat(t, name, torch.float32, n, self.device)
+                                               for t, n in zip(given, self._numels)])
+            lists.append((given, ptrs))
+        _launch(self.device, self.lib.tbe_adamw_state_values, (self._prob, lists[0][1], lists[1][1]), stream,
+                "tbe_adamw_state_values")
+        return lists[0][0], lists[1][0]
