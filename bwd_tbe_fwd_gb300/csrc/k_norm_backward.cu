@@ -56,7 +56,6 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
   __shared__ float2 part[2][T / 32];
   const int lane = threadIdx.x % L;
   bool in[J];
-  float w[J][V], dw[J][V], db[J][V];
 #pragma unroll
   for (int j = 0; j < J; ++j) in[j] = (j * L + lane) * V < width;
   RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, walk.first, walk.step, smem);
@@ -66,12 +65,10 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
     dy.copy(k, walk.first + k * walk.step < walk.end, in);
     async_commit();
   }
+  F2 w[kPer / 2], dw[kPer / 2], db[kPer / 2];
+  read_weights<V, L>(g.weight, a.wtype, in[0] ? col0 + lane * V : col0, in, 1.f, w);
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    load_weights<V>(g.weight, a.wtype, in[j] ? col0 + (j * L + lane) * V : col0, 1.f, w[j]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) dw[j][i] = db[j][i] = 0.f;
-  }
+  for (int i = 0; i < kPer / 2; ++i) dw[i] = db[i] = F2(0.f);
   const float inv_n = 1.f / static_cast<float>(width);
   float mu = 0.f, rs = 0.f;  // of the row to come
   if (walk.first < walk.end) {
@@ -88,65 +85,53 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
     async_commit();
     async_wait<kStages - 1>();
     const bool valid = r < walk.end;
-    float xh[J][V], h[J][V];
+    F2 xh[kPer / 2], h[kPer / 2];
     x.read(stage, valid, in, xh);
     dy.read(stage, valid, in, h);
     stage = stage == kStages - 1 ? 0 : stage + 1;
-    float2 c = make_float2(0.f, 0.f);
-    const float m = valid ? mu : 0.f, q = valid ? rs : 0.f;
+    const float q = valid ? rs : 0.f;
+    const F2 shift(valid ? -mu : 0.f), scale(q);
     if (r + walk.step < walk.end) {
       mu = g.mean[(r + walk.step) * a.segments + seg];
       rs = g.rstd[(r + walk.step) * a.segments + seg];
     }
+    F2 s1(0.f), s2(0.f);
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float d = h[j][i];
-        xh[j][i] = (xh[j][i] - m) * q;  // times d = 0 outside the row
-        dw[j][i] = fmaf(d, xh[j][i], dw[j][i]);
-        db[j][i] += d;
-        h[j][i] = d * w[j][i];
-        c.x += h[j][i];
-        c.y = fmaf(h[j][i], xh[j][i], c.y);
-      }
-    if (g.dx == nullptr) continue;
-    c = row_sum2<L, T>(c, part[k & 1]);  // the next row's sums go to the other buffer: one barrier a row
-    if (!valid) continue;
-    const float c1 = c.x * inv_n * q, c2 = c.y * inv_n * q;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if (!in[j]) continue;
-#pragma unroll
-      for (int i = 0; i < V; ++i) h[j][i] = fmaf(-xh[j][i], c2, fmaf(h[j][i], q, -c1));
-      Pack<X, V> o;
-      o.set(h[j]);
-      o.store(dx + j * L * V);
+    for (int i = 0; i < kPer / 2; ++i) {
+      xh[i] = (xh[i] + shift) * scale;  // outside the row times dy = 0
+      dw[i] = fma2(h[i], xh[i], dw[i]);
+      db[i] = db[i] + h[i];
+      h[i] = h[i] * w[i];
+      s1 = s1 + h[i];
+      s2 = fma2(h[i], xh[i], s2);
     }
+    if (g.dx == nullptr) continue;
+    // the next row's sums go to the other buffer: one barrier a row
+    const float2 c = row_sum2<L, T>(make_float2(s1.lo() + s1.hi(), s2.lo() + s2.hi()), part[k & 1]);
+    if (!valid) continue;
+    const F2 c1(-c.x * inv_n * q), c2(-c.y * inv_n * q);
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) h[i] = fma2(xh[i], c2, fma2(h[i], scale, c1));
+    write_row<X, V, L>(dx, in, h);
   }
   if (!out.wanted()) return;
+  auto value = [](const F2 (&f)[kPer / 2], int i) { return i & 1 ? f[i / 2].hi() : f[i / 2].lo(); };
   if constexpr (L > 32) {  // each thread owns its columns
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (in[j]) out.put(a, slot, col0 + (j * L + lane) * V + i, dw[j][i], db[j][i]);
+        if (in[j]) out.put(a, slot, col0 + (j * L + lane) * V + i, value(dw, j * V + i), value(db, j * V + i));
   } else {  // the T / L groups of the CTA hold the same columns: [groups][kPer * L] sums in shared memory, added in order
     async_wait<0>();
     __syncthreads();  // every thread is done with the stages
     float* sums = reinterpret_cast<float*>(smem);
     constexpr int kSpan = kPer * L;
-    auto combine = [&](const float (&v)[J][V], int pass) {
-      float* mine = sums + pass * T * kPer + (threadIdx.x / L) * kSpan;
+    bool all[J];
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        Pack<float, V> o;
-        o.set(v[j]);
-        o.store(mine + (j * L + lane) * V);
-      }
-    };
-    combine(dw, 0);
-    combine(db, 1);
+    for (int j = 0; j < J; ++j) all[j] = true;
+    write_row<float, V, L>(sums + threadIdx.x / L * kSpan + lane * V, all, dw);
+    write_row<float, V, L>(sums + T * kPer + threadIdx.x / L * kSpan + lane * V, all, db);
     __syncthreads();
     for (int c = threadIdx.x; c < width; c += T) {
       float tw = 0.f, tb = 0.f;

@@ -24,7 +24,6 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
   __shared__ float part[2][T / 32];
   const int lane = threadIdx.x % L;
   bool in[J];
-  float w[J][V], b[J][V];
 #pragma unroll
   for (int j = 0; j < J; ++j) in[j] = (j * L + lane) * V < width;
   RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, walk.first, walk.step, smem);
@@ -32,12 +31,10 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
     x.copy(k, walk.first + k * walk.step < walk.end, in);
     async_commit();
   }
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int c = in[j] ? col0 + (j * L + lane) * V : col0;
-    load_weights<V>(g.weight, a.wtype, c, 1.f, w[j]);
-    load_weights<V>(g.bias, a.wtype, c, 0.f, b[j]);
-  }
+  F2 w[kPer / 2], b[kPer / 2];
+  const int first_col = in[0] ? col0 + lane * V : col0;
+  read_weights<V, L>(g.weight, a.wtype, first_col, in, 1.f, w);
+  read_weights<V, L>(g.bias, a.wtype, first_col, in, 0.f, b);
   const float inv_n = 1.f / static_cast<float>(width);
   int stage = 0;
   int64_t r = walk.first;
@@ -47,34 +44,25 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
     async_commit();
     async_wait<kStages - 1>();
     const bool valid = r < walk.end;
-    float f[J][V];
+    F2 f[kPer / 2];
     x.read(stage, valid, in, f);
     stage = stage == kStages - 1 ? 0 : stage + 1;
-    float s = 0.f;
+    F2 s(0.f);
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+    for (int i = 0; i < kPer / 2; ++i) s = s + f[i];
+    const float mu = row_sum<L, T>(s.lo() + s.hi(), part[0]) * inv_n;
+    s = F2(0.f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) s += f[j][i];
-    const float mu = row_sum<L, T>(s, part[0]) * inv_n;
-    s = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        f[j][i] = in[j] ? f[j][i] - mu : 0.f;
-        s = fmaf(f[j][i], f[j][i], s);
-      }
-    const float rs = __frsqrt_rn(fmaf(row_sum<L, T>(s, part[1]), inv_n, a.eps));
+    for (int i = 0; i < kPer / 2; ++i) {
+      const bool in0 = in[2 * i / V], in1 = in[(2 * i + 1) / V];
+      f[i] = f[i] + F2(V > 1 || in0 ? -mu : 0.f, V > 1 || in1 ? -mu : 0.f);
+      if (V == 1 || in0) s = fma2(f[i], f[i], s);
+    }
+    const float rs = __frsqrt_rn(fmaf(row_sum<L, T>(s.lo() + s.hi(), part[1]), inv_n, a.eps));
     if (!valid) continue;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if (!in[j]) continue;
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[j][i] = fmaf(f[j][i] * rs, w[j][i], b[j][i]);
-      Pack<Y, V> o;
-      o.set(f[j]);
-      o.store(y + j * L * V);
-    }
+    for (int i = 0; i < kPer / 2; ++i) f[i] = fma2(f[i] * F2(rs), w[i], b[i]);
+    write_row<Y, V, L>(y, in, f);
     if (g.mean != nullptr && lane == 0) {
       g.mean[r * a.segments + seg] = mu;
       g.rstd[r * a.segments + seg] = rs;

@@ -57,8 +57,8 @@ struct RowReader {
     }
   }
 
-  // The thread's elements of the row in a stage (zero outside it).
-  __device__ __forceinline__ void read(int stage, bool valid, const bool (&in)[J], float (&f)[J][V]) {
+  // The thread's elements of the row in a stage (zero outside it), in pairs: those of vector 0, of vector 1, ...
+  __device__ __forceinline__ void read(int stage, bool valid, const bool (&in)[J], F2 (&f)[kPer / 2]) {
     Pack<E, V> v[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -77,11 +77,39 @@ struct RowReader {
     }
     if constexpr (V == 1) next += step;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[j][i] = v[j].get(i);
+    for (int k = 0; k < kPer / 2; ++k)
+      f[k] = F2(v[2 * k / V].get(2 * k % V), v[(2 * k + 1) / V].get((2 * k + 1) % V));
   }
 };
+
+// The weights of a thread's elements, in pairs as RowReader::read's.
+template <int V, int L>
+__device__ __forceinline__ void read_weights(const void* p, int type, int col, const bool (&in)[kPer / V], float none,
+                                             F2 (&f)[kPer / 2]) {
+  float w[kPer / V][V];
+#pragma unroll
+  for (int j = 0; j < kPer / V; ++j) load_weights<V>(p, type, in[j] ? col + j * L * V : col, none, w[j]);
+#pragma unroll
+  for (int k = 0; k < kPer / 2; ++k) f[k] = F2(w[2 * k / V][2 * k % V], w[(2 * k + 1) / V][(2 * k + 1) % V]);
+}
+
+// Stores a thread's elements, rounded.
+template <typename E, int V, int L>
+__device__ __forceinline__ void write_row(E* p, const bool (&in)[kPer / V], const F2 (&f)[kPer / 2]) {
+  float s[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer / 2; ++k) f[k].get(s[2 * k], s[2 * k + 1]);
+#pragma unroll
+  for (int j = 0; j < kPer / V; ++j)
+    if (in[j]) {
+      float part[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) part[i] = s[j * V + i];
+      Pack<E, V> o;
+      o.set(part);
+      o.store(p + j * L * V);
+    }
+}
 
 // The rows of a thread: `first`, then every `step`th below `end`, `count` of them for every thread of the CTA.
 struct RowWalk {

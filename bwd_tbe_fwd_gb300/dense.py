@@ -333,13 +333,17 @@ class DenseAdamW:
     def state_values(self, exp_avg=None, exp_avg_sq=None, stream=None):
         """What the 8-bit states stand for: two lists of float32 tensors (given ones are written)."""
         lists = []
+        index = -1 if self.device.index is None else self.device.index
         for given, name in ((exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq")):
             if given is None:
                 given = [_empty(n, torch.float32, self.device, stream) for n in self._numels]
             self._same_count(given, name)
-            ptrs = (vp * max(1, len(given)))(*[_flat(t, name, torch.float32, n, self.device)
-                                               for t, n in zip(given, self._numels)])
-            lists.append((given, ptrs))
+            addresses = []
+            for t, n in zip(given, self._numels):
+                if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
+                    _flat(t, name, torch.float32, n, self.device)  # says what is wrong
+                addresses.append(t.data_ptr())
+            lists.append((given, (vp * max(1, len(given)))(*addresses)))
         _launch(self.device, self.lib.tbe_adamw_state_values, (self._prob, lists[0][1], lists[1][1]), stream,
                 "tbe_adamw_state_values")
         return lists[0][0], lists[1][0]
