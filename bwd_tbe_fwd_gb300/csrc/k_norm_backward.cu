@@ -58,8 +58,8 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
   bool in[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) in[j] = (j * L + lane) * V < width;
-  RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, walk.first, walk.step, smem);
-  RowReader<Y, V, L, T> dy(g.dy, a.y_stride, col0 + lane * V, walk.first, walk.step, smem + kStages * stage_bytes<X, V>(T));
+  RowReader<X, V, L, T> x(g.x, a.x_stride, col0, width, walk.first, walk.step, smem);
+  RowReader<Y, V, L, T> dy(g.dy, a.y_stride, col0, width, walk.first, walk.step, smem + kStages * stage_bytes<X, V>(T));
   for (int k = 0; k < kStages - 1; ++k) {
     x.copy(k, walk.first + k * walk.step < walk.end, in);
     dy.copy(k, walk.first + k * walk.step < walk.end, in);
@@ -80,10 +80,12 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
   X* dx = static_cast<X*>(g.dx) + r * a.dx_stride + col0 + lane * V;
   for (int64_t k = 0; k < walk.count; ++k, r += walk.step, dx += walk.step * a.dx_stride) {
     const bool more = r + (kStages - 1) * walk.step < walk.end;
+    x.reuse();
     x.copy(stage == 0 ? kStages - 1 : stage - 1, more, in);
     dy.copy(stage == 0 ? kStages - 1 : stage - 1, more, in);
     async_commit();
     async_wait<kStages - 1>();
+    x.share();
     const bool valid = r < walk.end;
     F2 xh[kPer / 2], h[kPer / 2];
     x.read(stage, valid, in, xh);
@@ -105,7 +107,10 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
       s1 = s1 + h[i];
       s2 = fma2(h[i], xh[i], s2);
     }
-    if (g.dx == nullptr) continue;
+    if (g.dx == nullptr) {
+      x.share();
+      continue;
+    }
     // the next row's sums go to the other buffer: one barrier a row
     const float2 c = row_sum2<L, T>(make_float2(s1.lo() + s1.hi(), s2.lo() + s2.hi()), part[k & 1]);
     if (!valid) continue;
@@ -171,9 +176,9 @@ __global__ void __launch_bounds__(kGroupThreads, 4)
     const RowWalk walk{row0 + threadIdx.x / L, T / L, row1, (row1 - row0 + T / L - 1) / (T / L)};
     backward_rows<X, Y, V, L, T>(a, g, out, slot, seg, col0, width, walk, smem);
   };
-  if (V > 1 && width <= row_capacity(4)) go(std::integral_constant<int, 4>());
-  else if (V > 1 && width <= row_capacity(8)) go(std::integral_constant<int, 8>());
-  else if (V > 1 && width <= row_capacity(16)) go(std::integral_constant<int, 16>());
+  if (width <= row_capacity(4)) go(std::integral_constant<int, 4>());
+  else if (width <= row_capacity(8)) go(std::integral_constant<int, 8>());
+  else if (width <= row_capacity(16)) go(std::integral_constant<int, 16>());
   else go(std::integral_constant<int, 32>());
 }
 
@@ -191,48 +196,64 @@ __global__ void __launch_bounds__(T, 512 / T)
   backward_rows<X, Y, V, T, T>(a, g, out, slot, seg, col0, width, walk, smem);
 }
 
-// Rows wider than a CTA's registers.  First the columns' sums: a thread to a column, down the rows of
-// a slot (dx may overwrite x or dy afterwards).
-template <typename X, typename Y>
-__global__ void __launch_bounds__(256)
+// Rows wider than a CTA's registers.  First the columns' sums: a thread to V columns, down the rows of a slot (dx may
+// overwrite x or dy afterwards).
+constexpr int kColumnThreads = 128;
+
+template <typename X, typename Y, int V>
+__global__ void __launch_bounds__(kColumnThreads)
     norm_backward_columns_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RowIn in,
                                  const __grid_constant__ SumsOut out) {
-  const X* x = static_cast<const X*>(in.x);
-  const Y* dy = static_cast<const Y*>(in.dy);
   int col0, width;
-  segment_span<1>(a, blockIdx.y, &col0, &width);
-  const int tiles = (a.width + 255) / 256;
-  const int c = static_cast<int>(blockIdx.x % tiles) * 256 + threadIdx.x;
+  segment_span<V>(a, blockIdx.y, &col0, &width);
+  const int tiles = (a.width + kColumnThreads * V - 1) / (kColumnThreads * V);
+  const int c = (static_cast<int>(blockIdx.x % tiles) * kColumnThreads + threadIdx.x) * V;
   const int64_t slot = blockIdx.x / tiles;
   if (c >= width) return;
   const int64_t per = (a.rows + out.slots - 1) / out.slots;
   const int64_t row0 = min(slot * per, a.rows), row1 = min(row0 + per, a.rows);
-  float dw = 0.f, db = 0.f;
-#pragma unroll 8
+  const X* x = static_cast<const X*>(in.x) + row0 * a.x_stride + col0 + c;
+  const Y* dy = static_cast<const Y*>(in.dy) + row0 * a.y_stride + col0 + c;
+  const float* mean = in.mean + row0 * a.segments + blockIdx.y;
+  const float* rstd = in.rstd + row0 * a.segments + blockIdx.y;
+  float dw[V], db[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.f;
+#pragma unroll 4
   for (int64_t r = row0; r < row1; ++r) {
-    Pack<X, 1> vx;
-    Pack<Y, 1> vy;
-    vx.load(x + r * a.x_stride + col0 + c);
-    vy.load(dy + r * a.y_stride + col0 + c);
-    const float d = vy.get(0);
-    dw = fmaf(d, (vx.get(0) - in.mean[r * a.segments + blockIdx.y]) * in.rstd[r * a.segments + blockIdx.y], dw);
-    db += d;
+    Pack<X, V> vx;
+    Pack<Y, V> vy;
+    vx.load(x);
+    vy.load(dy);
+    const float mu = *mean, rs = *rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float d = vy.get(i);
+      dw[i] = fmaf(d, (vx.get(i) - mu) * rs, dw[i]);
+      db[i] += d;
+    }
+    x += a.x_stride;
+    dy += a.y_stride;
+    mean += a.segments;
+    rstd += a.segments;
   }
-  out.put(a, slot, col0 + c, dw, db);
+#pragma unroll
+  for (int i = 0; i < V; ++i) out.put(a, slot, col0 + c + i, dw[i], db[i]);
 }
 
 // Then dx, in two passes over each row.
+constexpr int kLongThreads = 512;
+
 template <typename X, typename Y, int V>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kLongThreads)
     norm_backward_long_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RowIn in, int64_t row_slots) {
-  __shared__ float2 part[2][32];
+  __shared__ float2 part[2][kLongThreads / 32];
   const X* x = static_cast<const X*>(in.x);
   const Y* dy = static_cast<const Y*>(in.dy);
   X* dx = static_cast<X*>(in.dx);
   const int seg = blockIdx.x % a.segments;
   int col0, width;
   segment_span<V>(a, seg, &col0, &width);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float inv_n = 1.f / static_cast<float>(width);
   int buf = 0;
   for (int64_t r = blockIdx.x / a.segments; r < a.rows; r += row_slots, buf ^= 1) {
@@ -242,7 +263,7 @@ __global__ void __launch_bounds__(1024)
     X* dr = dx + r * a.dx_stride + col0;
     float c1 = 0.f, c2 = 0.f;
 #pragma unroll 2
-    for (int c = threadIdx.x * V; c < width; c += 1024 * V) {
+    for (int c = threadIdx.x * V; c < width; c += kLongThreads * V) {
       Pack<X, V> vx;
       Pack<Y, V> vy;
       vx.load(xr + c);
@@ -256,14 +277,11 @@ __global__ void __launch_bounds__(1024)
         c2 = fmaf(h, (vx.get(i) - mu) * rs, c2);
       }
     }
-    c1 = lanes_sum<32>(c1);
-    c2 = lanes_sum<32>(c2);
-    if (lane == 0) part[buf][warp] = make_float2(c1, c2);
-    __syncthreads();
-    const float2 p = part[buf][lane];
-    c1 = lanes_sum<32>(p.x) * inv_n;
-    c2 = lanes_sum<32>(p.y) * inv_n;
-    for (int c = threadIdx.x * V; c < width; c += 1024 * V) {
+    const float2 sums = row_sum2<kLongThreads, kLongThreads>(make_float2(c1, c2), part[buf]);
+    c1 = sums.x * inv_n;
+    c2 = sums.y * inv_n;
+#pragma unroll 2
+    for (int c = threadIdx.x * V; c < width; c += kLongThreads * V) {
       Pack<X, V> vx;
       Pack<Y, V> vy;
       vx.load(xr + c);
@@ -328,16 +346,16 @@ tbe_status launch(const NormArgs& a, const RowIn& in, SumsOut out, const DeviceI
     go(norm_backward_wide_kernel<X, Y, V, 512>, 512, false);
   } else {
     if (out.dweight != nullptr || out.dbias != nullptr) {
-      const int64_t tiles = (a.width + 255) / 256;
-      norm_backward_columns_kernel<X, Y>
-          <<<dim3(static_cast<unsigned>(tiles * out.slots), a.segments), 256, 0, s>>>(a, in, out);
+      const int64_t tiles = (a.width + kColumnThreads * V - 1) / (kColumnThreads * V);
+      norm_backward_columns_kernel<X, Y, V>
+          <<<dim3(static_cast<unsigned>(tiles * out.slots), a.segments), kColumnThreads, 0, s>>>(a, in, out);
       note_launch();
     }
     if (in.dx != nullptr) {
-      const int per_seg = persistent_grid(norm_backward_long_kernel<X, Y, V>, 1024, 0, dev, INT32_MAX) / a.segments;
+      const int per_seg = persistent_grid(norm_backward_long_kernel<X, Y, V>, kLongThreads, 0, dev, INT32_MAX) / a.segments;
       const int64_t row_slots = per_seg < 1 ? 1 : per_seg < a.rows ? per_seg : a.rows;
       norm_backward_long_kernel<X, Y, V>
-          <<<static_cast<unsigned>(row_slots * a.segments), 1024, 0, s>>>(a, in, row_slots);
+          <<<static_cast<unsigned>(row_slots * a.segments), kLongThreads, 0, s>>>(a, in, row_slots);
       note_launch();
     }
     return cuda_status(cudaGetLastError());
@@ -351,7 +369,7 @@ tbe_status launch(const NormArgs& a, const RowIn& in, SumsOut out, const DeviceI
 
 int norm_backward_slots(const NormArgs& a, const DeviceInfo& dev) {
   // By parts of warps: two waves of four CTAs to an SM, no fewer than 32 rows to a slot.  By CTAs: one wave of 512
-  // threads to an SM.  Wider still: enough that 256-column tiles fill the SMs four times.
+  // threads to an SM.  Wider still: enough that tiles of 1024 columns fill the SMs sixteen times.
   int64_t want, least;
   if (a.width <= row_capacity(32)) {
     want = static_cast<int64_t>(dev.sms) * 8 / a.segments;
@@ -362,7 +380,7 @@ int norm_backward_slots(const NormArgs& a, const DeviceInfo& dev) {
     want = static_cast<int64_t>(dev.sms) * (512 / threads) / a.segments;
     least = 1;
   } else {
-    want = static_cast<int64_t>(dev.sms) * 4 / (static_cast<int64_t>(a.segments) * ((a.width + 255) / 256));
+    want = static_cast<int64_t>(dev.sms) * 16 / (static_cast<int64_t>(a.segments) * ((a.width + 1023) / 1024));
     least = 16;
   }
   const int64_t most = (a.rows + least - 1) / least;

@@ -26,7 +26,7 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
   bool in[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) in[j] = (j * L + lane) * V < width;
-  RowReader<X, V, L, T> x(g.x, a.x_stride, col0 + lane * V, walk.first, walk.step, smem);
+  RowReader<X, V, L, T> x(g.x, a.x_stride, col0, width, walk.first, walk.step, smem);
   for (int k = 0; k < kStages - 1; ++k) {
     x.copy(k, walk.first + k * walk.step < walk.end, in);
     async_commit();
@@ -40,9 +40,11 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
   int64_t r = walk.first;
   Y* y = static_cast<Y*>(g.y) + r * a.y_stride + col0 + lane * V;
   for (int64_t k = 0; k < walk.count; ++k, r += walk.step, y += walk.step * a.y_stride) {
+    x.reuse();
     x.copy(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * walk.step < walk.end, in);
     async_commit();
     async_wait<kStages - 1>();
+    x.share();
     const bool valid = r < walk.end;
     F2 f[kPer / 2];
     x.read(stage, valid, in, f);
@@ -87,9 +89,9 @@ __global__ void __launch_bounds__(kGroupThreads, 6)
     const RowWalk walk{row0 + threadIdx.x / L, T / L, row1, (row1 - row0 + T / L - 1) / (T / L)};
     forward_rows<X, Y, V, L, T>(a, g, seg, col0, width, walk, smem);
   };
-  if (V > 1 && width <= row_capacity(4)) go(std::integral_constant<int, 4>());
-  else if (V > 1 && width <= row_capacity(8)) go(std::integral_constant<int, 8>());
-  else if (V > 1 && width <= row_capacity(16)) go(std::integral_constant<int, 16>());
+  if (width <= row_capacity(4)) go(std::integral_constant<int, 4>());
+  else if (width <= row_capacity(8)) go(std::integral_constant<int, 8>());
+  else if (width <= row_capacity(16)) go(std::integral_constant<int, 16>());
   else go(std::integral_constant<int, 32>());
 }
 

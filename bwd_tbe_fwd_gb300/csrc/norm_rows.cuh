@@ -5,7 +5,7 @@
 // shuffles to an element (with 4 elements to a thread, half of the instructions were shuffles and
 // addresses, and the kernels were bound by issue).  Rows to come are copied into shared memory
 // asynchronously, kStages - 1 ahead, each thread's elements to its own place: loads stay in flight over the
-// reductions without registers to hold them.  Elements that allow no vector (V = 1) are loaded directly.
+// reductions without registers to hold them.
 #pragma once
 
 #include "dense_common.cuh"
@@ -22,63 +22,133 @@ constexpr int kPlainSmem = 47 * 1024;
 // Widest row that L threads share.
 constexpr int row_capacity(int L) { return kPer * L; }
 
-// Bytes of one stage of type E for T threads.
+// Bytes of one stage of type E for T threads; of rows without vectors (V = 1), 32 more for each row.
 template <typename E, int V>
-constexpr int stage_bytes(int T) { return V == 1 ? 0 : T * kPer * static_cast<int>(sizeof(E)); }
+constexpr int stage_bytes(int T) {
+  return T * kPer * static_cast<int>(sizeof(E)) + (V > 1 ? 0 : 32 * (T <= kGroupThreads ? T / 4 : 1));
+}
 
-// One matrix's rows as a thread sees them.
+// One matrix's rows as a thread sees them: V > 1, each thread copies its own elements.
 template <typename E, int V, int L, int T>
 struct RowReader {
   static constexpr int J = kPer / V;
   static constexpr int kChunk = V * static_cast<int>(sizeof(E)) >= 16 ? 16 : V * static_cast<int>(sizeof(E));
-  static constexpr int kChunks = V == 1 ? 1 : V * static_cast<int>(sizeof(E)) / kChunk;
-  const E* next;       // the thread's first element in the next row to copy (V = 1: to read)
+  static constexpr int kChunks = V * static_cast<int>(sizeof(E)) / kChunk;
+  const E* next;       // the thread's first element in the next row to copy
   int64_t step;        // from one of the thread's rows to the next
   uint32_t place;      // shared memory: the thread's first chunk of stage 0
 
-  __device__ __forceinline__ RowReader(const void* p, int64_t stride, int col, int64_t first_row, int64_t row_step, char* smem)
-      : next(static_cast<const E*>(p) + first_row * stride + col), step(row_step * stride),
+  __device__ __forceinline__ RowReader(const void* p, int64_t stride, int col, int, int64_t first_row, int64_t row_step, char* smem)
+      : next(static_cast<const E*>(p) + first_row * stride + col + threadIdx.x % L * V), step(row_step * stride),
         place(smem_u32(smem) + threadIdx.x * kChunk) {}
 
   // Begins the copy of the next row into a stage; `valid`: the row exists.
   __device__ __forceinline__ void copy(int stage, bool valid, const bool (&in)[J]) {
-    if constexpr (V > 1) {
-      if (valid) {
+    if (valid) {
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-          if (in[j]) {
+      for (int j = 0; j < J; ++j)
+        if (in[j]) {
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k)
-              async_copy<kChunk>(place + stage * stage_bytes<E, V>(T) + (j * kChunks + k) * T * kChunk,
-                                 reinterpret_cast<const char*>(next + j * L * V) + k * kChunk);
-          }
-      }
-      next += step;
+          for (int k = 0; k < kChunks; ++k)
+            async_copy<kChunk>(place + stage * stage_bytes<E, V>(T) + (j * kChunks + k) * T * kChunk,
+                               reinterpret_cast<const char*>(next + j * L * V) + k * kChunk);
+        }
     }
+    next += step;
   }
 
   // The thread's elements of the row in a stage (zero outside it), in pairs: those of vector 0, of vector 1, ...
-  __device__ __forceinline__ void read(int stage, bool valid, const bool (&in)[J], F2 (&f)[kPer / 2]) {
+  __device__ __forceinline__ void read(int stage, bool valid, const bool (&in)[J], F2 (&f)[kPer / 2]) const {
     Pack<E, V> v[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       v[j].zero();
       if (valid && in[j]) {
-        if constexpr (V == 1) {
-          v[j].load(next + j * L);
-        } else {
 #pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            const uint32_t at = place + stage * stage_bytes<E, V>(T) + (j * kChunks + k) * T * kChunk;
-            shared_words<kChunk>(at, &v[j].w[(kChunk / 4) * k]);
-          }
-        }
+        for (int k = 0; k < kChunks; ++k)
+          shared_words<kChunk>(place + stage * stage_bytes<E, V>(T) + (j * kChunks + k) * T * kChunk, &v[j].w[(kChunk / 4) * k]);
       }
     }
-    if constexpr (V == 1) next += step;
 #pragma unroll
     for (int k = 0; k < kPer / 2; ++k)
       f[k] = F2(v[2 * k / V].get(2 * k % V), v[(2 * k + 1) / V].get((2 * k + 1) % V));
+  }
+
+  static __device__ __forceinline__ void share() {}
+  static __device__ __forceinline__ void reuse() {}
+};
+
+// V = 1: rows that start anywhere.  The 16-byte pieces that a row lies in are copied by the threads that share
+// it, whichever element they hold; a piece's bytes past the row's end are not read, those before its start belong to
+// rows before it (or to the gap between them); a piece that begins before the matrix is loaded element by element.
+template <typename E, int L, int T>
+struct RowReader<E, 1, L, T> {
+  static constexpr int J = kPer;
+  static constexpr int kRegion = kPer * L * static_cast<int>(sizeof(E)) + 32;  // of a row in a stage
+  const char* base;    // the segment's first byte in row 0
+  int64_t row, row_step;
+  int64_t pitch;       // bytes from a row to the next
+  int bytes;           // of the segment
+  uint32_t place;      // shared memory: the row's region of stage 0
+
+  __device__ __forceinline__ RowReader(const void* p, int64_t stride, int col, int width, int64_t first_row, int64_t row_step_,
+                                       char* smem)
+      : base(reinterpret_cast<const char*>(static_cast<const E*>(p) + col)), row(first_row), row_step(row_step_),
+        pitch(stride * static_cast<int64_t>(sizeof(E))), bytes(width * static_cast<int>(sizeof(E))),
+        place(smem_u32(smem) + threadIdx.x / L * kRegion) {}
+
+  __device__ __forceinline__ void copy(int stage, bool valid, const bool (&)[J]) {
+    if (valid) {
+      const char* start = base + row * pitch;
+      const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(start) % 16);
+      const uint32_t dst = place + stage * stage_bytes<E, 1>(T);
+      for (int at = threadIdx.x % L * 16; at < skew + bytes; at += L * 16) {
+        if (at == 0 && start - skew < base) {
+          for (int k = 0; k < 16 - skew && k < bytes; k += static_cast<int>(sizeof(E))) {
+            if constexpr (sizeof(E) == 2)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + skew + k), "h"(*reinterpret_cast<const uint16_t*>(start + k)) : "memory");
+            else
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + skew + k), "r"(*reinterpret_cast<const uint32_t*>(start + k)) : "memory");
+          }
+        } else {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + at), "l"(start - skew + at),
+                       "r"(min(16, skew + bytes - at)) : "memory");
+        }
+      }
+    }
+    row += row_step;
+  }
+
+  __device__ __forceinline__ void read(int stage, bool valid, const bool (&in)[J], F2 (&f)[kPer / 2]) const {
+    // the row in the stage is kStages rows behind the next one to copy
+    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(base + (row - kStages * row_step) * pitch) % 16);
+    const uint32_t src = place + stage * stage_bytes<E, 1>(T) + skew + threadIdx.x % L * static_cast<int>(sizeof(E));
+    Pack<E, 1> v[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      v[j].zero();
+      if (valid && in[j]) {
+        if constexpr (sizeof(E) == 2) {
+          uint16_t h;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(src + j * L * 2) : "memory");
+          v[j].w[0] = h;
+        } else {
+          shared_words<4>(src + j * L * 4, v[j].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) f[k] = F2(v[2 * k].get(0), v[2 * k + 1].get(0));
+  }
+
+  // Before other threads' copies are read.
+  static __device__ __forceinline__ void share() {
+    if constexpr (L <= 32) __syncwarp();
+    else __syncthreads();
+  }
+  // Before a stage that other threads have read is filled again (a CTA's row sum has a barrier since).
+  static __device__ __forceinline__ void reuse() {
+    if constexpr (L <= 32) __syncwarp();
   }
 };
 
