@@ -8,6 +8,7 @@ namespace tbe {
 namespace {
 
 constexpr int64_t kMaxCols = int64_t(1) << 30;
+constexpr int64_t kMaxElems = (int64_t(1) << 39) - 1;
 
 tbe_status make_norm(const tbe_norm_problem* p, NormArgs* a) {
   if (p == nullptr || p->rows < 0 || p->segments < 1 || p->widths == nullptr) return TBE_ERR_INVALID_ARG;
@@ -24,7 +25,7 @@ tbe_status make_norm(const tbe_norm_problem* p, NormArgs* a) {
     widest = w > widest ? w : widest;
     equal = equal && w == p->widths[0];
   }
-  if (cols > kMaxCols || p->rows >= (int64_t(1) << 40)) return TBE_ERR_UNSUPPORTED;
+  if (cols > kMaxCols || p->rows > kMaxElems / cols) return TBE_ERR_UNSUPPORTED;
   if (!equal && (p->col_offsets == nullptr || !is_aligned(p->col_offsets, 4))) return TBE_ERR_INVALID_ARG;
   a->rows = p->rows;
   a->x_stride = p->x_stride;

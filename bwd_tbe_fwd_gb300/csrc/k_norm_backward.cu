@@ -36,19 +36,6 @@ struct RowIn {
   void* dx;
 };
 
-template <int L, int T>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* part) {
-  if constexpr (L <= 32) {
-    return make_float2(lanes_sum<L>(v.x), lanes_sum<L>(v.y));
-  } else {
-    v = make_float2(lanes_sum<32>(v.x), lanes_sum<32>(v.y));
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    const float2 p = threadIdx.x % 32 < T / 32 ? part[threadIdx.x % 32] : make_float2(0.f, 0.f);
-    return make_float2(lanes_sum<32>(p.x), lanes_sum<32>(p.y));
-  }
-}
-
 template <typename X, typename Y, int V, int L, int T>
 __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g, const SumsOut& out, int64_t slot, int seg,
                                               int col0, int width, const RowWalk& walk, char* smem) {
@@ -61,8 +48,8 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
   RowReader<X, V, L, T> x(g.x, a.x_stride, col0, width, walk.first, walk.step, smem);
   RowReader<Y, V, L, T> dy(g.dy, a.y_stride, col0, width, walk.first, walk.step, smem + kStages * stage_bytes<X, V>(T));
   for (int k = 0; k < kStages - 1; ++k) {
-    x.copy(k, walk.first + k * walk.step < walk.end, in);
-    dy.copy(k, walk.first + k * walk.step < walk.end, in);
+    x.copy(k, k < walk.mine, in);
+    dy.copy(k, k < walk.mine, in);
     async_commit();
   }
   F2 w[kPer / 2], dw[kPer / 2], db[kPer / 2];
@@ -71,31 +58,36 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
   for (int i = 0; i < kPer / 2; ++i) dw[i] = db[i] = F2(0.f);
   const float inv_n = 1.f / static_cast<float>(width);
   float mu = 0.f, rs = 0.f;  // of the row to come
-  if (walk.first < walk.end) {
-    mu = g.mean[walk.first * a.segments + seg];
-    rs = g.rstd[walk.first * a.segments + seg];
+  const int64_t stat_step = walk.step * a.segments;
+  const float* mean = g.mean + walk.first * a.segments + seg;
+  const float* rstd = g.rstd + walk.first * a.segments + seg;
+  if (walk.mine > 0) {
+    mu = *mean;
+    rs = *rstd;
   }
   int stage = 0;
-  int64_t r = walk.first;
-  X* dx = static_cast<X*>(g.dx) + r * a.dx_stride + col0 + lane * V;
-  for (int64_t k = 0; k < walk.count; ++k, r += walk.step, dx += walk.step * a.dx_stride) {
-    const bool more = r + (kStages - 1) * walk.step < walk.end;
+  X* dx = static_cast<X*>(g.dx) + walk.first * a.dx_stride + col0 + lane * V;
+  const int64_t dx_step = walk.step * a.dx_stride;
+  for (int k = 0; k < walk.count; ++k, dx += dx_step) {
+    const bool more = k + kStages - 1 < walk.mine;
     x.reuse();
     x.copy(stage == 0 ? kStages - 1 : stage - 1, more, in);
     dy.copy(stage == 0 ? kStages - 1 : stage - 1, more, in);
     async_commit();
     async_wait<kStages - 1>();
     x.share();
-    const bool valid = r < walk.end;
+    const bool valid = k < walk.mine;
     F2 xh[kPer / 2], h[kPer / 2];
     x.read(stage, valid, in, xh);
     dy.read(stage, valid, in, h);
     stage = stage == kStages - 1 ? 0 : stage + 1;
     const float q = valid ? rs : 0.f;
     const F2 shift(valid ? -mu : 0.f), scale(q);
-    if (r + walk.step < walk.end) {
-      mu = g.mean[(r + walk.step) * a.segments + seg];
-      rs = g.rstd[(r + walk.step) * a.segments + seg];
+    if (k + 1 < walk.mine) {
+      mean += stat_step;
+      rstd += stat_step;
+      mu = *mean;
+      rs = *rstd;
     }
     F2 s1(0.f), s2(0.f);
 #pragma unroll
@@ -173,7 +165,7 @@ __global__ void __launch_bounds__(kGroupThreads, 4)
   segment_span<V>(a, seg, &col0, &width);
   auto go = [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const RowWalk walk{row0 + threadIdx.x / L, T / L, row1, (row1 - row0 + T / L - 1) / (T / L)};
+    const RowWalk walk(row0 + threadIdx.x / L, T / L, row0, row1);
     backward_rows<X, Y, V, L, T>(a, g, out, slot, seg, col0, width, walk, smem);
   };
   if (width <= row_capacity(4)) go(std::integral_constant<int, 4>());
@@ -192,7 +184,7 @@ __global__ void __launch_bounds__(T, 512 / T)
   const int64_t slot = blockIdx.x / a.segments;
   int col0, width;
   segment_span<V>(a, seg, &col0, &width);
-  const RowWalk walk{slot, out.slots, a.rows, (a.rows - slot + out.slots - 1) / out.slots};
+  const RowWalk walk(slot, out.slots, slot, a.rows);
   backward_rows<X, Y, V, T, T>(a, g, out, slot, seg, col0, width, walk, smem);
 }
 
@@ -301,11 +293,12 @@ __global__ void __launch_bounds__(kLongThreads)
 __global__ void __launch_bounds__(1024)
     norm_sum_slots_kernel(const float* partial, int64_t slots, int cols, int wtype, void* dweight, void* dbias) {
   __shared__ float sums[2][32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the kernel before it ends
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float dw = 0.f, db = 0.f;
   if (c < cols) {
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t s = warp; s < slots; s += 32) {
       dw += partial[s * cols + c];
       db += partial[(slots + s) * cols + c];
@@ -410,9 +403,18 @@ tbe_status launch_norm_backward(const NormArgs& a, int xtype, int ytype, int vec
     });
   });
   if (st != TBE_OK || out.partial == nullptr) return st;
-  norm_sum_slots_kernel<<<(a.cols + 31) / 32, 1024, 0, s>>>(partial, out.slots, a.cols, a.wtype, dweight, dbias);
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3((a.cols + 31) / 32);
+  config.blockDim = dim3(1024);
+  config.stream = s;
+  config.attrs = &early;
+  config.numAttrs = 1;
   note_launch();
-  return cuda_status(cudaGetLastError());
+  return cuda_status(cudaLaunchKernelEx(&config, norm_sum_slots_kernel, static_cast<const float*>(partial), out.slots, a.cols,
+                                        a.wtype, dweight, dbias));
 }
 
 }  // namespace tbe

@@ -28,7 +28,7 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
   for (int j = 0; j < J; ++j) in[j] = (j * L + lane) * V < width;
   RowReader<X, V, L, T> x(g.x, a.x_stride, col0, width, walk.first, walk.step, smem);
   for (int k = 0; k < kStages - 1; ++k) {
-    x.copy(k, walk.first + k * walk.step < walk.end, in);
+    x.copy(k, k < walk.mine, in);
     async_commit();
   }
   F2 w[kPer / 2], b[kPer / 2];
@@ -37,15 +37,17 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
   read_weights<V, L>(g.bias, a.wtype, first_col, in, 0.f, b);
   const float inv_n = 1.f / static_cast<float>(width);
   int stage = 0;
-  int64_t r = walk.first;
+  const int64_t r = walk.first;
   Y* y = static_cast<Y*>(g.y) + r * a.y_stride + col0 + lane * V;
-  for (int64_t k = 0; k < walk.count; ++k, r += walk.step, y += walk.step * a.y_stride) {
+  const int64_t y_step = walk.step * a.y_stride, stat_step = walk.step * a.segments;
+  int64_t stat = r * a.segments + seg;
+  for (int k = 0; k < walk.count; ++k, y += y_step, stat += stat_step) {
     x.reuse();
-    x.copy(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * walk.step < walk.end, in);
+    x.copy(stage == 0 ? kStages - 1 : stage - 1, k + kStages - 1 < walk.mine, in);
     async_commit();
     async_wait<kStages - 1>();
     x.share();
-    const bool valid = r < walk.end;
+    const bool valid = k < walk.mine;
     F2 f[kPer / 2];
     x.read(stage, valid, in, f);
     stage = stage == kStages - 1 ? 0 : stage + 1;
@@ -66,8 +68,8 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
     for (int i = 0; i < kPer / 2; ++i) f[i] = fma2(f[i] * F2(rs), w[i], b[i]);
     write_row<Y, V, L>(y, in, f);
     if (g.mean != nullptr && lane == 0) {
-      g.mean[r * a.segments + seg] = mu;
-      g.rstd[r * a.segments + seg] = rs;
+      g.mean[stat] = mu;
+      g.rstd[stat] = rs;
     }
   }
 }
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(kGroupThreads, 6)
   segment_span<V>(a, seg, &col0, &width);
   auto go = [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const RowWalk walk{row0 + threadIdx.x / L, T / L, row1, (row1 - row0 + T / L - 1) / (T / L)};
+    const RowWalk walk(row0 + threadIdx.x / L, T / L, row0, row1);
     forward_rows<X, Y, V, L, T>(a, g, seg, col0, width, walk, smem);
   };
   if (width <= row_capacity(4)) go(std::integral_constant<int, 4>());
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(T, T <= 256 ? 768 / T : 1)
   const int64_t slot = blockIdx.x / a.segments;
   int col0, width;
   segment_span<V>(a, seg, &col0, &width);
-  const RowWalk walk{slot, slots, a.rows, (a.rows - slot + slots - 1) / slots};
+  const RowWalk walk(slot, slots, slot, a.rows);
   forward_rows<X, Y, V, T, T>(a, g, seg, col0, width, walk, smem);
 }
 

@@ -181,10 +181,14 @@ __device__ __forceinline__ void write_row(E* p, const bool (&in)[kPer / V], cons
     }
 }
 
-// The rows of a thread: `first`, then every `step`th below `end`, `count` of them for every thread of the CTA.
+// The rows of a thread: `first`, then every `step`th, `mine` of them; the CTA's threads all go round `count` times.  (A
+// matrix of fewer than 2^39 elements has no more rows to a thread than 31 bits count.)
 struct RowWalk {
-  int64_t first, step, end;
-  int64_t count;
+  int64_t first, step;
+  int count, mine;
+  __device__ __forceinline__ RowWalk(int64_t first_, int64_t step_, int64_t begin, int64_t end)
+      : first(first_), step(step_), count(static_cast<int>((end - begin + step_ - 1) / step_)),
+        mine(first_ < end ? static_cast<int>((end - first_ + step_ - 1) / step_) : 0) {}
 };
 
 // Sum over the L threads that share a row.  `part`: shared memory of T / 32 floats that no other sum uses until
@@ -197,8 +201,36 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
     v = lanes_sum<32>(v);
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
-    return lanes_sum<32>(threadIdx.x % 32 < T / 32 ? part[threadIdx.x % 32] : 0.f);
+    return lanes_sum<T / 32>(part[threadIdx.x % (T / 32)]);
   }
+}
+
+// Two sums at once, x by one half of the lanes and y by the other: half the shuffles.  `part`: T / 32 pairs.
+template <int L>
+__device__ __forceinline__ float lanes_sum_halves(float x, float y) {
+  const bool upper = threadIdx.x % L >= L / 2;
+  const float mine = upper ? y : x, other = upper ? x : y;
+  return lanes_sum<L / 2>(mine + __shfl_xor_sync(kFull, other, L / 2));
+}
+template <int L, int T>
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* part) {
+  constexpr int N = L <= 32 ? L : 32;
+  float s = lanes_sum_halves<N>(v.x, v.y);
+  if constexpr (L > 32) {
+    constexpr int W = T / 32;
+    const int lane = threadIdx.x % 32;
+    if (lane % 16 == 0) reinterpret_cast<float*>(part)[threadIdx.x / 32 * 2 + lane / 16] = s;
+    __syncthreads();
+    if constexpr (W <= 16) {
+      s = lanes_sum<W>(reinterpret_cast<const float*>(part)[lane % W * 2 + lane / 16]);
+    } else {
+      const float2 p = part[lane];
+      s = lanes_sum_halves<32>(p.x, p.y);
+    }
+  }
+  const float t = __shfl_xor_sync(kFull, s, N / 2);
+  const bool upper = threadIdx.x % N >= N / 2;
+  return upper ? make_float2(t, s) : make_float2(s, t);
 }
 
 }  // namespace tbe

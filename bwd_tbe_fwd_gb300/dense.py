@@ -129,7 +129,7 @@ class LayerNorm:
         for w in self.widths:
             offsets.append(offsets[-1] + w)
         self.col_offsets = torch.tensor(offsets, dtype=torch.int32, device=self.device)
-        self.prob = NormProblem(1 << 30, len(self.widths), self._widths, self.col_offsets.data_ptr(), self.cols, self.cols,
+        self.prob = NormProblem(((1 << 39) - 1) // max(1, self.cols), len(self.widths), self._widths, self.col_offsets.data_ptr(), self.cols, self.cols,
                                 self.cols, _WDTYPE[self.x_dtype], _WDTYPE[self.y_dtype], _WDTYPE[weight_dtype], eps)
         self._prob = ctypes.byref(self.prob)
         with torch.cuda.device(self.device):  # the most that any number of rows takes
