@@ -137,6 +137,7 @@ class LayerNorm:
         if n == 0:
             raise TBEError("tbe_layer_norm_backward_workspace_size rejected the problem")
         self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self._ws, self._ws_bytes = self.ws.data_ptr(), n
 
     def _rows(self, t, name, dtype, rows=None):
         """Row stride of a [rows, cols] matrix."""
@@ -167,14 +168,20 @@ class LayerNorm:
         p.rows = rows = x.shape[0]
         if y is None:
             y = _empty((rows, self.cols), self.y_dtype, self.device, stream)
-        p.y_stride = self._rows(y, "y", self.y_dtype, rows)
+            p.y_stride = self.cols
+        else:
+            p.y_stride = self._rows(y, "y", self.y_dtype, rows)
         if (mean is None) != (rstd is None):
             raise ValueError("mean and rstd are given together")
         if mean is None:
-            mean, rstd = _empty((2, rows, len(self.widths)), torch.float32, self.device, stream).unbind(0)
+            mean = _empty((rows, len(self.widths)), torch.float32, self.device, stream)
+            rstd = _empty((rows, len(self.widths)), torch.float32, self.device, stream)
+            stats = mean.data_ptr(), rstd.data_ptr()
+        else:
+            stats = self._stat(mean, "mean", rows), self._stat(rstd, "rstd", rows)
         _launch(self.device, self.lib.tbe_layer_norm_forward,
-                (self._prob, x.data_ptr(), self._param(weight, "weight"), self._param(bias, "bias"), y.data_ptr(),
-                 self._stat(mean, "mean", rows), self._stat(rstd, "rstd", rows)), stream, "tbe_layer_norm_forward")
+                (self._prob, x.data_ptr(), self._param(weight, "weight"), self._param(bias, "bias"), y.data_ptr(), *stats),
+                stream, "tbe_layer_norm_forward")
         return y, mean, rstd
 
     def backward(self, dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, stream=None):
@@ -185,7 +192,9 @@ class LayerNorm:
         p.y_stride = self._rows(dy, "dy", self.y_dtype, rows)
         if dx is None:
             dx = _empty((rows, self.cols), self.x_dtype, self.device, stream)
-        p.dx_stride = self._rows(dx, "dx", self.x_dtype, rows)
+            p.dx_stride = self.cols
+        else:
+            p.dx_stride = self._rows(dx, "dx", self.x_dtype, rows)
         if dweight is None:
             dweight = _empty(self.cols, self.weight_dtype, self.device, stream)
         if dbias is None:
@@ -193,7 +202,7 @@ class LayerNorm:
         _launch(self.device, self.lib.tbe_layer_norm_backward,
                 (self._prob, dy.data_ptr(), x.data_ptr(), self._stat(mean, "mean", rows), self._stat(rstd, "rstd", rows),
                  self._param(weight, "weight"), dx.data_ptr(), self._param(dweight, "dweight"),
-                 self._param(dbias, "dbias"), self.ws.data_ptr(), self.ws.numel()), stream, "tbe_layer_norm_backward")
+                 self._param(dbias, "dbias"), self._ws, self._ws_bytes), stream, "tbe_layer_norm_backward")
         return dx, dweight, dbias
 
 
