@@ -771,7 +771,7 @@ tbe_status tbe_grad_norm(int32_t count, const void* const* grads, const int64_t*
   return with_type(dtype, [&](auto tag) {
     using G = typename decltype(tag)::type;
     return for_lists<NormEntry, kLargeNorm>(
-        count, chunk_elems(total, dev, 4), [&](int i) { return numels[i]; },
+        count, chunk_elems(total, dev, 16), [&](int i) { return numels[i]; },
         [&](int i, NormEntry* e) { *e = NormEntry{grads[i], numels[i]}; },
         [&](auto& list, bool first, bool last) {
           constexpr int CAP = static_cast<int>(sizeof(list.e) / sizeof(list.e[0]));
@@ -840,7 +840,7 @@ tbe_status tbe_adamw_state_values(const tbe_adamw_problem* prob, float* const* e
   if ((st = device_info(&dev)) != TBE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return for_lists<ValuesEntry, kLargeValues>(
-      prob->count, chunk_elems(total, dev, 4), [&](int i) { return prob->tensors[i].numel; },
+      prob->count, kStep, [&](int i) { return prob->tensors[i].numel; },
       [&](int i, ValuesEntry* e) {
         const tbe_dense_tensor& d = prob->tensors[i];
         float* m = exp_avg_values != nullptr ? exp_avg_values[i] : nullptr;
