@@ -120,6 +120,62 @@ def test_norm_misaligned_base():
             within(v, t, b, "misaligned")
 
 
+@pytest.mark.parametrize("width", [3, 37, 300, 1001, 3001])
+@pytest.mark.parametrize("offset", [1, 5, 7])
+def test_norm_odd_rows_from_anywhere(width, offset):
+    """Rows of an odd width that start at any element of a buffer: nothing around them is read into them or written."""
+    rows, g = 29, gen(width + offset)
+    n = rows * width
+    buf = torch.full((n + 64,), math.nan).half()
+    buf[offset:offset + n] = torch.randn(n, generator=g).half()
+    x = buf.cuda()[offset:offset + n].view(rows, width)
+    out = torch.full((n + 64,), 7.0).half().cuda()
+    ln = LayerNorm([width], torch.float16)
+    y, mean, rstd = ln.forward(x, y=out[offset:offset + n].view(rows, width))
+    want, bound = ref.layer_norm(host(x), [width], None, None, float(np.float32(1e-5)), "f16")
+    for got, v, b in zip((y, mean, rstd), want, bound):
+        within(got, v, b, "odd rows")
+    dx, dw, db = ln.backward(x, x, mean, rstd)
+    want, bound = ref.layer_norm_gradients(host(x), host(x), host(mean), host(rstd), [width], None, "f16")
+    for got, v, b in zip((dx, dw, db), want, bound):
+        within(got, v, b, "odd rows' gradients")
+    assert bool((out[:offset] == 7).all()) and bool((out[offset + n:] == 7).all())
+
+
+@pytest.mark.parametrize("width", [37, 64, 1000, 3001, 9000])
+def test_norm_results_left_out(width):
+    """The C interface's NULLs: no statistics, no dx, no dweight, no dbias; the others are the same bits."""
+    s = norm_inputs(300, [width], "f32", "f32")
+    ln = LayerNorm([width])
+    y, mean, rstd = ln.forward(s["x"], s["weight"], s["bias"])
+    dx, dw, db = ln.backward(s["dy"], s["x"], mean, rstd, s["weight"])
+    y2 = torch.empty_like(y)
+    stream = torch.cuda.current_stream().cuda_stream
+    p = lambda v: None if v is None else v.data_ptr()  # noqa: E731
+    assert ln.lib.tbe_layer_norm_forward(ln._prob, p(s["x"]), p(s["weight"]), p(s["bias"]), p(y2), None, None, stream) == 0
+    assert torch.equal(y, y2)
+    for keep in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (0, 1, 1), (1, 1, 0)):
+        out = [torch.full_like(v, 3.0) if k else None for v, k in zip((dx, dw, db), keep)]
+        assert ln.lib.tbe_layer_norm_backward(ln._prob, p(s["dy"]), p(s["x"]), p(mean), p(rstd), p(s["weight"]), p(out[0]),
+                                              p(out[1]), p(out[2]), p(ln.ws), ln.ws.numel(), stream) == 0
+        for got, want in zip(out, (dx, dw, db)):
+            assert got is None or torch.equal(got, want)
+
+
+@pytest.mark.parametrize("offsets", [[0, 1 << 30, -5, 96], [90, 10, 5, 0], [1, 3, 95, 97], [0, 96, 96, 96]])
+def test_norm_column_offsets_that_disagree_stay_in_the_row(offsets):
+    """col_offsets that are not the widths' (a caller's mistake): unspecified values, but nothing outside the row."""
+    ln = LayerNorm([32, 60, 4])
+    ln.col_offsets.copy_(torch.tensor(offsets, dtype=torch.int32))
+    wide = torch.randn(50, 128, device="cuda")
+    y = torch.full((50, 128), 7.0, device="cuda")
+    _, mean, rstd = ln.forward(wide[:, 16:112], y=y[:, 16:112])
+    assert bool((y[:, :16] == 7).all()) and bool((y[:, 112:] == 7).all())
+    dx = torch.full((50, 128), 7.0, device="cuda")
+    ln.backward(wide[:, 16:112], wide[:, 16:112], mean, rstd, dx=dx[:, 16:112])
+    assert bool((dx[:, :16] == 7).all()) and bool((dx[:, 112:] == 7).all())
+
+
 def test_norm_large_offset_and_constant_rows():
     # a mean 2^8 times the spread: the deviations are taken from the mean, not from E[x^2]
     check_norm(40, [256], shift=256.0, seed=3)
@@ -156,10 +212,12 @@ def test_norm_no_rows(width):
     assert bool((dw == 0).all()) and bool((db == 0).all())
 
 
-@pytest.mark.parametrize("width", [128, 2000, 12000, 20000])
-def test_norm_in_place(width):
-    s = norm_inputs(41, [width], "f32", "f32")
-    ln = LayerNorm([width])
+@pytest.mark.parametrize("width,dtype", [(128, "f32"), (2000, "f32"), (12000, "f32"), (20000, "f32"), (5, "f16"), (37, "f16"),
+                                         (257, "f32"), (1001, "f16"), (4097, "bf16")])
+def test_norm_in_place(width, dtype):
+    s = norm_inputs(741, [width], dtype, dtype)
+    ln = LayerNorm([width], DT[dtype], weight_dtype=torch.float32)
+    s["weight"], s["bias"] = s["weight"].float(), s["bias"].float()
     y, mean, rstd = ln.forward(s["x"], s["weight"], s["bias"])
     dx, dw, db = ln.backward(s["dy"], s["x"], mean, rstd, s["weight"])
     x = s["x"].clone()
