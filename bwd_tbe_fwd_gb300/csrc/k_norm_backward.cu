@@ -57,14 +57,16 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
 #pragma unroll
   for (int i = 0; i < kPer / 2; ++i) dw[i] = db[i] = F2(0.f);
   const float inv_n = 1.f / static_cast<float>(width);
-  float mu = 0.f, rs = 0.f;  // of the row to come
-  const int64_t stat_step = walk.step * a.segments;
-  const float* mean = g.mean + walk.first * a.segments + seg;
-  const float* rstd = g.rstd + walk.first * a.segments + seg;
-  if (walk.mine > 0) {
-    mu = *mean;
-    rs = *rstd;
-  }
+  // The rows' statistics, B rows to a load (a lane each) and a batch ahead; a row's come by shuffle.
+  constexpr int B = L < 32 ? L : 32;
+  const int64_t stat_step = walk.step * a.segments, stat0 = walk.first * a.segments + seg;
+  const int my_row = threadIdx.x % B;
+  auto stats = [&](int k0) {
+    const bool have = k0 + my_row < walk.mine;
+    const int64_t at = stat0 + (k0 + my_row) * stat_step;
+    return make_float2(have ? g.mean[at] : 0.f, have ? g.rstd[at] : 0.f);
+  };
+  float2 batch = stats(0), batch_ahead = stats(B);
   int stage = 0;
   X* dx = static_cast<X*>(g.dx) + walk.first * a.dx_stride + col0 + lane * V;
   const int64_t dx_step = walk.step * a.dx_stride;
@@ -81,13 +83,11 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
     x.read(stage, valid, in, xh);
     dy.read(stage, valid, in, h);
     stage = stage == kStages - 1 ? 0 : stage + 1;
-    const float q = valid ? rs : 0.f;
-    const F2 shift(valid ? -mu : 0.f), scale(q);
-    if (k + 1 < walk.mine) {
-      mean += stat_step;
-      rstd += stat_step;
-      mu = *mean;
-      rs = *rstd;
+    const float mu = __shfl_sync(kFull, batch.x, k % B, B), q = __shfl_sync(kFull, batch.y, k % B, B);  // 0 past the rows
+    const F2 shift(-mu), scale(q);
+    if (k % B == B - 1) {
+      batch = batch_ahead;
+      batch_ahead = stats(k + 1 + B);
     }
     F2 s1(0.f), s2(0.f);
 #pragma unroll
