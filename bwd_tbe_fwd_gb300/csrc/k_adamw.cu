@@ -1,9 +1,15 @@
 // k_adamw.cu -- one AdamW step of many tensors (tbe_adamw_update), the values of its 8-bit states
 // (tbe_adamw_state_values) and the global norm of many gradients (tbe_grad_norm).
 //
-// Each element is read and written once; all three are bound by DRAM.  A thread takes 8 consecutive
-// elements: 16 bytes of a 16-bit type, 32 of fp32, 8 of codes; a warp then takes one block of the 8-bit
-// states, whose scale needs one reduction over the warp and no shared memory.
+// Each element is read and written once.  A thread takes 8 consecutive elements: 16 bytes of a 16-bit type, 32
+// of fp32, 8 of codes; a warp then takes one block of the 8-bit states, whose scale needs one reduction over the
+// warp and no shared memory.
+//
+// Measured on a GB300 (copy rate 6.78 TB/s): 32-bit states are bound by DRAM (227M bf16 parameters with masters,
+// 28 bytes an element: 935 us, 6.78 TB/s), so is the norm (227M bf16: 70 us, 6.4 TB/s) and, with a write
+// for every quarter byte read, the states' values (113M of each moment: 178 us, 6.4 TB/s).  The 8-bit step is bound by issue: 60
+// instructions an element for 10 bytes of traffic (113M bf16: 250 us, 4.5 TB/s), of which decoding takes 15, the step 15, scaling
+// and encoding 20.
 #include <algorithm>
 #include <cmath>
 
@@ -443,12 +449,12 @@ struct Q8Ragged {
 };
 
 // A CTA takes a contiguous share of the chunks (of one pass, a block to a warp), so that the table and the factors
-// are made once for it.  Whole blocks of a tensor go by running pointers and are copied into shared memory
-// kQ8Stages - 1 blocks ahead, each lane's part to its own place (loads into registers waited for by the table's
-// and the reductions' results too: 280 us instead of what async copies take, for 113M bf16 parameters); what is
-// ragged or not aligned is loaded element by element.
-constexpr int kQ8Ahead = 1;
-constexpr int kQ8Resident = 5;  // CTAs to an SM
+// are made once for it (every gridDim-th chunk instead: 312 us, for 113M bf16 parameters, against 250).  Whole blocks of a
+// tensor go by running pointers, the next one asked for in L2 while this one's codes are computed (without that 295;
+// loaded into registers instead 280, into shared memory 294: their waits or traffic meet the table's); what is ragged or
+// not aligned is loaded element by element.
+constexpr int kQ8Ahead = 1;     // passes (2: 266 us)
+constexpr int kQ8Resident = 5;  // CTAs to an SM (3: 277 us, 4: 263, 5: 250 in spite of a few spilled registers)
 
 template <typename P, typename G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads, kQ8Resident)
@@ -616,6 +622,8 @@ __global__ void __launch_bounds__(kThreads, kNormResident)
 // Host
 // ------------------------------------------------------------------------------------------
 // Elements of a chunk: up to `most` passes of a CTA (a power of two), fewer while that leaves less than 16 chunks to an SM.
+// AdamW with 32-bit states takes 4 (935 us at 227M; 1: 1050), the norm 16 (70 us; 4: 74), the values 1 (178 us; 4: 200,
+// 16: 228: two streams in and two out like a narrow band).
 uint32_t chunk_elems(int64_t total, const DeviceInfo& dev, int most) {
   int passes = 1;
   while (passes < most && total / (2 * passes * kStep) >= 16 * static_cast<int64_t>(dev.sms)) passes *= 2;

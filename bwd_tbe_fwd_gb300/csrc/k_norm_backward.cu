@@ -4,6 +4,12 @@
 // One pass reads x and dy once, writes dx and keeps each column's sums of dy * xhat and dy in registers
 // over the rows that a CTA takes (its slot); the slots' sums meet in a second kernel, in a fixed
 // order.  The bound is DRAM; the partial rows add 16 bytes a column and slot to it.
+//
+// Measured on a GB300 (copy rate 6.78 TB/s): 8192 rows of 26 tables of 128, fp32 with bf16 dy, 43.9 us and 2.9 us for the slots'
+// sums, 6.2 TB/s while the rows last; 16384 rows of 4096 bf16 69 + 4 us, 5.8 TB/s: there the latency of a row's two sums
+// shows, as the columns' sums (32 registers a thread, with x, dy and the weight 117) leave 16 warps to an SM.  Reading
+// the row a second time from shared memory for a third CTA an SM was slower (90 us), as were 2, 4 or 6 stages (75 to 76
+// before the statistics came by shuffle).
 #include "norm_rows.cuh"
 
 namespace tbe {
