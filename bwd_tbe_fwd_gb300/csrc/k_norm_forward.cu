@@ -39,6 +39,11 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
   const int first_col = in[0] ? col0 + lane * V : col0;
   read_weights<V, L>(g.weight, a.wtype, first_col, in, 1.f, w);
   read_weights<V, L>(g.bias, a.wtype, first_col, in, 0.f, b);
+  F2 part_of[V == 1 ? kPer / 2 : 1];  // V = 1: -1 for the row's elements, 0 past its end
+  if constexpr (V == 1) {
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) part_of[i] = F2(in[2 * i] ? -1.f : 0.f, in[2 * i + 1] ? -1.f : 0.f);
+  }
   const float inv_n = 1.f / static_cast<float>(width);
   int stage = 0;
   const int64_t r = walk.first;
@@ -62,9 +67,13 @@ __device__ __forceinline__ void forward_rows(const NormArgs& a, const ForwardArg
     s = F2(0.f);
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) {
-      const bool in0 = in[2 * i / V], in1 = in[(2 * i + 1) / V];
-      f[i] = f[i] + F2(V > 1 || in0 ? -mu : 0.f, V > 1 || in1 ? -mu : 0.f);
-      if (V == 1 || in0) s = fma2(f[i], f[i], s);
+      if constexpr (V == 1) {
+        f[i] = fma2(part_of[i], F2(mu), f[i]);
+        s = fma2(f[i], f[i], s);
+      } else {
+        f[i] = f[i] + F2(-mu);
+        if (in[2 * i / V]) s = fma2(f[i], f[i], s);
+      }
     }
     const float rs = __frsqrt_rn(fmaf(row_sum<L, T>(s.lo() + s.hi(), part[1]), inv_n, a.eps));
     if (!valid) continue;

@@ -79,55 +79,67 @@ struct RowReader {
 };
 
 // V = 1: rows that start anywhere.  The 16-byte pieces that a row lies in are copied by the threads that share
-// it, whichever element they hold; a piece's bytes past the row's end are not read, those before its start belong to
-// rows before it (or to the gap between them); a piece that begins before the matrix is loaded element by element.
+// it, whichever element they hold; a piece's bytes past the row's end are not read but filled with zeros, and so is the
+// rest of the row's region, so that every thread reads 16 elements without asking which of them exist (the
+// questions were a third of the instructions).  Bytes before a row's start belong to rows before it (or to the gap between
+// them); a piece that begins before the matrix is loaded element by element.
 template <typename E, int L, int T>
 struct RowReader<E, 1, L, T> {
   static constexpr int J = kPer;
   static constexpr int kRegion = kPer * L * static_cast<int>(sizeof(E)) + 32;  // of a row in a stage
   const char* base;    // the segment's first byte in row 0
-  int64_t row, row_step;
-  int64_t pitch;       // bytes from a row to the next
+  const char* start;   // ... in the next row to copy
+  int64_t step;        // bytes from one of the thread's rows to the next
   int bytes;           // of the segment
   uint32_t place;      // shared memory: the row's region of stage 0
 
-  __device__ __forceinline__ RowReader(const void* p, int64_t stride, int col, int width, int64_t first_row, int64_t row_step_,
+  __device__ __forceinline__ RowReader(const void* p, int64_t stride, int col, int width, int64_t first_row, int64_t row_step,
                                        char* smem)
-      : base(reinterpret_cast<const char*>(static_cast<const E*>(p) + col)), row(first_row), row_step(row_step_),
-        pitch(stride * static_cast<int64_t>(sizeof(E))), bytes(width * static_cast<int>(sizeof(E))),
-        place(smem_u32(smem) + threadIdx.x / L * kRegion) {}
+      : base(reinterpret_cast<const char*>(static_cast<const E*>(p) + col)),
+        start(base + first_row * stride * static_cast<int64_t>(sizeof(E))), step(row_step * stride * static_cast<int64_t>(sizeof(E))),
+        bytes(width * static_cast<int>(sizeof(E))), place(smem_u32(smem) + threadIdx.x / L * kRegion) {
+    for (int s = 0; s < kStages; ++s)
+      for (int at = threadIdx.x % L * 16; at < kRegion; at += L * 16)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(place + s * stage_bytes<E, 1>(T) + at), "r"(0) : "memory");
+    share();
+  }
+
+  static __device__ __forceinline__ void put(uint32_t at, const char* from, bool have) {
+    if constexpr (sizeof(E) == 2) {
+      const uint16_t v = have ? *reinterpret_cast<const uint16_t*>(from) : 0;
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(v) : "memory");
+    } else {
+      const uint32_t v = have ? *reinterpret_cast<const uint32_t*>(from) : 0;
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+    }
+  }
 
   __device__ __forceinline__ void copy(int stage, bool valid, const bool (&)[J]) {
     if (valid) {
-      const char* start = base + row * pitch;
       const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(start) % 16);
       const uint32_t dst = place + stage * stage_bytes<E, 1>(T);
-      for (int at = threadIdx.x % L * 16; at < skew + bytes; at += L * 16) {
+      // as many pieces as any start may need: those that this one does not are zeros
+      for (int at = threadIdx.x % L * 16; at < bytes + 15; at += L * 16) {
         if (at == 0 && start - skew < base) {
-          for (int k = 0; k < 16 - skew && k < bytes; k += static_cast<int>(sizeof(E))) {
-            if constexpr (sizeof(E) == 2)
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + skew + k), "h"(*reinterpret_cast<const uint16_t*>(start + k)) : "memory");
-            else
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + skew + k), "r"(*reinterpret_cast<const uint32_t*>(start + k)) : "memory");
-          }
+          for (int k = 0; k < 16 - skew; k += static_cast<int>(sizeof(E))) put(dst + skew + k, start + k, k < bytes);
         } else {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + at), "l"(start - skew + at),
-                       "r"(min(16, skew + bytes - at)) : "memory");
+          const int n = max(min(16, skew + bytes - at), 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + at), "l"(n > 0 ? start - skew + at : start - skew),
+                       "r"(n) : "memory");
         }
       }
     }
-    row += row_step;
+    start += step;
   }
 
-  __device__ __forceinline__ void read(int stage, bool valid, const bool (&in)[J], F2 (&f)[kPer / 2]) const {
+  __device__ __forceinline__ void read(int stage, bool valid, const bool (&)[J], F2 (&f)[kPer / 2]) const {
     // the row in the stage is kStages rows behind the next one to copy
-    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(base + (row - kStages * row_step) * pitch) % 16);
+    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(start - kStages * step) % 16);
     const uint32_t src = place + stage * stage_bytes<E, 1>(T) + skew + threadIdx.x % L * static_cast<int>(sizeof(E));
     Pack<E, 1> v[J];
+    if (valid) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      v[j].zero();
-      if (valid && in[j]) {
+      for (int j = 0; j < J; ++j) {
         if constexpr (sizeof(E) == 2) {
           uint16_t h;
           asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(src + j * L * 2) : "memory");
@@ -136,6 +148,9 @@ struct RowReader<E, 1, L, T> {
           shared_words<4>(src + j * L * 4, v[j].w);
         }
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j) v[j].zero();
     }
 #pragma unroll
     for (int k = 0; k < kPer / 2; ++k) f[k] = F2(v[2 * k].get(0), v[2 * k + 1].get(0));

@@ -4,8 +4,8 @@ output, the global norm of many gradients, and one AdamW step of many tensors.
 As in ``tbe.py``, argument marshalling only: torch supplies device memory and the current stream,
 every step runs in the CUDA library, and there is nothing to fall back on.  The three classes hold
 what a program sets up once (descriptions, workspaces); a call checks its tensors and launches.  An
-object's own workspace is used by its calls in order: calls of one object must not overlap on
-different streams.
+object is ready for any stream when its constructor returns.  Its workspace is used by its calls in
+order: calls of one object must not overlap on different streams or host threads.
 """
 from __future__ import annotations
 
@@ -71,21 +71,40 @@ def _device(device) -> torch.device:
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _launch(device, fn, args, stream, what):
-    """Calls the library with `device` current, on `stream` (default: the device's current one)."""
+def _raw_stream(stream, device):
+    """The cudaStream_t of `stream`, or of the device's current one when None."""
     if stream is not None:
-        s = stream.cuda_stream
-    elif _current_raw_stream is not None and device.type == "cuda":
-        s = _current_raw_stream(device.index)
-    else:
-        s = torch.cuda.current_stream(device).cuda_stream
-    if device.type == "cuda" and torch.cuda.current_device() == device.index:
-        status = fn(*args, s)
-    else:
-        with torch.cuda.device(device):
+        return stream.cuda_stream
+    if _current_raw_stream is not None and device.type == "cuda":
+        return _current_raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+class _Handle:
+    """What the three classes share: the device, memory of their own, and the launch of an entry point."""
+
+    def _own(self, *tensors):
+        """Memory that the object's kernels use: complete when the constructor returns, and kept from reuse
+        while a call on another stream than the constructor's may be at work on it."""
+        self._kept = tensors
+        self._home = _raw_stream(None, self.device)
+        if self.device.type == "cuda":
+            torch.cuda.current_stream(self.device).synchronize()
+
+    def _launch(self, fn, args, stream, what):
+        """Calls the library with the device current, on `stream` (default: the device's current one)."""
+        device = self.device
+        s = _raw_stream(stream, device)
+        if s != self._home and device.type == "cuda":
+            for t in self._kept:
+                t.record_stream(stream or torch.cuda.current_stream(device))
+        if device.type == "cuda" and torch.cuda.current_device() == device.index:
             status = fn(*args, s)
-    if status != TBE_OK:
-        _check(load(), status, what)
+        else:
+            with torch.cuda.device(device):
+                status = fn(*args, s)
+        if status != TBE_OK:
+            _check(load(), status, what)
 
 
 def _empty(shape, dtype, device, stream):
@@ -107,7 +126,7 @@ def _flat(t, name, dtype, numel, device):
     return t.data_ptr()
 
 
-class LayerNorm:
+class LayerNorm(_Handle):
     """Layer norm of [rows, sum(widths)] matrices, each segment of ``widths[s]`` columns on its own: one
     segment is the ordinary layer norm; ``LayerNorm(tbe.D, ...)`` normalises every table's part of
     TableBatchedEmbedding.forward's output, and its dx is backward_update's grad_out.
@@ -138,6 +157,7 @@ class LayerNorm:
             raise TBEError("tbe_layer_norm_backward_workspace_size rejected the problem")
         self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
         self._ws, self._ws_bytes = self.ws.data_ptr(), n
+        self._own(self.col_offsets, self.ws)
 
     def _rows(self, t, name, dtype, rows=None):
         """Row stride of a [rows, cols] matrix."""
@@ -179,7 +199,7 @@ class LayerNorm:
             stats = mean.data_ptr(), rstd.data_ptr()
         else:
             stats = self._stat(mean, "mean", rows), self._stat(rstd, "rstd", rows)
-        _launch(self.device, self.lib.tbe_layer_norm_forward,
+        self._launch(self.lib.tbe_layer_norm_forward,
                 (self._prob, x.data_ptr(), self._param(weight, "weight"), self._param(bias, "bias"), y.data_ptr(), *stats),
                 stream, "tbe_layer_norm_forward")
         return y, mean, rstd
@@ -199,7 +219,7 @@ class LayerNorm:
             dweight = _empty(self.cols, self.weight_dtype, self.device, stream)
         if dbias is None:
             dbias = _empty(self.cols, self.weight_dtype, self.device, stream)
-        _launch(self.device, self.lib.tbe_layer_norm_backward,
+        self._launch(self.lib.tbe_layer_norm_backward,
                 (self._prob, dy.data_ptr(), x.data_ptr(), self._stat(mean, "mean", rows), self._stat(rstd, "rstd", rows),
                  self._param(weight, "weight"), dx.data_ptr(), self._param(dweight, "dweight"),
                  self._param(dbias, "dbias"), self._ws, self._ws_bytes), stream, "tbe_layer_norm_backward")
@@ -223,7 +243,7 @@ def _pointers(tensors):
     return (vp * max(1, len(tensors)))(*[t.data_ptr() for t in tensors])
 
 
-class GradNorm:
+class GradNorm(_Handle):
     """The norm of many gradients together and the coefficient that clips it, left on the device.  The
     gradients are those tensors' memory: refill it in place, or make a new object."""
 
@@ -235,19 +255,20 @@ class GradNorm:
         self._ptrs = _pointers(self.grads)
         self._numels = (c_i64 * max(1, len(self.grads)))(*[t.numel() for t in self.grads])
         self.ws = torch.zeros(self.lib.tbe_grad_norm_workspace_size(), dtype=torch.uint8, device=self.device)
+        self._own(self.ws)
 
     def compute(self, max_norm: float = math.inf, out=None, stream=None):
         """Returns out: float32 [2], the norm and min(1, max_norm / (norm + 1e-6))."""
         if out is None:
             out = _empty(2, torch.float32, self.device, stream)
-        _launch(self.device, self.lib.tbe_grad_norm,
+        self._launch(self.lib.tbe_grad_norm,
                 (len(self.grads), self._ptrs, self._numels, self._dtype, max_norm,
                  _flat(out, "out", torch.float32, 2, self.device), self.ws.data_ptr(), self.ws.numel()), stream,
                 "tbe_grad_norm")
         return out
 
 
-class DenseAdamW:
+class DenseAdamW(_Handle):
     """AdamW over many tensors at once.  ``params`` and ``grads`` are updated from and in their own memory
     (refill gradients in place, or call bind_grads).  ``states``: "f32", or "q8" for 8-bit states with
     a float32 scale for each 256 elements.  ``master``: None, or float32 tensors that hold 16-bit
@@ -268,11 +289,13 @@ class DenseAdamW:
         if self.master is not None and n and self.params[0].dtype == torch.float32:
             raise TypeError("float32 params take no master")
         state = dict(state or {})
+        made = []
 
         def held(key, dtype, sizes):
             got = state.pop(key, None)
             if got is None:
                 got = [torch.zeros(k, dtype=dtype, device=self.device) for k in sizes]
+                made.extend(got)
             got = list(got)
             self._same_count(got, key)
             for t, k in zip(got, sizes):
@@ -287,6 +310,7 @@ class DenseAdamW:
         self.steps = state.pop("step", None)
         if self.steps is None:
             self.steps = torch.zeros(1, dtype=torch.int64, device=self.device)
+            made.append(self.steps)
         _flat(self.steps, "step", torch.int64, 1, self.device)
         if state:
             raise TypeError(f"unknown state {sorted(state)}")
@@ -311,6 +335,7 @@ class DenseAdamW:
         self._prob = ctypes.byref(self.prob)
         self.bind_grads(grads)
         self.ws = torch.zeros(self.lib.tbe_adamw_workspace_size(), dtype=torch.uint8, device=self.device)
+        self._own(self.ws, *made)
 
     def _same_count(self, tensors, name):
         if len(tensors) != len(self.params):
@@ -335,7 +360,7 @@ class DenseAdamW:
 
     def step(self, lr: float, clip=None, stream=None):
         """One update.  clip: the result of GradNorm.compute (where its norm is not finite nothing changes)."""
-        _launch(self.device, self.lib.tbe_adamw_update,
+        self._launch(self.lib.tbe_adamw_update,
                 (self._prob, lr, None if clip is None else _flat(clip, "clip", torch.float32, 2, self.device),
                  self.steps.data_ptr(), self.ws.data_ptr(), self.ws.numel()), stream, "tbe_adamw_update")
 
@@ -353,6 +378,6 @@ class DenseAdamW:
                     _flat(t, name, torch.float32, n, self.device)  # says what is wrong
                 addresses.append(t.data_ptr())
             lists.append((given, (vp * max(1, len(given)))(*addresses)))
-        _launch(self.device, self.lib.tbe_adamw_state_values, (self._prob, lists[0][1], lists[1][1]), stream,
+        self._launch(self.lib.tbe_adamw_state_values, (self._prob, lists[0][1], lists[1][1]), stream,
                 "tbe_adamw_state_values")
         return lists[0][0], lists[1][0]

@@ -651,6 +651,27 @@ def test_adamw_step_and_norm_in_a_graph():
     assert all(torch.equal(a, b) for a, b in zip(s["params"], s2["params"])) and int(opt.steps) == 3
 
 
+def test_objects_made_and_used_on_different_streams():
+    """Made on one stream, used on another at once and dropped while the work may still run: the object's memory is
+    complete when the constructor returns and is not handed out again before the other stream is done."""
+    side = torch.cuda.Stream()
+    p, g = torch.zeros(1 << 20, device="cuda"), torch.ones(1 << 20, device="cuda")
+    x = torch.randn(1 << 14, 64, device="cuda")
+    want = LayerNorm([64]).forward(x)
+    grads = LayerNorm([64]).backward(x, x, want[1], want[2])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        opt = DenseAdamW([p], [g], "q8", weight_decay=0.0)
+        opt.step(1e-3, clip=GradNorm([g]).compute(stream=side), stream=side)
+        got = LayerNorm([64]).backward(x, x, want[1], want[2], stream=side)
+        steps = opt.steps
+        del opt
+        torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda")  # would land in freed memory
+        side.synchronize()
+        assert int(steps) == 1 and all(torch.equal(a, b) for a, b in zip(got, grads))
+    np.testing.assert_allclose(host(p), -5e-3, rtol=1e-5)
+
+
 def test_adamw_rebound_gradients():
     s = adam_inputs([100], "f32", "f32", False)
     opt = DenseAdamW(s["params"], s["grads"], weight_decay=0.0)
