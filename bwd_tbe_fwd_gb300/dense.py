@@ -9,6 +9,7 @@ order: calls of one object must not overlap on different streams or host threads
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 
@@ -282,6 +283,7 @@ class DenseAdamW(_Handle):
         self.params = _tensor_list(params, "params")
         n = len(self.params)
         self.device = self.params[0].device if n else _device(device)
+        self._index = -1 if self.device.index is None else self.device.index
         q8 = {"f32": False, "q8": True}[states]
         self.states = states
         self._numels = numels = [p.numel() for p in self.params]
@@ -367,17 +369,19 @@ class DenseAdamW(_Handle):
     def state_values(self, exp_avg=None, exp_avg_sq=None, stream=None):
         """What the 8-bit states stand for: two lists of float32 tensors (given ones are written)."""
         lists = []
-        index = -1 if self.device.index is None else self.device.index
+        T = torch.Tensor
         for given, name in ((exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq")):
             if given is None:
                 given = [_empty(n, torch.float32, self.device, stream) for n in self._numels]
             self._same_count(given, name)
-            addresses = []
-            for t, n in zip(given, self._numels):
-                if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
-                    _flat(t, name, torch.float32, n, self.device)  # says what is wrong
-                addresses.append(t.data_ptr())
-            lists.append((given, (vp * max(1, len(given)))(*addresses)))
-        self._launch(self.lib.tbe_adamw_state_values, (self._prob, lists[0][1], lists[1][1]), stream,
-                "tbe_adamw_state_values")
+            # all at once, and one by one only to say what is wrong
+            if given and not ([*map(T.numel, given)] == self._numels and all(map(T.is_contiguous, given))
+                              and {*map(T.get_device, given)} == {self._index}
+                              and {t.dtype for t in given} == {torch.float32}):
+                for t, n in zip(given, self._numels):
+                    _flat(t, name, torch.float32, n, self.device)
+            lists.append((given, array.array("Q", map(T.data_ptr, given))))
+        self._launch(self.lib.tbe_adamw_state_values,
+                     (self._prob, lists[0][1].buffer_info()[0], lists[1][1].buffer_info()[0]), stream,
+                     "tbe_adamw_state_values")
         return lists[0][0], lists[1][0]
