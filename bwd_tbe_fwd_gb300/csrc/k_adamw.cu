@@ -6,9 +6,9 @@
 // warp and no shared memory.
 //
 // Measured on a GB300 (copy rate 6.78 TB/s): 32-bit states are bound by DRAM (227M bf16 parameters with masters,
-// 28 bytes an element: 935 us, 6.78 TB/s), so is the norm (227M bf16: 70 us, 6.4 TB/s) and, with a write
+// 28 bytes an element: 923 us, 6.87 TB/s), so is the norm (227M bf16: 70 us, 6.4 TB/s) and, with a write
 // for every quarter byte read, the states' values (113M of each moment: 178 us, 6.4 TB/s).  The 8-bit step is bound by issue: 60
-// instructions an element for 10 bytes of traffic (113M bf16: 250 us, 4.5 TB/s), of which decoding takes 15, the step 15, scaling
+// instructions an element for 10 bytes of traffic (113M bf16: 248 us, 4.6 TB/s), of which decoding takes 15, the step 15, scaling
 // and encoding 20.
 #include <algorithm>
 #include <cmath>
@@ -97,26 +97,53 @@ __device__ __forceinline__ float bias_correction(float log_beta, int64_t t) {
   return -expm1f(static_cast<float>(t) * log_beta);
 }
 
-// False when the gradients' norm says that the step is to be left out.
-__device__ __forceinline__ bool adam_factors(const AdamScalars& s, AdamFactors* f) {
-  f->coef = 1.f;
-  if (s.clip != nullptr) {
-    if (!isfinite(s.clip[0])) return false;
-    f->coef = s.clip[1];
-  }
+// A CTA's start: one thread reads the step and the clip coefficient and makes the factors (while the others' first loads
+// are in flight), then takes a ticket; the last one to take one knows that every CTA has read the step, and advances it.
+struct AdamStart {
+  float coef, step_size, inv_sqrt_bc2;
+  bool go;  // false: the gradients' norm says that the step is to be left out
+  uint32_t place;
+  int64_t t;
+};
+
+// Before the CTA's barrier, thread 0 only.
+__device__ __forceinline__ void adam_begin(const AdamScalars& s, AdamStart& start) {
+  float norm = 0.f, coef = 1.f;
   const int64_t t = *s.step + 1;
-  f->beta1 = s.beta1, f->beta2 = s.beta2, f->omb1 = s.one_minus_beta1, f->omb2 = s.one_minus_beta2;
-  f->step_size = s.lr / bias_correction(s.log_beta1, t);
-  f->inv_sqrt_bc2 = __frsqrt_rn(bias_correction(s.log_beta2, t));
-  f->eps = s.eps;
-  f->lr = s.lr;
-  f->minus_zero = s.minus_zero;
-  return true;
+  if (s.clip != nullptr) {
+    norm = s.clip[0];
+    coef = s.clip[1];
+  }
+  start.coef = coef;
+  start.step_size = s.lr / bias_correction(s.log_beta1, t);
+  start.inv_sqrt_bc2 = __frsqrt_rn(bias_correction(s.log_beta2, t));
+  start.go = isfinite(norm);
+  start.t = t;
 }
 
-__device__ __forceinline__ void advance_step(const AdamScalars& s) {
-  // every CTA has read the step before the last one to arrive changes it
-  if (last_cta(s.ticket) && s.advance && threadIdx.x == 0) *s.step += 1;
+__device__ __forceinline__ AdamFactors adam_factors(const AdamScalars& s, const AdamStart& start) {
+  AdamFactors f;
+  f.coef = start.coef;
+  f.beta1 = s.beta1, f.beta2 = s.beta2, f.omb1 = s.one_minus_beta1, f.omb2 = s.one_minus_beta2;
+  f.step_size = start.step_size;
+  f.inv_sqrt_bc2 = start.inv_sqrt_bc2;
+  f.eps = s.eps;
+  f.lr = s.lr;
+  f.minus_zero = s.minus_zero;
+  return f;
+}
+
+// After the barrier, thread 0 only: its place among the CTAs; and, at the kernel's end, what the last one does.
+__device__ __forceinline__ void adam_arrive(const AdamScalars& s, AdamStart& start) {
+  __threadfence();
+  start.place = atomicAdd(s.ticket, 1u);
+}
+__device__ __forceinline__ void adam_end(const AdamScalars& s, const AdamStart& start) {
+  if (start.place == gridDim.x - 1) {
+    __threadfence();
+    *s.ticket = 0;
+    if (s.advance) *s.step = start.t;
+  }
 }
 
 // 8 elements at p (aligned), or the first `n` of them one by one.
@@ -146,51 +173,76 @@ __device__ __forceinline__ void store8(T* p, int n, bool vec, const F2 (&f)[4]) 
 // ------------------------------------------------------------------------------------------
 // 32-bit states
 // ------------------------------------------------------------------------------------------
+// 8 elements of a tensor from `at` on, the first n of them in it.
 template <typename P, typename G, bool MASTER>
-__device__ __forceinline__ void adam_step_at(const AdamEntry& e, const AdamFactors& f, int64_t at, int n, bool vec) {
-  F2 p[4], g[4], m[4], v[4];
-  unpack8(load8(static_cast<const G*>(e.g) + at, n, vec), g);
-  unpack8(load8(static_cast<const float*>(e.m) + at, n, vec), m);
-  unpack8(load8(static_cast<const float*>(e.v) + at, n, vec), v);
-  if constexpr (MASTER) unpack8(load8(e.master + at, n, vec), p);
-  else unpack8(load8(static_cast<const P*>(e.p) + at, n, vec), p);
-  const AdamRates rates(f, e.lr_scale, e.decay);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    adam_moments(f, g[i], m[i], v[i]);
-    p[i] = adam_param(f, rates, p[i], m[i], v[i]);
-  }
-  if constexpr (MASTER) store8(e.master + at, n, vec, p);
-  store8(static_cast<P*>(e.p) + at, n, vec, p);
-  store8(static_cast<float*>(e.m) + at, n, vec, m);
-  store8(static_cast<float*>(e.v) + at, n, vec, v);
-}
+struct AdamPart {
+  using Held = typename std::conditional<MASTER, float, P>::type;
+  Pack<G, kVec> g;
+  Pack<Held, kVec> p;
+  Pack<float, kVec> m, v;
 
-template <typename P, typename G, bool MASTER, int CAP>
-__global__ void __launch_bounds__(kThreads)
-    adamw_kernel(const __grid_constant__ AdamList<CAP> list, const __grid_constant__ AdamScalars s) {
-  if (blockIdx.x < list.first[list.count]) {
-    const int t = tensor_of_chunk(list, blockIdx.x);
-    const AdamEntry& e = list.e[t];
-    AdamFactors f;
-    if (!adam_factors(s, &f)) return;  // in every CTA alike
-    const bool vec = e.head != kScalar;
-    const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[t]) * list.chunk_elems;
-    const int64_t end = min(begin + list.chunk_elems, e.n);
-    if (vec) {
-      // vectors start `head` elements in; the elements before belong to the first chunk's first thread
-      if (begin == 0 && threadIdx.x == 0 && e.head > 0)
-        adam_step_at<P, G, MASTER>(e, f, 0, static_cast<int>(min(static_cast<int64_t>(e.head), e.n)), false);
-      const int64_t stop = min(end + e.head, e.n);
-      for (int64_t at = begin + e.head + threadIdx.x * kVec; at < stop; at += kStep)
-        adam_step_at<P, G, MASTER>(e, f, at, static_cast<int>(min(static_cast<int64_t>(kVec), stop - at)), true);
-    } else {
-      for (int64_t at = begin + threadIdx.x; at < end; at += kThreads) adam_step_at<P, G, MASTER>(e, f, at, 1, false);
-    }
-  } else if (s.clip != nullptr && !isfinite(s.clip[0])) {
-    return;  // no tensor has an element, and the step is left out
+  __device__ __forceinline__ void load(const AdamEntry& e, int64_t at, int n, bool vec) {
+    g = load8(static_cast<const G*>(e.g) + at, n, vec);
+    m = load8(static_cast<const float*>(e.m) + at, n, vec);
+    v = load8(static_cast<const float*>(e.v) + at, n, vec);
+    p = load8((MASTER ? reinterpret_cast<const Held*>(e.master) : static_cast<const Held*>(e.p)) + at, n, vec);
   }
-  advance_step(s);
+  __device__ __forceinline__ void step(const AdamEntry& e, const AdamFactors& f, int64_t at, int n, bool vec) const {
+    F2 pf[4], gf[4], mf[4], vf[4];
+    unpack8(g, gf);
+    unpack8(m, mf);
+    unpack8(v, vf);
+    unpack8(p, pf);
+    const AdamRates rates(f, e.lr_scale, e.decay);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      adam_moments(f, gf[i], mf[i], vf[i]);
+      pf[i] = adam_param(f, rates, pf[i], mf[i], vf[i]);
+    }
+    if constexpr (MASTER) store8(e.master + at, n, vec, pf);
+    store8(static_cast<P*>(e.p) + at, n, vec, pf);
+    store8(static_cast<float*>(e.m) + at, n, vec, mf);
+    store8(static_cast<float*>(e.v) + at, n, vec, vf);
+  }
+};
+
+constexpr int kResident = 3;  // CTAs to an SM (227M bf16 parameters with masters: 923 us; 2: 935, 4: 942)
+
+// A CTA takes a chunk; its first loads are in flight while thread 0 makes the factors (394K fp32 parameters: 4.1 us,
+// 4.8 with the factors first and the ticket last).
+template <typename P, typename G, bool MASTER, int CAP>
+__global__ void __launch_bounds__(kThreads, kResident)
+    adamw_kernel(const __grid_constant__ AdamList<CAP> list, const __grid_constant__ AdamScalars s) {
+  __shared__ AdamStart start;
+  const bool any = blockIdx.x < list.first[list.count];  // a list without elements has one CTA, for the step alone
+  const int t = any ? tensor_of_chunk(list, blockIdx.x) : 0;
+  const AdamEntry& e = list.e[t];
+  const bool vec = any && e.head != kScalar;
+  const int64_t begin = any ? static_cast<int64_t>(blockIdx.x - list.first[t]) * list.chunk_elems : 0;
+  const int64_t end = any ? min(begin + list.chunk_elems, e.n) : 0;
+  // aligned: vectors start `head` elements in; else a thread takes single elements
+  const int64_t stop = vec ? min(end + e.head, e.n) : end;
+  const int stride = vec ? kStep : kThreads;
+  int64_t at = begin + (vec ? e.head + threadIdx.x * kVec : threadIdx.x);
+  auto count = [&] { return vec ? static_cast<int>(min(static_cast<int64_t>(kVec), stop - at)) : 1; };
+  AdamPart<P, G, MASTER> part;
+  if (at < stop) part.load(e, at, count(), vec);
+  if (threadIdx.x == 0) adam_begin(s, start);
+  __syncthreads();
+  if (!start.go) return;  // in every CTA alike
+  if (threadIdx.x == 0) adam_arrive(s, start);
+  const AdamFactors f = adam_factors(s, start);
+  while (at < stop) {
+    part.step(e, f, at, count(), vec);
+    at += stride;
+    if (at < stop) part.load(e, at, count(), vec);
+  }
+  if (vec && begin == 0 && threadIdx.x == 0 && e.head > 0) {  // the elements before the first vector
+    const int n = static_cast<int>(min(static_cast<int64_t>(e.head), e.n));
+    part.load(e, 0, n, false);
+    part.step(e, f, 0, n, false);
+  }
+  if (threadIdx.x == 0) adam_end(s, start);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -220,7 +272,6 @@ __device__ __forceinline__ void q8_fill(Q8Lines& t) {
   static_assert(kThreads == 256, "a thread to an exponent");
   t.m[threadIdx.x] = q8_line(7, threadIdx.x);
   t.v[threadIdx.x] = q8_line(8, threadIdx.x);
-  __syncthreads();
 }
 
 // The values of two codes (the low 8 bits of each half of `pair`), in units of the scale: with c the
@@ -460,9 +511,13 @@ template <typename P, typename G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads, kQ8Resident)
     adamw_q8_kernel(const __grid_constant__ AdamList<CAP> list, const __grid_constant__ AdamScalars s) {
   __shared__ Q8Lines lines;
+  __shared__ AdamStart start;
+  if (threadIdx.x == 0) adam_begin(s, start);
   q8_fill(lines);
-  AdamFactors f;
-  if (!adam_factors(s, &f)) return;  // in every CTA alike
+  __syncthreads();
+  if (!start.go) return;  // in every CTA alike
+  if (threadIdx.x == 0) adam_arrive(s, start);
+  const AdamFactors f = adam_factors(s, start);
   using Place = Q8Place<P, G, MASTER>;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint64_t chunks = list.first[list.count];
@@ -495,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, kQ8Resident)
       q8_step<P, G, MASTER>(f, rates, lines, n, ragged, ragged);
     }
   }
-  advance_step(s);
+  if (threadIdx.x == 0) adam_end(s, start);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -622,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, kNormResident)
 // Host
 // ------------------------------------------------------------------------------------------
 // Elements of a chunk: up to `most` passes of a CTA (a power of two), fewer while that leaves less than 16 chunks to an SM.
-// AdamW with 32-bit states takes 4 (935 us at 227M; 1: 1050), the norm 16 (70 us; 4: 74), the values 1 (178 us; 4: 200,
+// AdamW with 32-bit states takes 4 (at 227M, 1 took a ninth longer), the norm 16 (70 us; 4: 74), the values 1 (178 us; 4: 200,
 // 16: 228: two streams in and two out like a narrow band).
 uint32_t chunk_elems(int64_t total, const DeviceInfo& dev, int most) {
   int passes = 1;
