@@ -84,25 +84,28 @@ def _raw_stream(stream, device):
 class _Handle:
     """What the three classes share: the device, memory of their own, and the launch of an entry point."""
 
+    def _on(self, device):
+        self.device = device
+        self._index = -1 if device.index is None else device.index  # as Tensor.get_device
+
     def _own(self, *tensors):
         """Memory that the object's kernels use: complete when the constructor returns, and kept from reuse
         while a call on another stream than the constructor's may be at work on it."""
         self._kept = tensors
         self._home = _raw_stream(None, self.device)
-        if self.device.type == "cuda":
+        if self._index >= 0:
             torch.cuda.current_stream(self.device).synchronize()
 
     def _launch(self, fn, args, stream, what):
         """Calls the library with the device current, on `stream` (default: the device's current one)."""
-        device = self.device
-        s = _raw_stream(stream, device)
-        if s != self._home and device.type == "cuda":
+        s = _raw_stream(stream, self.device)
+        if s != self._home and self._index >= 0:
             for t in self._kept:
-                t.record_stream(stream or torch.cuda.current_stream(device))
-        if device.type == "cuda" and torch.cuda.current_device() == device.index:
+                t.record_stream(stream or torch.cuda.current_stream(self.device))
+        if self._index >= 0 and torch.cuda.current_device() == self._index:
             status = fn(*args, s)
         else:
-            with torch.cuda.device(device):
+            with torch.cuda.device(self.device):
                 status = fn(*args, s)
         if status != TBE_OK:
             _check(load(), status, what)
@@ -139,8 +142,7 @@ class LayerNorm(_Handle):
     def __init__(self, widths, x_dtype=torch.float32, y_dtype=None, weight_dtype=torch.float32, eps: float = 1e-5,
                  device="cuda"):
         self.lib = _bind(load())
-        self.device = _device(device)
-        self._index = -1 if self.device.index is None else self.device.index
+        self._on(_device(device))
         self.widths = [int(w) for w in ([widths] if isinstance(widths, int) else widths)]
         self.cols = sum(self.widths)
         self.x_dtype, self.y_dtype, self.weight_dtype = x_dtype, y_dtype or x_dtype, weight_dtype
@@ -251,21 +253,24 @@ class GradNorm(_Handle):
     def __init__(self, grads, device="cuda"):
         self.lib = _bind(load())
         self.grads = _tensor_list(grads, "gradients")
-        self.device = self.grads[0].device if self.grads else _device(device)
+        self._on(self.grads[0].device if self.grads else _device(device))
         self._dtype = _WDTYPE[self.grads[0].dtype] if self.grads else _WDTYPE[torch.float32]
         self._ptrs = _pointers(self.grads)
         self._numels = (c_i64 * max(1, len(self.grads)))(*[t.numel() for t in self.grads])
         self.ws = torch.zeros(self.lib.tbe_grad_norm_workspace_size(), dtype=torch.uint8, device=self.device)
+        self._ws, self._ws_bytes = self.ws.data_ptr(), self.ws.numel()
         self._own(self.ws)
 
     def compute(self, max_norm: float = math.inf, out=None, stream=None):
         """Returns out: float32 [2], the norm and min(1, max_norm / (norm + 1e-6))."""
         if out is None:
             out = _empty(2, torch.float32, self.device, stream)
+            address = out.data_ptr()
+        else:
+            address = _flat(out, "out", torch.float32, 2, self.device)
         self._launch(self.lib.tbe_grad_norm,
-                (len(self.grads), self._ptrs, self._numels, self._dtype, max_norm,
-                 _flat(out, "out", torch.float32, 2, self.device), self.ws.data_ptr(), self.ws.numel()), stream,
-                "tbe_grad_norm")
+                     (len(self.grads), self._ptrs, self._numels, self._dtype, max_norm, address, self._ws, self._ws_bytes),
+                     stream, "tbe_grad_norm")
         return out
 
 
@@ -282,8 +287,7 @@ class DenseAdamW(_Handle):
         self.lib = _bind(load())
         self.params = _tensor_list(params, "params")
         n = len(self.params)
-        self.device = self.params[0].device if n else _device(device)
-        self._index = -1 if self.device.index is None else self.device.index
+        self._on(self.params[0].device if n else _device(device))
         q8 = {"f32": False, "q8": True}[states]
         self.states = states
         self._numels = numels = [p.numel() for p in self.params]
