@@ -37,6 +37,7 @@ extern "C" {
  *   dx = rstd * (h - sum h / n - xhat * sum (h * xhat) / n),
  *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy.
  * A segment of one column, or of equal values (the pooled row of an empty bag), has xhat = 0.
+ * Limits: 4096 segments, 2^30 columns, fewer than 2^39 elements (TBE_ERR_UNSUPPORTED beyond).
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
   int64_t rows;                /* >= 0 */
@@ -89,12 +90,13 @@ typedef enum { TBE_STATE_F32 = 0, TBE_STATE_Q8 = 1 } tbe_state_type;
 typedef struct {
   void* param;             /* pdtype [numel] */
   const void* grad;        /* gdtype [numel] */
-  float* master;           /* fp32 [numel], or NULL: then param itself is read */
+  float* master;           /* fp32 [numel] of 16-bit params, for all tensors or for none (NULL): then
+                              param itself is read */
   void* exp_avg;           /* first moment: fp32 or uint8 [numel] */
   void* exp_avg_sq;        /* second moment */
   float* exp_avg_scale;    /* TBE_STATE_Q8: fp32 [ceil(numel / TBE_Q8_BLOCK)]; else not read */
   float* exp_avg_sq_scale;
-  int64_t numel;           /* >= 0 */
+  int64_t numel;           /* 0 .. 2^40 */
   float lr_scale;          /* the tensor's learning rate is lr * lr_scale */
   float weight_decay;
 } tbe_dense_tensor;
