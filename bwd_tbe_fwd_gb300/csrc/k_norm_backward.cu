@@ -63,16 +63,19 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
 #pragma unroll
   for (int i = 0; i < kPer / 2; ++i) dw[i] = db[i] = F2(0.f);
   const float inv_n = 1.f / static_cast<float>(width);
-  // The rows' statistics, B rows to a load (a lane each) and a batch ahead; a row's come by shuffle.
-  constexpr int B = L < 32 ? L : 32;
+  // The rows' statistics.  Wide rows of 16-bit types: 32 rows to a load (a lane each), a batch ahead, and a row's by shuffle
+  // (16384 x 4096: 69 us, 74 by the other way).  Others: each row's, a row ahead (16384 x 4096 fp32 with bf16 dy: 106 us, 124
+  // by shuffles; rows shared by parts of warps: the same).
+  constexpr bool kBatches = V == 8 && L > 32;
+  constexpr int B = kBatches ? 32 : 1;
   const int64_t stat_step = walk.step * a.segments, stat0 = walk.first * a.segments + seg;
-  const int my_row = threadIdx.x % B;
+  const int my_row = kBatches ? threadIdx.x % B : 0;
   auto stats = [&](int k0) {
     const bool have = k0 + my_row < walk.mine;
     const int64_t at = stat0 + (k0 + my_row) * stat_step;
     return make_float2(have ? g.mean[at] : 0.f, have ? g.rstd[at] : 0.f);
   };
-  float2 batch = stats(0), batch_ahead = stats(B);
+  float2 batch = stats(0), batch_ahead = kBatches ? stats(B) : make_float2(0.f, 0.f);
   int stage = 0;
   X* dx = static_cast<X*>(g.dx) + walk.first * a.dx_stride + col0 + lane * V;
   const int64_t dx_step = walk.step * a.dx_stride;
@@ -89,12 +92,18 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, const RowIn& g,
     x.read(stage, valid, in, xh);
     dy.read(stage, valid, in, h);
     stage = stage == kStages - 1 ? 0 : stage + 1;
-    const float mu = __shfl_sync(kFull, batch.x, k % B, B), q = __shfl_sync(kFull, batch.y, k % B, B);  // 0 past the rows
-    const F2 shift(-mu), scale(q);
-    if (k % B == B - 1) {
-      batch = batch_ahead;
-      batch_ahead = stats(k + 1 + B);
+    float mu = batch.x, q = batch.y;  // 0 past the rows
+    if constexpr (kBatches) {
+      mu = __shfl_sync(kFull, mu, k % B);
+      q = __shfl_sync(kFull, q, k % B);
+      if (k % B == B - 1) {
+        batch = batch_ahead;
+        batch_ahead = stats(k + 1 + B);
+      }
+    } else {
+      batch = stats(k + 1);
     }
+    const F2 shift(-mu), scale(q);
     F2 s1(0.f), s2(0.f);
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) {
