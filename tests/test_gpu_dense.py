@@ -238,6 +238,26 @@ def test_norm_same_bits_every_time_and_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(out + grads, out2 + grads2))
 
 
+@pytest.mark.parametrize("width", [128, 1001, 3000, 9000])
+def test_norm_in_a_graph(width):
+    s = norm_inputs(500, [width], "f32", "bf16")
+    ln = LayerNorm([width], torch.float32, torch.bfloat16)
+    y, mean, rstd = ln.forward(s["x"], s["weight"], s["bias"])
+    grads = ln.backward(s["dy"], s["x"], mean, rstd, s["weight"])
+    out = [torch.zeros_like(v) for v in (y, mean, rstd, *grads)]
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        ln.forward(s["x"], s["weight"], s["bias"], y=out[0], mean=out[1], rstd=out[2])
+        ln.backward(s["dy"], s["x"], out[1], out[2], s["weight"], dx=out[3], dweight=out[4], dbias=out[5])
+    for _ in range(2):
+        for v in out:
+            v.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, (y, mean, rstd, *grads)))
+
+
 def test_norm_backward_is_the_difference_quotient_of_forward():
     """<dx, d> + <dweight, e> + <dbias, f> against the change of <y, dy> along (d, e, f).  y is fp32: with a step of
     2^-6 the quotient's rounding part is |dy|_1 2^-24 |y| 2^6 ~ 2^-14 of the sum's size; its cubic part, halved step
@@ -670,6 +690,18 @@ def test_objects_made_and_used_on_different_streams():
         side.synchronize()
         assert int(steps) == 1 and all(torch.equal(a, b) for a, b in zip(got, grads))
     np.testing.assert_allclose(host(p), -5e-3, rtol=1e-5)
+
+
+@pytest.mark.parametrize("states", ["f32", "q8"])
+def test_adamw_nothing_to_update(states):
+    """No tensor, or tensors without elements: the step is counted, unless the norm calls it off."""
+    for params in ([], [torch.empty(0, device="cuda")] * 2):
+        opt = DenseAdamW(params, [p.clone() for p in params], states)
+        opt.step(LR)
+        opt.step(LR, clip=torch.tensor([1.0, 1.0], device="cuda"))
+        opt.step(LR, clip=torch.tensor([math.inf, 0.0], device="cuda"))
+        opt.step(LR, clip=torch.tensor([math.nan, math.nan], device="cuda"))
+        assert int(opt.steps) == 2
 
 
 def test_adamw_rebound_gradients():
