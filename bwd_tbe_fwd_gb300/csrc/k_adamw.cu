@@ -6,7 +6,7 @@
 // warp and no shared memory.
 //
 // Measured on a GB300 (copy rate 6.78 TB/s): 32-bit states are bound by DRAM (227M bf16 parameters with masters,
-// 28 bytes an element: 923 us, 6.87 TB/s), so is the norm (227M bf16: 70 us, 6.4 TB/s) and, with a write
+// 28 bytes an element: 923 us, 6.87 TB/s), so is the norm (227M bf16: 71 us, 6.4 TB/s) and, with a write
 // for every quarter byte read, the states' values (113M of each moment: 178 us, 6.4 TB/s).  The 8-bit step is bound by issue: 60
 // instructions an element for 10 bytes of traffic (113M bf16: 248 us, 4.6 TB/s), of which decoding takes 15, the step 15, scaling
 // and encoding 20.
@@ -601,7 +601,7 @@ constexpr int kLargeNorm = 1500;
 static_assert(sizeof(TensorList<NormEntry, kLargeNorm>) + 64 <= 32764, "kernel parameters");
 
 constexpr int kNormMaxGrid = 4096;
-constexpr int kNormResident = 8;  // CTAs to an SM
+constexpr int kNormResident = 4;  // CTAs to an SM (2.4M bf16 gradients: 10.7 us, 13.4 with 8, whose tickets meet at one address; 227M: 73.0, 72.5)
 struct NormWs {
   uint32_t ticket;
   uint32_t pad;
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, kNormResident)
 // Host
 // ------------------------------------------------------------------------------------------
 // Elements of a chunk: up to `most` passes of a CTA (a power of two), fewer while that leaves less than 16 chunks to an SM.
-// AdamW with 32-bit states takes 4 (at 227M, 1 took a ninth longer), the norm 16 (70 us; 4: 74), the values 1 (178 us; 4: 200,
+// AdamW with 32-bit states takes 4 (at 227M, 1 took a ninth longer), the norm 16 (with eight CTAs an SM 70 us; 4: 74), the values 1 (178 us; 4: 200,
 // 16: 228: two streams in and two out like a narrow band).
 uint32_t chunk_elems(int64_t total, const DeviceInfo& dev, int most) {
   int passes = 1;
