@@ -239,8 +239,21 @@ tbe_status launch_norm_backward(const NormArgs& a, int xtype, int ytype, int vec
                                 const float* mean, const float* rstd, const void* weight, void* dx, void* dweight,
                                 void* dbias, float* partial, const DeviceInfo& dev, cudaStream_t s);
 
-// First column and width of segment s.  Both are clamped into the row, and to multiples of V, so that col_offsets that disagree with
-// the host's widths give wrong sums but no access outside a row and none that is misaligned.
+// Columns [c0, c1) of a row of `cols`, as first column and width (at most `widest`), clamped so that whatever c0 and c1
+// are the columns lie in the row and start and end at multiples of V.  The first column has V columns of the row from it on
+// even where the width is 0: a thread without a column of its own reads the weights there.
+template <int V>
+__host__ __device__ __forceinline__ void clamp_span(int c0, int c1, int cols, int widest, int* col, int* width) {
+  c0 = c0 < 0 ? 0 : c0 > cols - V ? cols - V : c0;
+  c1 = c1 < c0 ? c0 : c1 > cols ? cols : c1;
+  c0 -= c0 % V;
+  const int w = c1 - c0 < widest ? c1 - c0 : widest;
+  *col = c0;
+  *width = w - w % V;
+}
+
+// First column and width of segment s; col_offsets that disagree with the host's widths give wrong sums but no access outside
+// a row or the weights and none that is misaligned.
 template <int V>
 __device__ __forceinline__ void segment_span(const NormArgs& a, int s, int* col, int* width) {
   if (a.col_offsets == nullptr) {
@@ -248,12 +261,7 @@ __device__ __forceinline__ void segment_span(const NormArgs& a, int s, int* col,
     *width = a.width;
     return;
   }
-  int c0 = min(max(__ldg(a.col_offsets + s), 0), a.cols), c1 = min(max(__ldg(a.col_offsets + s + 1), c0), a.cols);
-  c0 -= c0 % V;
-  int w = min(c1 - c0, a.width);
-  w -= w % V;
-  *col = c0;
-  *width = w;
+  clamp_span<V>(__ldg(a.col_offsets + s), __ldg(a.col_offsets + s + 1), a.cols, a.width, col, width);
 }
 
 }  // namespace tbe
