@@ -1,5 +1,6 @@
 // dense_api.cu -- the layer norm's C interface (tbe_dense.h): argument validation and the choice of
 // vector width.
+#include <cfloat>
 #include <cmath>
 
 #include "dense_common.cuh"
@@ -36,7 +37,7 @@ tbe_status make_norm(const tbe_norm_problem* p, NormArgs* a) {
   a->width = static_cast<int>(widest);
   a->cols = static_cast<int>(cols);
   a->wtype = p->wdtype;
-  a->eps = p->eps;
+  a->eps = p->eps > FLT_MIN ? p->eps : FLT_MIN;  // 2^-126: a segment without spread has an rstd all the same
   return TBE_OK;
 }
 

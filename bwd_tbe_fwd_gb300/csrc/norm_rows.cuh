@@ -74,6 +74,14 @@ struct RowReader {
       f[k] = F2(v[2 * k / V].get(2 * k % V), v[(2 * k + 1) / V].get((2 * k + 1) % V));
   }
 
+  // Vector j of a row in a stage, which starts at `row` in memory; the vector lies in the row.
+  static __device__ __forceinline__ void read_one(char* smem, int stage, const E*, int j, int, Pack<E, V>& v) {
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k)
+      shared_words<kChunk>(smem_u32(smem) + threadIdx.x * kChunk + stage * stage_bytes<E, V>(T) + (j * kChunks + k) * T * kChunk,
+                           &v.w[(kChunk / 4) * k]);
+  }
+
   static __device__ __forceinline__ void share() {}
   static __device__ __forceinline__ void reuse() {}
 };
@@ -154,6 +162,18 @@ struct RowReader<E, 1, L, T> {
     }
 #pragma unroll
     for (int k = 0; k < kPer / 2; ++k) f[k] = F2(v[2 * k].get(0), v[2 * k + 1].get(0));
+  }
+
+  static __device__ __forceinline__ void read_one(char* smem, int stage, const E* row, int j, int lane, Pack<E, 1>& v) {
+    const uint32_t src = smem_u32(smem) + threadIdx.x / L * kRegion + stage * stage_bytes<E, 1>(T) +
+                         static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16) + (j * L + lane) * static_cast<int>(sizeof(E));
+    if constexpr (sizeof(E) == 2) {
+      uint16_t h;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(src) : "memory");
+      v.w[0] = h;
+    } else {
+      shared_words<4>(src, v.w);
+    }
   }
 
   // Before other threads' copies are read.

@@ -36,7 +36,10 @@ extern "C" {
  * and backward, with xhat = (x - mean) * rstd and h = dy * weight:
  *   dx = rstd * (h - sum h / n - xhat * sum (h * xhat) / n),
  *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy.
- * A segment of one column, or of equal values (the pooled row of an empty bag), has xhat = 0.
+ * A segment of one column, or of equal values (the pooled row of an empty bag), has xhat = 0,
+ * exactly: mean is then the value itself (for magnitudes from 2^-50 on; below, to 2^-18 of it).
+ * eps counts as 2^-126 at least: with eps = 0 and no spread, rstd is 2^63.  A row's sums, and its
+ * mean times rstd, have to stay within fp32.
  * Limits: 4096 segments, 2^30 columns, fewer than 2^39 elements (TBE_ERR_UNSUPPORTED beyond).
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
