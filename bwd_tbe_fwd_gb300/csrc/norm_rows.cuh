@@ -256,12 +256,8 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* part) {
     const int lane = threadIdx.x % 32;
     if (lane % 16 == 0) reinterpret_cast<float*>(part)[threadIdx.x / 32 * 2 + lane / 16] = s;
     __syncthreads();
-    if constexpr (W <= 16) {
-      s = lanes_sum<W>(reinterpret_cast<const float*>(part)[lane % W * 2 + lane / 16]);
-    } else {
-      const float2 p = part[lane];
-      s = lanes_sum_halves<32>(p.x, p.y);
-    }
+    static_assert(W <= 16, "a part of each sum to half a warp's lanes");
+    s = lanes_sum<W>(reinterpret_cast<const float*>(part)[lane % W * 2 + lane / 16]);
   }
   const float t = __shfl_xor_sync(kFull, s, N / 2);
   const bool upper = threadIdx.x % N >= N / 2;
