@@ -116,8 +116,9 @@ typedef struct {
 
 /* The norm of all gradients together and the coefficient that clips it to max_norm:
  *   out[0] = sqrt(sum of squares),  out[1] = min(1, max_norm / (out[0] + 1e-6))
- * with out fp32 [2] on the device.  Squares are summed in fp32 by thread (at most 128 of them) and in fp64
- * from there on, in a fixed order; a non-finite gradient, or a square beyond fp32, gives a non-finite norm.  grads:
+ * with out fp32 [2] on the device.  Squares are summed in fp32 by thread (at most 130 of them) and in fp64
+ * from there on, in a fixed order; a non-finite gradient, or a square beyond fp32, gives a non-finite norm, and squares below
+ * 2^-150 count as 0.  grads:
  * host [count] device pointers, numels: host [count].  max_norm >= 0 (infinity: no clipping).
  * ws: tbe_grad_norm_workspace_size() bytes, 16-byte aligned, that the caller has zeroed once and no
  * other call uses at the same time; the call leaves it zeroed where that matters. */
