@@ -363,7 +363,7 @@ __device__ __forceinline__ uint2 q8_block(const float2 (&lines)[256], const F2 (
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         const float x = i & 1 ? f[i / 2].hi() : f[i / 2].lo();
-        if (!(w[i / 4] >> (8 * (i % 4)) & 0xffu) && __fmul_rn(x, inv) > 0.f) w[i / 4] |= 1u << (8 * (i % 4));
+        if (!(w[i / 4] >> (8 * (i % 4)) & 0xffu) && x > 0.f && inv > 0.f) w[i / 4] |= 1u << (8 * (i % 4));
       }
     }
   }
