@@ -85,8 +85,11 @@ tbe_status tbe_layer_norm_backward(const tbe_norm_problem* prob, const void* dy,
  * the scale, and 0 for 0: each leading zero is a power of 8, the bits below the leading one
  * divide its interval evenly, the largest code is the scale itself.  (After the dynamic
  * exponents of Dettmers et al., "8-bit Optimizers via Block-wise Quantization", 2022; base 8
- * makes every value exact in binary.)  A value takes the nearest code, but a positive second
- * moment at least code 1: rounded to zero it would leave the first moment divided by eps alone. */
+ * makes every value exact in binary.)  A magnitude takes the nearest code, except next to 0: of
+ * the first moment it takes code 0 up to 0.5625 of code 1's value (the middle of 8^-7 and 8^-6 times the
+ * scale), and a positive second moment takes at least code 1: rounded to zero it would leave the
+ * first moment divided by eps alone.  A block without a magnitude of 2^-120 or more is held as zeros,
+ * its scale too. */
 typedef enum { TBE_STATE_F32 = 0, TBE_STATE_Q8 = 1 } tbe_state_type;
 #define TBE_Q8_BLOCK 256
 
@@ -129,7 +132,8 @@ tbe_status tbe_grad_norm(int32_t count, const void* const* grads, const int64_t*
 /* One AdamW step of every tensor, in place, with g = grad * clip[1] and t = *step + 1:
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr wd) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32; p is the master where there is one (param then gets its rounding), else param.  step:
+ * in fp32, where v under the root counts as 2^-126 at least (its root as 2^-63, which matters beside a smaller
+ * eps); p is the master where there is one (param then gets its rounding), else param.  step:
  * device int64, the updates done so far, which the call increments.  clip: NULL (coefficient 1), or
  * the out of tbe_grad_norm: where its norm is not finite the call changes nothing, step
  * included.  In Q8, the update uses the moments before they are rounded to their codes; a
