@@ -7,9 +7,9 @@
 //
 // Measured on a GB300 (copy rate 6.78 TB/s): 32-bit states are bound by DRAM (227M bf16 parameters with masters,
 // 28 bytes an element: 923 us, 6.87 TB/s), so is the norm (227M bf16: 71 us, 6.4 TB/s) and, with a write
-// for every quarter byte read, the states' values (113M of each moment: 178 us, 6.4 TB/s).  The 8-bit step is bound by issue: 60
-// instructions an element for 10 bytes of traffic (113M bf16: 248 us, 4.6 TB/s), of which decoding takes 15, the step 15, scaling
-// and encoding 20.
+// for every quarter byte read, the states' values (113M of each moment: 178 us, 6.4 TB/s).  The 8-bit step (113M bf16: 248 us, 4.6
+// TB/s) has 60 instructions an element for 10 bytes of traffic, of which decoding takes 15, the step 15, scaling and encoding 20; two
+// thirds of the issue slots are taken, and the largest stall is the wait for a block's loads.
 #include <algorithm>
 #include <cmath>
 
@@ -208,7 +208,7 @@ struct AdamPart {
 
 constexpr int kResident = 3;  // CTAs to an SM (227M bf16 parameters with masters: 923 us; 2: 935, 4: 942)
 
-// A CTA takes a chunk; its first loads are in flight while thread 0 makes the factors (394K fp32 parameters: 4.1 us,
+// A CTA takes a chunk; its first loads are in flight while thread 0 makes the factors (297K fp32 parameters: 4.1 us,
 // 4.8 with the factors first and the ticket last).
 template <typename P, typename G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads, kResident)
@@ -505,7 +505,9 @@ struct Q8Ragged {
 // loaded into registers instead 280, into shared memory 294: their waits or traffic meet the table's); what is ragged or
 // not aligned is loaded element by element.
 constexpr int kQ8Ahead = 1;     // passes (2: 266 us)
-constexpr int kQ8Resident = 5;  // CTAs to an SM (3: 277 us, 4: 263, 5: 250 in spite of a few spilled registers)
+// CTAs to an SM, as bf16 without masters wants it: 3 274 us, 4 263, 5 248, in spite of 30 words that each thread reloads a pass.
+// Others, 4 and 5: bf16 with masters 341 and 334; fp32 320 and 331; bf16 with fp32 gradients and masters (50 words) 355 and 389.
+constexpr int kQ8Resident = 5;
 
 template <typename P, typename G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads, kQ8Resident)
@@ -601,7 +603,10 @@ constexpr int kLargeNorm = 1500;
 static_assert(sizeof(TensorList<NormEntry, kLargeNorm>) + 64 <= 32764, "kernel parameters");
 
 constexpr int kNormMaxGrid = 4096;
-constexpr int kNormResident = 4;  // CTAs to an SM (2.4M bf16 gradients: 10.7 us, 13.4 with 8, whose tickets meet at one address; 227M: 73.0, 72.5)
+// CTAs to an SM: 2.4M bf16 gradients 8.5 us, 10.0 with 8; 9.4M 13.1, 14.1; 38M 16.8, 17.8; 227M 71, 70.4.  At a few million
+// elements the fp64 pipe is the busiest part (41% of the SMs' active cycles): every thread adds in fp64 once a chunk and in the
+// CTA's sum.
+constexpr int kNormResident = 4;
 struct NormWs {
   uint32_t ticket;
   uint32_t pad;

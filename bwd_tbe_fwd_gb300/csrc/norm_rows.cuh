@@ -3,7 +3,7 @@
 // L threads share a row (a segment of one), 16 elements to a thread: 4 to 32 lanes of a warp, or a whole
 // CTA.  16 elements keep a row, its weights and the backward's two sums in registers, and leave few
 // shuffles to an element (with 4 elements to a thread, half of the instructions were shuffles and
-// addresses: 27 an element forward, 39 backward, against 9 and 16 now; 8192 x 26 x 128 backward took 67 us instead
+// addresses: 27 an element forward, 39 backward, against 10 and 16 now; 8192 x 26 x 128 backward took 67 us instead
 // of 47).  Rows to come are copied into shared memory asynchronously, kStages - 1 ahead, each thread's elements to
 // its own place: loads stay in flight over the reductions without registers to hold them.
 #pragma once
