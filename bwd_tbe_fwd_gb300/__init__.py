@@ -18,3 +18,4 @@ from .tbe import (  # noqa: F401
     tbe_bounds_check,
     tbe_forward,
 )
+from .tokens import SoftmaxLoss, TokenEmbedding  # noqa: F401

@@ -831,6 +831,8 @@ cudaError_t launch_tma_t(const FwdArgs& a, const TmaMap& map, const DeviceInfo& 
   return cudaGetLastError();
 }
 
+}  // namespace
+
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link against libcuda).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -845,6 +847,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+namespace {
 
 // The packed weights of equal-width tables as one [rows, D] matrix of 16-bit elements whose
 // copy box is one row: the tensor map of the tile::gather4 loads.

@@ -1,0 +1,651 @@
+// k_softmax.cu -- softmax cross entropy over a table's rows without keeping the logits (tbe_tokens.h).
+//
+// Forward: z = scale * hidden weight^T a 256 x 256 tile at a time on the tensor cores (pair_mma.cuh); the epilogue reduces
+// a tile's row to its maximum and sum of exponentials (in powers of 2), and picks the target's logit when its column
+// comes by; a second kernel joins a row's parts.  Backward: for a piece of the table's rows at a time, the logits again,
+// whose epilogue makes dz = c (p - onehot) in 16 bits, then dhidden += dz weight (summed over the pieces in fp32)
+// and dweight = dz^T hidden, which is complete for the piece's rows.
+#include <cfloat>
+
+#include "pair_mma.cuh"
+#include "tokens_common.cuh"
+
+namespace tbe {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // 2 ulp; below 2^-126 it is 0
+  return y;
+}
+
+// A token's target as a row of the table, or -1.
+__device__ __forceinline__ int load_target(const void* targets, int itype, int64_t i, int64_t rows) {
+  const int64_t t = itype == TBE_I32 ? ld_int<int32_t>(targets, i) : ld_int<int64_t>(targets, i);
+  return t >= 0 && t < rows ? static_cast<int>(t) : -1;
+}
+
+// 32 bytes at p, which is aligned to them.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// ------------------------------------------------------------------------------------------
+// Epilogues
+// ------------------------------------------------------------------------------------------
+// A row's part of the softmax over half a tile's columns: {maximum of z in powers of 2, sum of 2^(z - maximum)}.
+struct StatsJob {
+  struct Args {
+    const void* targets;
+    float2* part;          // [parts][parts_rows]
+    float* target_logit;   // [tokens]
+    uint32_t* ticket;      // set to 0 for the kernel that joins the parts
+    int64_t parts_rows, rows;
+    int tokens, itype;
+    float scale, scale2;   // scale2 = scale * log2(e)
+  };
+  static __device__ __forceinline__ void tile(const Args& a, int m, int n, int, int row, int half, uint32_t tmem) {
+    const int i = m * kPairM + row;
+    const int64_t col0 = static_cast<int64_t>(n) * 256 + half * 128;
+    if (m == 0 && n == 0 && row == 0 && half == 0) *a.ticket = 0;
+    const int t = i < a.tokens ? load_target(a.targets, a.itype, i, a.rows) : -1;
+    const int64_t tl = t < 0 ? -1 : t - col0;  // the target's column of this half
+    const int live = static_cast<int>(a.rows - col0 < 128 ? a.rows - col0 : 128);  // may be negative
+    float top = -INFINITY, sum = 0.0f;
+    pair::Columns c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c.request(tmem + j * 32);
+      c.landed();
+      if (live < j * 32 + 32) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (j * 32 + k >= live) c.r[k] = 0xff800000u;  // past the table: no part in the softmax
+      }
+      float most = c.get(0);
+#pragma unroll
+      for (int k = 1; k < 32; ++k) most = fmaxf(most, c.get(k));
+      const float next = fmaxf(top, most * a.scale2);
+      const float ref = next == -INFINITY ? 0.0f : next;  // nothing but -inf so far: no inf - inf
+      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 32; k += 4) {
+        s0 += exp2_fast(fmaf(c.get(k), a.scale2, -ref));
+        s1 += exp2_fast(fmaf(c.get(k + 1), a.scale2, -ref));
+        s2 += exp2_fast(fmaf(c.get(k + 2), a.scale2, -ref));
+        s3 += exp2_fast(fmaf(c.get(k + 3), a.scale2, -ref));
+      }
+      sum = sum * exp2_fast(top - ref) + ((s0 + s1) + (s2 + s3));
+      top = next;
+      const int tj = tl >= j * 32 && tl < j * 32 + 32 ? static_cast<int>(tl) - j * 32 : -1;
+      if (__any_sync(kFull, tj >= 0)) {
+        float z = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) z = tj == k ? c.get(k) : z;
+        if (tj >= 0) a.target_logit[i] = z * a.scale;
+      }
+    }
+    if (i < a.tokens) a.part[static_cast<int64_t>(n * 2 + half) * a.parts_rows + i] = make_float2(top, sum);
+  }
+};
+
+// dz = c (p - onehot), times the power of two that keeps it in 16 bits.
+template <typename T>
+struct GradJob {
+  struct Args {
+    const float* meta;     // {power of two, ...}
+    const float* coef;     // [tokens]; 0 where the token does not count
+    const float* lse2;     // [tokens] lse in powers of 2
+    const int* target;     // [tokens], -1 where the token does not count
+    T* dz;                 // [tokens][ld]
+    int64_t ld;
+    int tokens, first, live;   // first row of the piece, rows of the table from there on
+    float scale2;
+  };
+  static __device__ __forceinline__ void tile(const Args& a, int m, int n, int, int row, int half, uint32_t tmem) {
+    const int i = m * kPairM + row;
+    const bool in = i < a.tokens;
+    const int col0 = n * 256 + half * 128;
+    const int t = in ? a.target[i] : -1;
+    const int tl = t < 0 ? -1 : t - a.first - col0;
+    const float g = t < 0 ? 0.0f : a.coef[i] * a.meta[0], ref = in ? a.lse2[i] : 0.0f;
+    T* dst = a.dz + i * a.ld + col0;
+    pair::Columns c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c.request(tmem + j * 32);
+      c.landed();
+      const int tj = tl >= j * 32 && tl < j * 32 + 32 ? tl - j * 32 : -1;
+      float v[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = exp2_fast(fmaf(c.get(k), a.scale2, -ref));
+      if (__any_sync(kFull, tj >= 0)) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] -= tj == k ? 1.0f : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] *= g;
+      if (t < 0 || col0 + j * 32 + 32 > a.live) {  // no gradient: zeros, whatever the logits are
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = t < 0 || col0 + j * 32 + k >= a.live ? 0.0f : v[k];
+      }
+      if (in) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float f[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) f[k] = v[q * 16 + k];
+          Pack<T, 16> p;
+          p.set(f);
+          store32(dst + j * 32 + q * 16, p.w);
+        }
+      }
+    }
+  }
+};
+
+// A gradient's rows: the product times alpha, rounded.
+template <typename T, int BN>
+struct OutJob {
+  struct Args {
+    const float* meta;     // {.., alpha}
+    T* out;
+    int64_t stride, first, rows;   // first row of the product in `out`, rows of out
+    int cols;
+    int vec;               // rows allow 16-byte stores
+  };
+  static __device__ __forceinline__ void tile(const Args& a, int m, int n, int, int row, int half, uint32_t tmem) {
+    const int64_t i = a.first + static_cast<int64_t>(m) * kPairM + row;
+    const int col0 = n * BN + half * (BN / 2);
+    const float alpha = a.meta[1];
+    pair::Columns c;
+#pragma unroll
+    for (int j = 0; j < BN / 64; ++j) {
+      const int left = a.cols - col0 - j * 32;
+      if (left <= 0) break;
+      c.request(tmem + j * 32);
+      c.landed();
+      T* dst = a.out + i * a.stride + col0 + j * 32;
+#pragma unroll
+      for (int q = 0; q < 4 && i < a.rows; ++q) {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = c.get(q * 8 + k) * alpha;
+        Pack<T, 8> p;
+        p.set(f);
+        if (a.vec && left >= q * 8 + 8) p.store(dst + q * 8);
+        else p.store_some(dst + q * 8, left - q * 8);
+      }
+    }
+  }
+};
+
+// Partial sums in fp32, [split][tokens][stride]: stored by the first piece, added to by the others.
+template <int BN>
+struct SumJob {
+  struct Args {
+    float* sums;
+    int64_t stride;        // a multiple of 8
+    int tokens, add;
+  };
+  static __device__ __forceinline__ void tile(const Args& a, int m, int n, int s, int row, int half, uint32_t tmem) {
+    const int i = m * kPairM + row;
+    const int col0 = n * BN + half * (BN / 2);
+    pair::Columns c;
+#pragma unroll
+    for (int j = 0; j < BN / 64; ++j) {
+      const int64_t left = a.stride - col0 - j * 32;
+      if (left <= 0) break;
+      c.request(tmem + j * 32);
+      c.landed();
+      float* dst = a.sums + (static_cast<int64_t>(s) * a.tokens + i) * a.stride + col0 + j * 32;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (i >= a.tokens || left < q * 8 + 8) continue;
+        uint32_t v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = c.r[q * 8 + k];
+        if (a.add) {
+          const float4 x = reinterpret_cast<const float4*>(dst + q * 8)[0], y = reinterpret_cast<const float4*>(dst + q * 8)[1];
+          const float old[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(old[k] + __uint_as_float(v[k]));
+        }
+        store32(dst + q * 8, v);
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------------------------------
+// Before and after the products
+// ------------------------------------------------------------------------------------------
+constexpr int kPrepThreads = 256;
+
+struct PrepArgs {
+  int64_t tokens, rows, hidden_stride, weight_stride;
+  int64_t hidden_rows, weight_rows;   // rows to copy: tokens or 0, rows or 0
+  const uint16_t* hidden;
+  const uint16_t* weight;
+  uint16_t* hidden_copy;              // [.][dim_pad], rows of tokens that do not count as zeros
+  uint16_t* weight_copy;
+  int dim, dim_pad, itype;
+  int backward;                       // block 0 finds the power of two; the tokens' constants are laid out
+  const void* targets;
+  const float* lse;
+  const float* dloss;
+  const float* mean;
+  float scale;
+  float* meta;
+  float* coef;
+  float* lse2;
+  int* target;
+};
+
+__device__ __forceinline__ float coefficient(const PrepArgs& a, int64_t i) {
+  return (a.dloss != nullptr ? a.dloss[i] : 1.0f) * (a.mean != nullptr ? a.mean[1] : 1.0f);
+}
+
+// Copies rows to where TMA can address them, a warp to a row.
+__device__ __forceinline__ void copy_row(uint16_t* dst, const uint16_t* src, int dim, int dim_pad, bool live, int lane) {
+  const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && dim % 8 == 0;
+  for (int c = lane * 8; c < dim_pad; c += kWarp * 8) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (live) {
+      if (vec) {
+        v = *reinterpret_cast<const uint4*>(src + c);
+      } else {
+        uint32_t h[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] = c + k < dim ? src[c + k] : 0;
+        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + c) = v;
+  }
+}
+
+__global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const __grid_constant__ PrepArgs a) {
+  const int lane = lane_id(), w = threadIdx.x / kWarp;
+  const int block = static_cast<int>(blockIdx.x) - a.backward, blocks = static_cast<int>(gridDim.x) - a.backward;
+  if (block < 0) {
+    // The largest finite coefficient takes dz to 2^13 .. 2^14: |p - onehot| is at most 1, fp16 ends at 2^16, and what is
+    // 2^-38 of the largest is still a normal number there.
+    __shared__ float s_top[kPrepThreads / kWarp];
+    float top = 0.0f;
+    for (int64_t i = threadIdx.x; i < a.tokens; i += kPrepThreads) {
+      const float c = fabsf(coefficient(a, i));
+      if (load_target(a.targets, a.itype, i, a.rows) >= 0 && c <= FLT_MAX) top = fmaxf(top, c);
+    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    if (lane == 0) s_top[w] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int k = 1; k < kPrepThreads / kWarp; ++k) top = fmaxf(top, s_top[k]);
+      int e = top > 0.0f ? 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127) : 0;
+      e = e < -100 ? -100 : e > 100 ? 100 : e;
+      a.meta[0] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+      a.meta[1] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
+    return;
+  }
+  if (a.backward)
+    for (int64_t i = static_cast<int64_t>(block) * kPrepThreads + threadIdx.x; i < a.tokens; i += static_cast<int64_t>(blocks) * kPrepThreads) {
+      const int t = load_target(a.targets, a.itype, i, a.rows);
+      a.target[i] = t;
+      a.coef[i] = t >= 0 ? coefficient(a, i) : 0.0f;
+      a.lse2[i] = t >= 0 ? a.lse[i] * kLog2e : 0.0f;
+    }
+  const int64_t total = a.hidden_rows + a.weight_rows;
+  for (int64_t r = static_cast<int64_t>(block) * (kPrepThreads / kWarp) + w; r < total; r += static_cast<int64_t>(blocks) * (kPrepThreads / kWarp)) {
+    if (r < a.hidden_rows) {
+      const bool live = load_target(a.targets, a.itype, r, a.rows) >= 0;
+      copy_row(a.hidden_copy + r * a.dim_pad, a.hidden + r * a.hidden_stride, a.dim, a.dim_pad, live, lane);
+    } else {
+      const int64_t v = r - a.hidden_rows;
+      copy_row(a.weight_copy + v * a.dim_pad, a.weight + v * a.weight_stride, a.dim, a.dim_pad, true, lane);
+    }
+  }
+}
+
+// Joins the parts of 32 tokens' rows, a lane to a token, the parts dealt out to the warps; the last block adds up the losses.
+constexpr int kJoinThreads = 1024;
+struct BlockSum {
+  double loss;
+  long long count;
+};
+
+struct JoinArgs {
+  const float2* part;
+  const float* target_logit;
+  const void* targets;
+  float* loss;
+  float* lse;
+  float* mean;
+  BlockSum* sums;
+  uint32_t* ticket;
+  int64_t tokens, rows, parts_rows;
+  int parts, itype;
+  unsigned long long* stats;
+};
+
+__global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_constant__ JoinArgs a) {
+  constexpr int kWarps = kJoinThreads / kWarp;
+  __shared__ float2 s_part[kWarps][kWarp + 1];
+  __shared__ double s_loss[kWarps];
+  __shared__ long long s_count[kWarps];
+  __shared__ bool s_last;
+  const int lane = lane_id(), w = threadIdx.x / kWarp;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarp + lane;
+  float top = -INFINITY, sum = 0.0f;
+  if (i < a.tokens) {
+#pragma unroll 8
+    for (int p = w; p < a.parts; p += kWarps) {
+      const float2 v = a.part[p * a.parts_rows + i];
+      const float next = fmaxf(top, v.x), ref = next == -INFINITY ? 0.0f : next;
+      sum = sum * exp2_fast(top - ref) + v.y * exp2_fast(v.x - ref);
+      top = next;
+    }
+  }
+  s_part[w][lane] = make_float2(top, sum);
+  __syncthreads();
+  if (w == 0) {
+    top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_part[k][lane].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) sum += s_part[k][lane].y * exp2_fast(s_part[k][lane].x - ref);
+    const int64_t raw = i < a.tokens ? (a.itype == TBE_I32 ? ld_int<int32_t>(a.targets, i) : ld_int<int64_t>(a.targets, i)) : -1;
+    const bool counts = raw >= 0 && raw < a.rows;
+    const float lse = counts ? (ref + log2f(sum)) * kLn2 : 0.0f;
+    const float loss = counts ? lse - a.target_logit[i] : 0.0f;
+    if (i < a.tokens) a.lse[i] = lse, a.loss[i] = loss;
+    const unsigned bad = __ballot_sync(kFull, raw >= a.rows);
+    const unsigned live = __ballot_sync(kFull, counts);
+    double d = loss;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFull, d, o);
+    if (lane == 0) {
+      a.sums[blockIdx.x] = BlockSum{d, __popc(live)};
+      stat_add(a.stats, TBE_STAT_UNREPAIRED, __popc(bad));
+      __threadfence();
+      s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  double d = 0.0;
+  long long n = 0;
+  for (unsigned b = threadIdx.x; b < gridDim.x; b += kJoinThreads) d += __ldcg(&a.sums[b].loss), n += __ldcg(&a.sums[b].count);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFull, d, o), n += __shfl_xor_sync(kFull, n, o);
+  if (lane == 0) s_loss[w] = d, s_count[w] = n;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < kWarps; ++k) d += s_loss[k], n += s_count[k];
+    a.mean[0] = n > 0 ? static_cast<float>(d / static_cast<double>(n)) : 0.0f;
+    a.mean[1] = n > 0 ? static_cast<float>(1.0 / static_cast<double>(n)) : 0.0f;
+  }
+}
+
+// dhidden = alpha * the sums of all splits; zeros for tokens that do not count.
+template <typename T>
+struct FinishArgs {
+  const float* sums;
+  const float* meta;
+  const int* target;
+  T* out;
+  int64_t tokens, sums_stride, stride;
+  int splits, cols, vec;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant__ FinishArgs<T> a) {
+  const int64_t per_row = a.sums_stride / 8, total = a.tokens * per_row;
+  const float alpha = a.meta[1];
+  for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; x < total; x += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t i = x / per_row;
+    const int col = static_cast<int>(x - i * per_row) * 8;
+    float f[8] = {};
+    if (a.target[i] >= 0) {
+      for (int s = 0; s < a.splits; ++s) {
+        const float4* p = reinterpret_cast<const float4*>(a.sums + (s * a.tokens + i) * a.sums_stride + col);
+        const float4 u = p[0], v = p[1];
+        f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w, f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] *= alpha;
+    }
+    Pack<T, 8> p;
+    p.set(f);
+    T* dst = a.out + i * a.stride + col;
+    if (a.vec && col + 8 <= a.cols) p.store(dst);
+    else p.store_some(dst, a.cols - col);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Host
+// ------------------------------------------------------------------------------------------
+template <int BN, bool AMN, bool BMN, class Job>
+tbe_status launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, PairShape g, const typename Job::Args& args, bool bf16,
+                       const DeviceInfo& dev, cudaStream_t s) {
+  auto* kernel = pair_mma_kernel<BN, AMN, BMN, Job>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PairTile<BN>::kSmem);
+  if (e != cudaSuccess) return cuda_status(e);
+  g.idesc = pair_idesc(bf16, BN, AMN, BMN);
+  const int64_t items = static_cast<int64_t>(g.m_tiles) * g.n_tiles * g.splits;
+  const int64_t pairs = items < dev.sms / 2 ? items : dev.sms / 2;
+  kernel<<<static_cast<unsigned>(2 * pairs), kPairThreads, PairTile<BN>::kSmem, s>>>(ma, mb, g, args);
+  note_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+tbe_status launch_prep(const PrepArgs& p, const DeviceInfo& dev, cudaStream_t s) {
+  const int64_t rows = p.hidden_rows + p.weight_rows;
+  int64_t blocks = ceil_div(rows, kPrepThreads / kWarp);
+  if (blocks > dev.sms * 8) blocks = dev.sms * 8;
+  if (blocks < 1) blocks = 1;
+  loss_prep_kernel<<<static_cast<unsigned>(blocks + p.backward), kPrepThreads, 0, s>>>(p);
+  note_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+size_t place(size_t* at, int64_t bytes) {
+  const size_t here = *at;
+  *at += static_cast<size_t>(round_up(bytes, 256));
+  return here;
+}
+
+// Bytes of dz that a piece of the table may take.
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+
+// Columns of a tile of the gradients' products: the narrow one where the rows are no wider.
+int gradient_bn(const LossArgs& a) { return a.dim <= 128 ? 128 : 256; }
+
+template <typename T>
+tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, const void* hidden, void* dhidden,
+                         void* dweight, char* ws, const DeviceInfo& dev, cudaStream_t s) {
+  const bool bf16 = a.dtype == TBE_BF16;
+  const int N = static_cast<int>(a.tokens), m_tiles = static_cast<int>(ceil_div(N, kPairM)), bn = gradient_bn(a);
+  const int d_tiles = static_cast<int>(ceil_div(a.dim, bn)), d_blocks = static_cast<int>(ceil_div(a.dim, kPairK));
+  float* meta = reinterpret_cast<float*>(ws + l.meta);
+  const int* target = reinterpret_cast<const int*>(ws + l.target);
+  T* dz = reinterpret_cast<T*>(ws + l.dz);
+  float* sums = reinterpret_cast<float*>(ws + l.sums);
+  tbe_status st;
+  for (int64_t first = 0; first < a.rows; first += l.piece) {
+    const int live = static_cast<int>(a.rows - first < l.piece ? a.rows - first : l.piece);
+    const int v_tiles = static_cast<int>(ceil_div(live, 256)), f = static_cast<int>(first);
+    PairShape g{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 0, a.stats};
+    typename GradJob<T>::Args ga{meta, reinterpret_cast<const float*>(ws + l.coef), reinterpret_cast<const float*>(ws + l.lse2), target,
+                                 dz, l.piece, N, f, live, a.scale * kLog2e};
+    if ((st = launch_pair<256, false, false, GradJob<T>>(maps[0], maps[1], g, ga, bf16, dev, s)) != TBE_OK) return st;
+    // dhidden: dz [tokens, piece] by weight [piece, dim]
+    g = PairShape{m_tiles, d_tiles, l.splits, static_cast<int>(ceil_div(live, kPairK)), 0, 0, 0, f, 0, a.stats};
+    if (bn == 128) {
+      SumJob<128>::Args sa{sums, l.dim_pad, N, first > 0};
+      st = launch_pair<128, false, true, SumJob<128>>(maps[2], maps[3], g, sa, bf16, dev, s);
+    } else {
+      SumJob<256>::Args sa{sums, l.dim_pad, N, first > 0};
+      st = launch_pair<256, false, true, SumJob<256>>(maps[2], maps[3], g, sa, bf16, dev, s);
+    }
+    if (st != TBE_OK) return st;
+    // dweight: dz^T [piece, tokens] by hidden [tokens, dim]
+    g = PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, 0, a.stats};
+    const int vec = a.dweight_stride % 8 == 0 && is_aligned(dweight, 16);
+    if (bn == 128) {
+      typename OutJob<T, 128>::Args oa{meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, a.dim, vec};
+      st = launch_pair<128, true, true, OutJob<T, 128>>(maps[4], maps[5], g, oa, bf16, dev, s);
+    } else {
+      typename OutJob<T, 256>::Args oa{meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, a.dim, vec};
+      st = launch_pair<256, true, true, OutJob<T, 256>>(maps[4], maps[5], g, oa, bf16, dev, s);
+    }
+    if (st != TBE_OK) return st;
+  }
+  FinishArgs<T> fa{sums, meta, target, static_cast<T*>(dhidden), a.tokens, l.dim_pad, a.dhidden_stride, l.splits, a.dim,
+                   a.dhidden_stride % 8 == 0 && is_aligned(dhidden, 16)};
+  int64_t blocks = ceil_div(a.tokens * (l.dim_pad / 8), 256);
+  if (blocks > dev.sms * 8) blocks = dev.sms * 8;
+  loss_finish_kernel<T><<<static_cast<unsigned>(blocks), 256, 0, s>>>(fa);
+  note_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+bool encode_operand(CUtensorMap* map, const void* p, bool bf16, int64_t inner, int64_t outer, int64_t stride, int box_outer) {
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[2] = {kPairK, static_cast<cuuint32_t>(box_outer)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(p), dims, strides,
+                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+LossForwardLayout loss_forward_layout(const LossArgs& a) {
+  LossForwardLayout l{};
+  size_t at = 0;
+  const int64_t dim_pad = round_up(a.dim, 8);
+  l.parts = static_cast<int>(2 * ceil_div(a.rows, 256));
+  l.parts_rows = round_up(a.tokens, 32);
+  l.part = place(&at, l.parts * l.parts_rows * 8);
+  l.target = place(&at, a.tokens * 4);
+  l.ticket = place(&at, 256 + ceil_div(a.tokens, kWarp) * static_cast<int64_t>(sizeof(BlockSum)));  // and the blocks' sums
+  l.hidden = place(&at, a.tokens * dim_pad * 2);
+  l.weight = place(&at, a.copy_weight ? a.rows * dim_pad * 2 : 0);
+  l.total = at;
+  return l;
+}
+
+LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev) {
+  LossBackwardLayout l{};
+  size_t at = 0;
+  l.dim_pad = round_up(a.dim, 8);
+  int64_t most = kPieceBytes / 2 / (a.tokens > 0 ? a.tokens : 1) / 256 * 256;
+  if (most < 256) most = 256;
+  if (most > (1 << 30)) most = 1 << 30;
+  const int64_t pieces = ceil_div(a.rows, most);
+  l.piece = round_up(ceil_div(a.rows, pieces), 256);
+  const int64_t tiles = ceil_div(a.tokens, kPairM) * ceil_div(a.dim, gradient_bn(a)), blocks = ceil_div(l.piece, kPairK);
+  int64_t splits = tiles > 0 ? dev.sms / 2 / tiles : 1;
+  if (splits > blocks / 4) splits = blocks / 4;
+  // the last piece may be shorter: every split has to have a part of it
+  const int64_t last = ceil_div(a.rows - (ceil_div(a.rows, l.piece) - 1) * l.piece, kPairK);
+  if (splits > last) splits = last;
+  l.splits = splits < 1 ? 1 : static_cast<int>(splits);
+  l.meta = place(&at, 16);
+  l.coef = place(&at, a.tokens * 4);
+  l.lse2 = place(&at, a.tokens * 4);
+  l.target = place(&at, a.tokens * 4);
+  l.hidden = place(&at, a.tokens * l.dim_pad * 2);
+  l.weight = place(&at, a.copy_weight ? a.rows * l.dim_pad * 2 : 0);
+  // What these two take varies with the number of tokens both ways: as much as any smaller number may need, so that a
+  // workspace for the largest call serves every call.
+  const int64_t whole = a.tokens * round_up(a.rows, 256) * 2, least = a.tokens * 512;
+  const int64_t capped = least > kPieceBytes ? least : kPieceBytes;
+  l.dz = place(&at, whole < capped ? whole : capped);
+  const int64_t split = static_cast<int64_t>(dev.sms / 2) * kPairM * 256, once = a.tokens * l.dim_pad;  // splits * tiles <= sms / 2
+  l.sums = place(&at, (split > once ? split : once) * 4);
+  l.total = at;
+  return l;
+}
+
+tbe_status launch_loss_forward(const LossArgs& a, const LossForwardLayout& l, const void* hidden, const void* weight,
+                               const void* targets, float* loss, float* lse, float* mean, char* ws, const DeviceInfo& dev,
+                               cudaStream_t s) {
+  if (a.tokens == 0) return cuda_status(cudaMemsetAsync(mean, 0, 8, s));
+  const bool bf16 = a.dtype == TBE_BF16;
+  const int dim_pad = static_cast<int>(round_up(a.dim, 8));
+  tbe_status st;
+  int64_t hs = a.hidden_stride, wst = a.weight_stride;
+  if (a.copy_hidden || a.copy_weight) {
+    PrepArgs p{};
+    p.tokens = a.tokens, p.rows = a.rows, p.hidden_stride = a.hidden_stride, p.weight_stride = a.weight_stride;
+    p.hidden_rows = a.copy_hidden ? a.tokens : 0, p.weight_rows = a.copy_weight ? a.rows : 0;
+    p.hidden = static_cast<const uint16_t*>(hidden), p.weight = static_cast<const uint16_t*>(weight);
+    p.hidden_copy = reinterpret_cast<uint16_t*>(ws + l.hidden), p.weight_copy = reinterpret_cast<uint16_t*>(ws + l.weight);
+    p.dim = a.dim, p.dim_pad = dim_pad, p.itype = a.itype, p.targets = targets;
+    if ((st = launch_prep(p, dev, s)) != TBE_OK) return st;
+    if (a.copy_hidden) hidden = ws + l.hidden, hs = dim_pad;
+    if (a.copy_weight) weight = ws + l.weight, wst = dim_pad;
+  }
+  CUtensorMap ma, mb;
+  if (!encode_operand(&ma, hidden, bf16, a.dim, a.tokens, hs, 128) || !encode_operand(&mb, weight, bf16, a.dim, a.rows, wst, 128))
+    return cuda_status(cudaErrorInvalidValue);
+  uint32_t* ticket = reinterpret_cast<uint32_t*>(ws + l.ticket);
+  float2* part = reinterpret_cast<float2*>(ws + l.part);
+  float* target_logit = reinterpret_cast<float*>(ws + l.target);
+  const PairShape g{static_cast<int>(ceil_div(a.tokens, kPairM)), l.parts / 2, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, 0,
+                    a.stats};
+  const StatsJob::Args sa{targets, part, target_logit, ticket, l.parts_rows, a.rows, static_cast<int>(a.tokens), a.itype, a.scale,
+                          a.scale * kLog2e};
+  if ((st = launch_pair<256, false, false, StatsJob>(ma, mb, g, sa, bf16, dev, s)) != TBE_OK) return st;
+  const JoinArgs ja{part, target_logit, targets, loss, lse, mean, reinterpret_cast<BlockSum*>(ws + l.ticket + 256), ticket, a.tokens,
+                    a.rows, l.parts_rows, l.parts, a.itype, a.stats};
+  loss_join_kernel<<<static_cast<unsigned>(ceil_div(a.tokens, kWarp)), kJoinThreads, 0, s>>>(ja);
+  note_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+tbe_status launch_loss_backward(const LossArgs& a, const LossBackwardLayout& l, const void* hidden, const void* weight,
+                                const void* targets, const float* lse, const float* dloss, const float* mean, void* dhidden,
+                                void* dweight, char* ws, const DeviceInfo& dev, cudaStream_t s) {
+  if (a.tokens == 0)  // a sum over no tokens
+    return cuda_status(cudaMemset2DAsync(dweight, a.dweight_stride * 2, 0, static_cast<size_t>(a.dim) * 2, a.rows, s));
+  const bool bf16 = a.dtype == TBE_BF16;
+  PrepArgs p{};
+  p.tokens = a.tokens, p.rows = a.rows, p.hidden_stride = a.hidden_stride, p.weight_stride = a.weight_stride;
+  p.hidden_rows = a.tokens, p.weight_rows = a.copy_weight ? a.rows : 0;
+  p.hidden = static_cast<const uint16_t*>(hidden), p.weight = static_cast<const uint16_t*>(weight);
+  p.hidden_copy = reinterpret_cast<uint16_t*>(ws + l.hidden), p.weight_copy = reinterpret_cast<uint16_t*>(ws + l.weight);
+  p.dim = a.dim, p.dim_pad = static_cast<int>(l.dim_pad), p.itype = a.itype, p.backward = 1, p.targets = targets, p.lse = lse;
+  p.dloss = dloss, p.mean = mean, p.scale = a.scale;
+  p.meta = reinterpret_cast<float*>(ws + l.meta), p.coef = reinterpret_cast<float*>(ws + l.coef);
+  p.lse2 = reinterpret_cast<float*>(ws + l.lse2), p.target = reinterpret_cast<int*>(ws + l.target);
+  const tbe_status st = launch_prep(p, dev, s);
+  if (st != TBE_OK) return st;
+  const void* h = ws + l.hidden;
+  const int64_t wst = a.copy_weight ? l.dim_pad : a.weight_stride;
+  if (a.copy_weight) weight = ws + l.weight;
+  const void* dz = ws + l.dz;
+  CUtensorMap maps[6];
+  if (!encode_operand(&maps[0], h, bf16, a.dim, a.tokens, l.dim_pad, 128) || !encode_operand(&maps[1], weight, bf16, a.dim, a.rows, wst, 128) ||
+      !encode_operand(&maps[2], dz, bf16, l.piece, a.tokens, l.piece, 128) || !encode_operand(&maps[3], weight, bf16, a.dim, a.rows, wst, 64) ||
+      !encode_operand(&maps[4], dz, bf16, l.piece, a.tokens, l.piece, 64) || !encode_operand(&maps[5], h, bf16, a.dim, a.tokens, l.dim_pad, 64))
+    return cuda_status(cudaErrorInvalidValue);
+  if (bf16) return loss_backward<__nv_bfloat16>(a, l, maps, h, dhidden, dweight, ws, dev, s);
+  return loss_backward<__half>(a, l, maps, h, dhidden, dweight, ws, dev, s);
+}
+
+}  // namespace tbe

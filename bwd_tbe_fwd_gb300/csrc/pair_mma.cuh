@@ -1,0 +1,266 @@
+// pair_mma.cuh -- matrix products on the fifth-generation tensor cores by pairs of CTAs: C tile of 256 x BN =
+// sum over k of A[256][k] B[BN][k], 16-bit operands, fp32 accumulators, with an epilogue of the caller's.
+//
+// The two CTAs of a cluster sit on neighbouring SMs and work on one tile (tcgen05.mma.cta_group::2): each brings its
+// 128 rows of A and its half of B's rows into its shared memory, so a CTA copies BN / 2 rows of B where it would copy
+// BN alone: 64 bytes a clock at the full rate of a 256 x 256 tile, about what an SM can draw from L2.  Ten
+// warps: eight for the epilogue (warp w reads TMEM lanes 32 (w % 4) .. + 31 and half w / 4 of the columns), one thread that
+// issues the TMA copies of a ring of stages of 64 k's, one (in the even CTA) that issues the products.  The
+// accumulator takes all 512 columns of TMEM as two buffers, so that the products of the next tile run while the epilogue
+// reads the last one.  The grid is persistent: pair p takes tiles p, p + pairs, ...
+//
+// Every wait is bounded.  A role whose wait gives up leaves its loop, the others follow by their own limits, the copies
+// in flight are waited for once more, and TBE_STAT_WAIT_TIMEOUT is counted.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "tbe_internal.cuh"
+
+namespace tbe {
+
+constexpr int kPairM = 256;            // rows of a tile; 128 to each CTA
+constexpr int kPairK = 64;             // k's of a stage: 128 bytes, one row of the swizzle
+constexpr int kEpiWarps = 8;
+constexpr int kPairThreads = 32 * (kEpiWarps + 2);
+constexpr uint32_t kPairWaitLimit = 1u << 22;
+
+template <int BN>
+struct PairTile {
+  static constexpr int kA = 128 * kPairK * 2;            // bytes of a CTA's part of a stage
+  static constexpr int kB = BN / 2 * kPairK * 2;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = 196608 / kStage;        // 6 of 32 KB, 8 of 24 KB
+  static constexpr int kSmem = kStages * kStage + 1024;  // and room to align to the swizzle's 1024 bytes
+};
+
+struct PairShape {
+  int m_tiles, n_tiles, splits, k_blocks;  // k_blocks: of all splits together; splits <= k_blocks
+  int a_m0, a_k0, b_n0, b_k0;              // where the product starts in A's and B's coordinates
+  uint32_t idesc;
+  unsigned long long* stats;
+};
+
+// kind::f16 instruction descriptor: fp32 accumulator, 16-bit operands, M = 256.
+inline uint32_t pair_idesc(bool bf16, int bn, bool a_mn, bool b_mn) {
+  const uint32_t t = bf16 ? 1 : 0;
+  return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(kPairM >> 4) << 24);
+}
+
+namespace pair {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address, in the cluster's window, of the same place in the even CTA's shared memory.
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// Shared-memory descriptor of a 128-byte-swizzled operand tile.  K-major: rows of 64 k's, 8 of them (1024 bytes) to a
+// swizzle atom.  MN-major: blocks of 64 (m or n) x 64 k's, a k to a row of 128 bytes, the blocks 8192 bytes apart.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  const uint64_t lbo = MN ? 8192 >> 4 : 1;
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (lbo << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+// Arrives on the barrier at this place in both CTAs when the products issued so far are done.
+__device__ __forceinline__ void commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 accumulator columns of this thread's TMEM lane: requested, and there after landed().
+struct Columns {
+  uint32_t r[32];
+  __device__ __forceinline__ void request(uint32_t addr) {
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+  }
+  // The registers are operands, so that no use of them moves above the wait.
+  __device__ __forceinline__ void landed() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+  }
+  __device__ __forceinline__ float get(int i) const { return __uint_as_float(r[i]); }
+};
+
+}  // namespace pair
+
+// Job: `struct Args` and `tile(args, m, n, split, row, half, tmem)`: row = this thread's row of the tile (0 .. 255),
+// half = which half of the columns, tmem = the address of its first column.  All 32 lanes of a warp call it.
+template <int BN, bool AMN, bool BMN, class Job>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_mma_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ PairShape g, const __grid_constant__ typename Job::Args args) {
+  using T = PairTile<BN>;
+  constexpr int ST = T::kStages;
+  extern __shared__ uint8_t s_raw[];
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2];
+  __shared__ uint32_t s_tmem;
+  const uint32_t ring = (smem_u32(s_raw) + 1023u) & ~1023u;
+  const int w = threadIdx.x / kWarp, lane = lane_id();
+  const uint32_t rank = pair::cluster_rank();
+  const int pair_id = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int items = g.m_tiles * g.n_tiles * g.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], 2 * kEpiWarps);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (w == 0) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  pair::fence_before();
+  __syncthreads();
+  pair::cluster_sync();  // both CTAs' barriers exist
+  pair::fence_after();
+  const uint32_t tmem = s_tmem;
+  bool failed = false;
+
+  if (w == kEpiWarps) {
+    if (lane == 0) {  // copies
+      uint32_t it = 0;
+      for (int item = pair_id; item < items && !failed; item += pairs) {
+        const int m = item % g.m_tiles, rest = item / g.m_tiles, n = rest % g.n_tiles, s = rest / g.n_tiles;
+        const int am = g.a_m0 + m * kPairM + static_cast<int>(rank) * 128, bn = g.b_n0 + n * BN + static_cast<int>(rank) * (BN / 2);
+        const int k1 = static_cast<int>(static_cast<int64_t>(g.k_blocks) * (s + 1) / g.splits);
+        for (int kb = static_cast<int>(static_cast<int64_t>(g.k_blocks) * s / g.splits); kb < k1; ++kb, ++it) {
+          const uint32_t st = it % ST;
+          if (!mbar_wait_bounded(&empty[st], ((it / ST) & 1) ^ 1, kPairWaitLimit)) {
+            failed = true;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * T::kStage);
+          const uint32_t bar = pair::in_leader(smem_u32(&full[st])), a = ring + st * T::kStage, b = a + T::kA;
+          const int ak = g.a_k0 + kb * kPairK, bk = g.b_k0 + kb * kPairK;
+          if constexpr (AMN) {
+            pair::tma_2d(a, &map_a, am, ak, bar);
+            pair::tma_2d(a + 8192, &map_a, am + 64, ak, bar);
+          } else {
+            pair::tma_2d(a, &map_a, ak, am, bar);
+          }
+          if constexpr (BMN) {
+#pragma unroll
+            for (int x = 0; x < BN / 128; ++x) pair::tma_2d(b + x * 8192, &map_b, bn + x * 64, bk, bar);
+          } else {
+            pair::tma_2d(b, &map_b, bk, bn, bar);
+          }
+        }
+      }
+      // Copies must not be in flight when a CTA ends: in the even CTA, whose barriers count both CTAs' copies, the last
+      // round of every stage has landed (its products are done by then, unless a wait gave up).
+      if (rank == 0)
+        for (uint32_t k = it < ST ? 0 : it - ST; k < it; ++k)
+          failed = !mbar_wait_bounded(&full[k % ST], (k / ST) & 1, kPairWaitLimit) || failed;
+    }
+    __syncwarp();
+  } else if (w == kEpiWarps + 1) {
+    if (rank == 0 && lane == 0) {  // products
+      uint32_t it = 0, tile = 0;
+      for (int item = pair_id; item < items && !failed; item += pairs, ++tile) {
+        const int s = item / g.m_tiles / g.n_tiles;
+        const int k0 = static_cast<int>(static_cast<int64_t>(g.k_blocks) * s / g.splits);
+        const int k1 = static_cast<int>(static_cast<int64_t>(g.k_blocks) * (s + 1) / g.splits);
+        const uint32_t buf = tile & 1, d = tmem + buf * 256;
+        if (!mbar_wait_bounded(&acc_empty[buf], ((tile >> 1) & 1) ^ 1, kPairWaitLimit)) {
+          failed = true;
+          break;
+        }
+        pair::fence_after();
+        for (int kb = k0; kb < k1; ++kb, ++it) {
+          const uint32_t st = it % ST;
+          if (!mbar_wait_bounded(&full[st], (it / ST) & 1, kPairWaitLimit)) {
+            failed = true;
+            break;
+          }
+          pair::fence_after();
+          const uint64_t a = pair::operand_desc<AMN>(ring + st * T::kStage), b = pair::operand_desc<BMN>(ring + st * T::kStage + T::kA);
+#pragma unroll
+          for (int k = 0; k < kPairK / 16; ++k)  // 16 k's: 32 bytes along a row, or two groups of 8 rows
+            pair::mma(d, a + k * ((AMN ? 2048 : 32) >> 4), b + k * ((BMN ? 2048 : 32) >> 4), g.idesc, kb > k0 || k > 0);
+          pair::commit_both(&empty[st]);
+        }
+        pair::commit_both(&acc_full[buf]);
+      }
+    }
+    __syncwarp();
+  } else {
+    uint32_t tile = 0;
+    const int row = static_cast<int>(rank) * 128 + (w % 4) * 32 + lane, half = w / 4;
+    for (int item = pair_id; item < items; item += pairs, ++tile) {
+      const int m = item % g.m_tiles, rest = item / g.m_tiles, n = rest % g.n_tiles, s = rest / g.n_tiles;
+      const uint32_t buf = tile & 1;
+      failed = !mbar_wait_bounded(&acc_full[buf], (tile >> 1) & 1, kPairWaitLimit);
+      if (__any_sync(0xffffffffu, failed)) {
+        failed = true;
+        break;
+      }
+      pair::fence_after();
+      Job::tile(args, m, n, s, row, half, tmem + buf * 256 + half * (BN / 2) + (static_cast<uint32_t>((w % 4) * 32) << 16));
+      pair::fence_before();
+      __syncwarp();
+      if (lane == 0) pair::arrive_at(pair::in_leader(smem_u32(&acc_empty[buf])));
+    }
+  }
+  if (failed && lane == 0) stat_add(g.stats, TBE_STAT_WAIT_TIMEOUT, 1);
+  __syncwarp();
+  pair::fence_before();
+  pair::cluster_sync();  // neither CTA ends, or frees its TMEM, while the other may still reach it
+  pair::fence_after();
+  if (w == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // NULL where the driver has none
+
+// A [outer, inner] matrix of 16-bit elements, `stride` elements
+// between rows, copied as boxes of 64 x box_outer with the 128-byte swizzle.  Elements outside the matrix read as 0.
+bool encode_operand(CUtensorMap* map, const void* p, bool bf16, int64_t inner, int64_t outer, int64_t stride, int box_outer);
+
+}  // namespace tbe

@@ -46,6 +46,9 @@ EXPORTED = (
     "tbe_layer_norm_forward", "tbe_layer_norm_backward_workspace_size", "tbe_layer_norm_backward",
     "tbe_grad_norm_workspace_size", "tbe_grad_norm", "tbe_adamw_workspace_size", "tbe_adamw_update",
     "tbe_adamw_state_values",
+    "tbe_lookup_forward", "tbe_lookup_backward_workspace_size", "tbe_lookup_backward",
+    "tbe_softmax_loss_workspace_size", "tbe_softmax_loss_forward", "tbe_softmax_loss_backward_workspace_size",
+    "tbe_softmax_loss_backward",
 )
 TBE_STATIC_SCRATCH_BYTES = 64 * 1024 * 1024
 
