@@ -16,7 +16,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "tbe_internal.cuh"
+#include "cluster.cuh"
 
 namespace tbe {
 
@@ -51,21 +51,8 @@ inline uint32_t pair_idesc(bool bf16, int bn, bool a_mn, bool b_mn) {
 
 namespace pair {
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address, in the cluster's window, of the same place in the even CTA's shared memory.
-__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-  return r;
-}
+// The same place in the even CTA's shared memory.
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) { return cluster_address(addr, 0); }
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -144,7 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ uint32_t s_tmem;
   const uint32_t ring = (smem_u32(s_raw) + 1023u) & ~1023u;
   const int w = threadIdx.x / kWarp, lane = lane_id();
-  const uint32_t rank = pair::cluster_rank();
+  const uint32_t rank = cluster_rank();
   const int pair_id = blockIdx.x / 2, pairs = gridDim.x / 2;
   const int items = g.m_tiles * g.n_tiles * g.splits;
 
@@ -159,7 +146,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
   pair::fence_before();
   __syncthreads();
-  pair::cluster_sync();  // both CTAs' barriers exist
+  cluster_sync();  // both CTAs' barriers exist
   pair::fence_after();
   const uint32_t tmem = s_tmem;
   bool failed = false;
@@ -252,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (failed && lane == 0) stat_add(g.stats, TBE_STAT_WAIT_TIMEOUT, 1);
   __syncwarp();
   pair::fence_before();
-  pair::cluster_sync();  // neither CTA ends, or frees its TMEM, while the other may still reach it
+  cluster_sync();  // neither CTA ends, or frees its TMEM, while the other may still reach it
   pair::fence_after();
   if (w == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
