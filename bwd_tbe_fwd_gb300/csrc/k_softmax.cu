@@ -37,6 +37,26 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
 // ------------------------------------------------------------------------------------------
 // Epilogues
 // ------------------------------------------------------------------------------------------
+struct NoRow {
+  template <typename A>
+  __device__ __forceinline__ void load(const A&, const PairItem&, int) {}
+};
+struct NoState {};
+
+// Goes through the N columns from `tmem` on, 32 at a time, the next ones requested while f(j, columns) works on the j-th.
+template <int N, typename R, typename F>
+__device__ __forceinline__ void each_columns(uint32_t tmem, R&& release, F&& f) {
+  pair::Columns c[2];
+  c[0].request(tmem);
+#pragma unroll
+  for (int j = 0; j < N / 32; ++j) {
+    c[j & 1].landed();
+    if (j + 1 < N / 32) c[(j + 1) & 1].request(tmem + (j + 1) * 32);
+    else release();
+    f(j, c[j & 1]);
+  }
+}
+
 // A row's part of the softmax over half a tile's columns: {maximum of z in powers of 2, sum of 2^(z - maximum)}.
 struct StatsJob {
   struct Args {
@@ -46,21 +66,29 @@ struct StatsJob {
     uint32_t* ticket;      // set to 0 for the kernel that joins the parts
     int64_t parts_rows, rows;
     int tokens, itype;
+    int carry;             // one tile of rows: a thread's parts are joined from tile to tile, one for each pair
     float scale, scale2;   // scale2 = scale * log2(e)
   };
-  static __device__ __forceinline__ void tile(const Args& a, int m, int n, int, int row, int half, uint32_t tmem) {
-    const int i = m * kPairM + row;
-    const int64_t col0 = static_cast<int64_t>(n) * 256 + half * 128;
-    if (m == 0 && n == 0 && row == 0 && half == 0) *a.ticket = 0;
-    const int t = i < a.tokens ? load_target(a.targets, a.itype, i, a.rows) : -1;
-    const int64_t tl = t < 0 ? -1 : t - col0;  // the target's column of this half
-    const int live = static_cast<int>(a.rows - col0 < 128 ? a.rows - col0 : 128);  // may be negative
+  struct Row {
+    int target;
+    __device__ __forceinline__ void load(const Args& a, const PairItem& it, int row) {
+      const int i = it.m * kPairM + row;
+      target = i < a.tokens ? load_target(a.targets, a.itype, i, a.rows) : -1;
+    }
+  };
+  struct State {
     float top = -INFINITY, sum = 0.0f;
-    pair::Columns c;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      c.request(tmem + j * 32);
-      c.landed();
+  };
+  template <typename R>
+  static __device__ __forceinline__ void tile(const Args& a, const Row& r, State& s, const PairItem& it, int row, int half, uint32_t tmem,
+                                              uint16_t*, R&& release) {
+    const int i = it.m * kPairM + row;
+    const int64_t col0 = static_cast<int64_t>(it.n) * 256 + half * 128;
+    if (it.m == 0 && it.n == 0 && row == 0 && half == 0) *a.ticket = 0;
+    const int64_t tl = r.target < 0 ? -1 : r.target - col0;  // the target's column of this half
+    const int live = static_cast<int>(a.rows - col0 < 128 ? a.rows - col0 : 128);  // may be negative
+    float top = s.top, sum = s.sum;
+    each_columns<128>(tmem, release, [&](int j, pair::Columns& c) {
       if (live < j * 32 + 32) {
 #pragma unroll
         for (int k = 0; k < 32; ++k)
@@ -88,8 +116,12 @@ struct StatsJob {
         for (int k = 0; k < 32; ++k) z = tj == k ? c.get(k) : z;
         if (tj >= 0) a.target_logit[i] = z * a.scale;
       }
-    }
-    if (i < a.tokens) a.part[static_cast<int64_t>(n * 2 + half) * a.parts_rows + i] = make_float2(top, sum);
+    });
+    if (a.carry) s.top = top, s.sum = sum;
+    else if (i < a.tokens) a.part[static_cast<int64_t>(it.n * 2 + half) * a.parts_rows + i] = make_float2(top, sum);
+  }
+  static __device__ __forceinline__ void finish(const Args& a, const State& s, int pair, int row, int half) {
+    if (a.carry && row < a.tokens) a.part[static_cast<int64_t>(pair * 2 + half) * a.parts_rows + row] = make_float2(s.top, s.sum);
   }
 };
 
@@ -106,19 +138,27 @@ struct GradJob {
     int tokens, first, live;   // first row of the piece, rows of the table from there on
     float scale2;
   };
-  static __device__ __forceinline__ void tile(const Args& a, int m, int n, int, int row, int half, uint32_t tmem) {
-    const int i = m * kPairM + row;
+  struct Row {
+    int target;
+    float coef, lse2, power;
+    __device__ __forceinline__ void load(const Args& a, const PairItem& it, int row) {
+      const int i = it.m * kPairM + row;
+      target = -1, coef = 0.0f, lse2 = 0.0f;
+      power = a.meta[0];
+      if (i < a.tokens) target = a.target[i], coef = a.coef[i], lse2 = a.lse2[i];
+    }
+  };
+  using State = NoState;
+  template <typename R>
+  static __device__ __forceinline__ void tile(const Args& a, const Row& r, State&, const PairItem& it, int row, int half, uint32_t tmem,
+                                              uint16_t*, R&& release) {
+    const int i = it.m * kPairM + row;
     const bool in = i < a.tokens;
-    const int col0 = n * 256 + half * 128;
-    const int t = in ? a.target[i] : -1;
+    const int col0 = it.n * 256 + half * 128, t = r.target;
     const int tl = t < 0 ? -1 : t - a.first - col0;
-    const float g = t < 0 ? 0.0f : a.coef[i] * a.meta[0], ref = in ? a.lse2[i] : 0.0f;
+    const float g = r.coef * r.power, ref = r.lse2;
     T* dst = a.dz + i * a.ld + col0;
-    pair::Columns c;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      c.request(tmem + j * 32);
-      c.landed();
+    each_columns<128>(tmem, release, [&](int j, pair::Columns& c) {
       const int tj = tl >= j * 32 && tl < j * 32 + 32 ? tl - j * 32 : -1;
       float v[32];
 #pragma unroll
@@ -144,8 +184,9 @@ struct GradJob {
           store32(dst + j * 32 + q * 16, p.w);
         }
       }
-    }
+    });
   }
+  static __device__ __forceinline__ void finish(const Args&, const State&, int, int, int) {}
 };
 
 // A gradient's rows: the product times alpha, rounded.
@@ -156,35 +197,55 @@ struct OutJob {
     T* out;
     int64_t stride, first, rows;   // first row of the product in `out`, rows of out
     int cols;
-    int vec;               // rows allow 16-byte stores
+    int vec;               // bytes of a store that every row allows: 32, 16, or 0 for element by element
   };
-  static __device__ __forceinline__ void tile(const Args& a, int m, int n, int, int row, int half, uint32_t tmem) {
-    const int64_t i = a.first + static_cast<int64_t>(m) * kPairM + row;
-    const int col0 = n * BN + half * (BN / 2);
-    const float alpha = a.meta[1];
-    pair::Columns c;
+  struct Row {
+    float alpha;
+    __device__ __forceinline__ void load(const Args& a, const PairItem&, int) { alpha = a.meta[1]; }
+  };
+  using State = NoState;
+  template <typename R>
+  static __device__ __forceinline__ void tile(const Args& a, const Row& r, State&, const PairItem& it, int row, int half, uint32_t tmem,
+                                              uint16_t* staging, R&& release) {
+    const int64_t i = a.first + static_cast<int64_t>(it.m) * kPairM + row;
+    const int col0 = it.n * BN + half * (BN / 2), lane = lane_id();
+    each_columns<BN / 2>(tmem, release, [&](int j, pair::Columns& c) {
+      const int left = a.cols - col0 - j * 32;   // columns from this block's first on; the same for the whole warp
+      if (left <= 0) return;
+      Pack<T, 16> p[2];
 #pragma unroll
-    for (int j = 0; j < BN / 64; ++j) {
-      const int left = a.cols - col0 - j * 32;
-      if (left <= 0) break;
-      c.request(tmem + j * 32);
-      c.landed();
-      T* dst = a.out + i * a.stride + col0 + j * 32;
+      for (int q = 0; q < 2; ++q) {
+        float f[16];
 #pragma unroll
-      for (int q = 0; q < 4 && i < a.rows; ++q) {
-        float f[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = c.get(q * 8 + k) * alpha;
-        Pack<T, 8> p;
-        p.set(f);
-        if (a.vec && left >= q * 8 + 8) p.store(dst + q * 8);
-        else p.store_some(dst + q * 8, left - q * 8);
+        for (int k = 0; k < 16; ++k) f[k] = c.get(q * 16 + k) * r.alpha;
+        p[q].set(f);
       }
-    }
+      if (a.vec != 0 && left >= 32) {
+        T* dst = a.out + i * a.stride + col0 + j * 32;
+        if (i < a.rows) {
+          if (a.vec == 32) store32(dst, p[0].w), store32(dst + 16, p[1].w);
+          else p[0].store(dst), p[1].store(dst + 16);
+        }
+        return;
+      }
+      // Rows that begin anywhere: through shared memory, so that a warp's store lies in one row instead of 32.
+      uint32_t* mine = reinterpret_cast<uint32_t*>(staging) + lane * (kStageRow / 2);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) mine[k] = p[k / 8].w[k % 8];
+      __syncwarp();
+      const int64_t i0 = i - lane;
+      const int rows = static_cast<int>(a.rows - i0 < 32 ? a.rows - i0 : 32);
+      uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + i0 * a.stride + col0 + j * 32 + lane;
+      if (lane < left)
+        for (int x = 0; x < rows; ++x) dst[x * a.stride] = staging[x * kStageRow + lane];
+      __syncwarp();
+    });
   }
+  static __device__ __forceinline__ void finish(const Args&, const State&, int, int, int) {}
 };
 
-// Partial sums in fp32, [split][tokens][stride]: stored by the first piece, added to by the others.
+// Sums in fp32, [split][tokens][stride]: stored by the first piece, added to by the others (each by one thread, so that the order is
+// the pieces').
 template <int BN>
 struct SumJob {
   struct Args {
@@ -192,33 +253,34 @@ struct SumJob {
     int64_t stride;        // a multiple of 8
     int tokens, add;
   };
-  static __device__ __forceinline__ void tile(const Args& a, int m, int n, int s, int row, int half, uint32_t tmem) {
-    const int i = m * kPairM + row;
-    const int col0 = n * BN + half * (BN / 2);
-    pair::Columns c;
-#pragma unroll
-    for (int j = 0; j < BN / 64; ++j) {
-      const int64_t left = a.stride - col0 - j * 32;
-      if (left <= 0) break;
-      c.request(tmem + j * 32);
-      c.landed();
-      float* dst = a.sums + (static_cast<int64_t>(s) * a.tokens + i) * a.stride + col0 + j * 32;
+  using Row = NoRow;
+  using State = NoState;
+  template <typename R>
+  static __device__ __forceinline__ void tile(const Args& a, const Row&, State&, const PairItem& it, int row, int half, uint32_t tmem, uint16_t*,
+                                              R&& release) {
+    const int i = it.m * kPairM + row;
+    const int col0 = it.n * BN + half * (BN / 2);
+    float* dst = a.sums + (static_cast<int64_t>(it.split) * a.tokens + i) * a.stride + col0;
+    each_columns<BN / 2>(tmem, release, [&](int j, pair::Columns& c) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (i >= a.tokens || left < q * 8 + 8) continue;
-        uint32_t v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = c.r[q * 8 + k];
+        if (i >= a.tokens || col0 + j * 32 + q * 8 >= a.stride) continue;
         if (a.add) {
-          const float4 x = reinterpret_cast<const float4*>(dst + q * 8)[0], y = reinterpret_cast<const float4*>(dst + q * 8)[1];
-          const float old[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(old[k] + __uint_as_float(v[k]));
+          for (int x = 0; x < 2; ++x)
+            asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + j * 32 + q * 8 + x * 4), "f"(c.get(q * 8 + x * 4)),
+                         "f"(c.get(q * 8 + x * 4 + 1)), "f"(c.get(q * 8 + x * 4 + 2)), "f"(c.get(q * 8 + x * 4 + 3))
+                         : "memory");
+        } else {
+          uint32_t v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = c.r[q * 8 + k];
+          store32(dst + j * 32 + q * 8, v);
         }
-        store32(dst + q * 8, v);
       }
-    }
+    });
   }
+  static __device__ __forceinline__ void finish(const Args&, const State&, int, int, int) {}
 };
 
 // ------------------------------------------------------------------------------------------
@@ -250,27 +312,42 @@ __device__ __forceinline__ float coefficient(const PrepArgs& a, int64_t i) {
   return (a.dloss != nullptr ? a.dloss[i] : 1.0f) * (a.mean != nullptr ? a.mean[1] : 1.0f);
 }
 
-// Copies rows to where TMA can address them, a warp to a row.
-__device__ __forceinline__ void copy_row(uint16_t* dst, const uint16_t* src, int dim, int dim_pad, bool live, int lane) {
-  const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && dim % 8 == 0;
-  for (int c = lane * 8; c < dim_pad; c += kWarp * 8) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (live) {
-      if (vec) {
-        v = *reinterpret_cast<const uint4*>(src + c);
-      } else {
-        uint32_t h[8];
+// 8 elements of a row from column c on, zeros past its end.
+__device__ __forceinline__ uint4 row_piece(const uint16_t* src, int c, int dim, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(src + c);
+  uint32_t h[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = c + k < dim ? src[c + k] : 0;
-        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-      }
+  for (int k = 0; k < 8; ++k) h[k] = c + k < dim ? src[c + k] : 0;
+  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+
+// Copies rows to where TMA can address them, 8 elements to a thread, two at a time; rows of tokens that do not count as zeros
+// where targets are given.
+__device__ __forceinline__ void copy_rows(uint16_t* dst, const uint16_t* src, int64_t rows, int64_t stride, int dim, int dim_pad,
+                                          const PrepArgs* mask, int64_t t, int64_t n) {
+  const int groups = dim_pad / 8;
+  const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && dim % 8 == 0 && stride % 8 == 0;
+  const int64_t total = rows * groups;
+  for (int64_t x0 = t; x0 < total; x0 += 2 * n) {
+    uint4 v[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t x = x0 + u * n;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (x >= total) continue;
+      const int64_t r = total >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(groups) : x / groups;
+      if (mask == nullptr || load_target(mask->targets, mask->itype, r, mask->rows) >= 0)
+        v[u] = row_piece(src + r * stride, static_cast<int>(x - r * groups) * 8, dim, vec);
     }
-    *reinterpret_cast<uint4*>(dst + c) = v;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (x0 + u * n < total) *reinterpret_cast<uint4*>(dst + (x0 + u * n) * 8) = v[u];
   }
 }
 
 __global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const __grid_constant__ PrepArgs a) {
   const int lane = lane_id(), w = threadIdx.x / kWarp;
+  may_follow();
   const int block = static_cast<int>(blockIdx.x) - a.backward, blocks = static_cast<int>(gridDim.x) - a.backward;
   if (block < 0) {
     // The largest finite coefficient takes dz to 2^13 .. 2^14: |p - onehot| is at most 1, fp16 ends at 2^16, and what is
@@ -293,23 +370,16 @@ __global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const __grid_co
     }
     return;
   }
+  const int64_t t = static_cast<int64_t>(block) * kPrepThreads + threadIdx.x, n = static_cast<int64_t>(blocks) * kPrepThreads;
   if (a.backward)
-    for (int64_t i = static_cast<int64_t>(block) * kPrepThreads + threadIdx.x; i < a.tokens; i += static_cast<int64_t>(blocks) * kPrepThreads) {
-      const int t = load_target(a.targets, a.itype, i, a.rows);
-      a.target[i] = t;
-      a.coef[i] = t >= 0 ? coefficient(a, i) : 0.0f;
-      a.lse2[i] = t >= 0 ? a.lse[i] * kLog2e : 0.0f;
+    for (int64_t i = t; i < a.tokens; i += n) {
+      const int target = load_target(a.targets, a.itype, i, a.rows);
+      a.target[i] = target;
+      a.coef[i] = target >= 0 ? coefficient(a, i) : 0.0f;
+      a.lse2[i] = target >= 0 ? a.lse[i] * kLog2e : 0.0f;
     }
-  const int64_t total = a.hidden_rows + a.weight_rows;
-  for (int64_t r = static_cast<int64_t>(block) * (kPrepThreads / kWarp) + w; r < total; r += static_cast<int64_t>(blocks) * (kPrepThreads / kWarp)) {
-    if (r < a.hidden_rows) {
-      const bool live = load_target(a.targets, a.itype, r, a.rows) >= 0;
-      copy_row(a.hidden_copy + r * a.dim_pad, a.hidden + r * a.hidden_stride, a.dim, a.dim_pad, live, lane);
-    } else {
-      const int64_t v = r - a.hidden_rows;
-      copy_row(a.weight_copy + v * a.dim_pad, a.weight + v * a.weight_stride, a.dim, a.dim_pad, true, lane);
-    }
-  }
+  copy_rows(a.hidden_copy, a.hidden, a.hidden_rows, a.hidden_stride, a.dim, a.dim_pad, &a, t, n);
+  copy_rows(a.weight_copy, a.weight, a.weight_rows, a.weight_stride, a.dim, a.dim_pad, nullptr, t, n);
 }
 
 // Joins the parts of 32 tokens' rows, a lane to a token, the parts dealt out to the warps; the last block adds up the losses.
@@ -342,6 +412,7 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_co
   const int lane = lane_id(), w = threadIdx.x / kWarp;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarp + lane;
   float top = -INFINITY, sum = 0.0f;
+  wait_before();
   if (i < a.tokens) {
 #pragma unroll 8
     for (int p = w; p < a.parts; p += kWarps) {
@@ -409,6 +480,7 @@ struct FinishArgs {
 template <typename T>
 __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant__ FinishArgs<T> a) {
   const int64_t per_row = a.sums_stride / 8, total = a.tokens * per_row;
+  wait_before();
   const float alpha = a.meta[1];
   for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; x < total; x += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t i = x / per_row;
@@ -434,18 +506,40 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant_
 // ------------------------------------------------------------------------------------------
 // Host
 // ------------------------------------------------------------------------------------------
-template <int BN, bool AMN, bool BMN, class Job>
-tbe_status launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, PairShape g, const typename Job::Args& args, bool bf16,
-                       const DeviceInfo& dev, cudaStream_t s) {
-  auto* kernel = pair_mma_kernel<BN, AMN, BMN, Job>;
+template <int BN, class P0, class P1>
+tbe_status launch_pair(const typename P0::Args& p0, const typename P1::Args& p1, PairPlan plan, cudaStream_t s) {
+  auto* kernel = pair_mma_kernel<BN, P0, P1>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PairTile<BN>::kSmem);
   if (e != cudaSuccess) return cuda_status(e);
-  g.idesc = pair_idesc(bf16, BN, AMN, BMN);
-  const int64_t items = static_cast<int64_t>(g.m_tiles) * g.n_tiles * g.splits;
-  const int64_t pairs = items < dev.sms / 2 ? items : dev.sms / 2;
-  kernel<<<static_cast<unsigned>(2 * pairs), kPairThreads, PairTile<BN>::kSmem, s>>>(ma, mb, g, args);
-  note_launch();
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_after(kernel, static_cast<unsigned>(2 * plan.pairs), kPairThreads, PairTile<BN>::kSmem, s, p0, p1, plan));
+}
+
+template <int BN, class P>
+tbe_status launch_product(const typename P::Args& p, const LossArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  const int64_t items = static_cast<int64_t>(p.g.m_tiles) * p.g.n_tiles * p.g.splits;
+  const PairPlan plan{static_cast<int>(items < dev.sms / 2 ? items : dev.sms / 2), 0, 0, a.stats};
+  return launch_pair<BN, P, NoProduct>(p, NoProduct::Args{}, plan, s);
+}
+
+// Two products in one launch: the first one's tiles are long and leave some pairs a tile short; how many of the second's
+// tiles those take before the rest is dealt out, so that the last pair to end does so soonest.
+PairPlan plan_two(const PairShape& g0, const PairShape& g1, const LossArgs& a, const DeviceInfo& dev) {
+  const int64_t n0 = static_cast<int64_t>(g0.m_tiles) * g0.n_tiles * g0.splits, n1 = static_cast<int64_t>(g1.m_tiles) * g1.n_tiles * g1.splits;
+  const int64_t most = dev.sms / 2, pairs = n0 + n1 < most ? n0 + n1 : most;
+  PairPlan best{static_cast<int>(pairs), 0, 0, a.stats};
+  const int64_t c0 = g0.k_blocks / g0.splits + 3, c1 = g1.k_blocks / g1.splits + 3;  // blocks, and what a tile costs besides
+  const int64_t busy = n0 % pairs, lazy = pairs - busy, each = n0 / pairs;
+  int64_t least = INT64_MAX;
+  for (int64_t extra = busy == 0 ? 0 : c0 / c1; extra >= 0 && extra <= (busy == 0 ? 0 : c0 / c1 + 1); ++extra) {
+    const int64_t some = lazy * extra <= n1 ? extra : n1 / lazy;
+    const int64_t rest = n1 - lazy * some, round = rest / pairs, left = rest % pairs;
+    for (int first = 0; first < 2; ++first) {
+      const int64_t l = each * c0 + (some + round + (first ? left > 0 : left > busy)) * c1;
+      const int64_t b = busy == 0 ? 0 : (each + 1) * c0 + (round + (first ? left > lazy : left > 0)) * c1;
+      if ((l > b ? l : b) < least) least = l > b ? l : b, best.extra = static_cast<int>(some), best.lazy_first = first;
+    }
+  }
+  return best;
 }
 
 tbe_status launch_prep(const PrepArgs& p, const DeviceInfo& dev, cudaStream_t s) {
@@ -465,58 +559,55 @@ size_t place(size_t* at, int64_t bytes) {
 }
 
 // Bytes of dz that a piece of the table may take.
-constexpr int64_t kPieceBytes = int64_t(256) << 20;
+constexpr int64_t kPieceBytes = int64_t(512) << 20;
 
-// Columns of a tile of the gradients' products: the narrow one where the rows are no wider.
-int gradient_bn(const LossArgs& a) { return a.dim <= 128 ? 128 : 256; }
+// Columns of a tile of the gradients' products: 128 where tiles of 256 would be a fifth or more emptier.
+int gradient_bn(int dim) { return round_up(dim, 128) * 5 <= round_up(dim, 256) * 4 ? 128 : 256; }
 
-template <typename T>
-tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, const void* hidden, void* dhidden,
-                         void* dweight, char* ws, const DeviceInfo& dev, cudaStream_t s) {
+template <typename T, int BN>
+tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, void* dhidden, void* dweight, char* ws,
+                         const DeviceInfo& dev, cudaStream_t s) {
   const bool bf16 = a.dtype == TBE_BF16;
-  const int N = static_cast<int>(a.tokens), m_tiles = static_cast<int>(ceil_div(N, kPairM)), bn = gradient_bn(a);
-  const int d_tiles = static_cast<int>(ceil_div(a.dim, bn)), d_blocks = static_cast<int>(ceil_div(a.dim, kPairK));
+  const int N = static_cast<int>(a.tokens), m_tiles = static_cast<int>(ceil_div(N, kPairM));
+  const int d_tiles = static_cast<int>(ceil_div(a.dim, BN)), d_blocks = static_cast<int>(ceil_div(a.dim, kPairK));
   float* meta = reinterpret_cast<float*>(ws + l.meta);
   const int* target = reinterpret_cast<const int*>(ws + l.target);
   T* dz = reinterpret_cast<T*>(ws + l.dz);
   float* sums = reinterpret_cast<float*>(ws + l.sums);
+  using Grad = Product<false, false, GradJob<T>>;
+  using Sum = Product<false, true, SumJob<BN>>;
+  using Out = Product<true, true, OutJob<T, BN>>;
+  const int aligned = a.dweight_stride % 16 == 0 && is_aligned(dweight, 32) ? 32 : a.dweight_stride % 8 == 0 && is_aligned(dweight, 16) ? 16 : 0;
   tbe_status st;
   for (int64_t first = 0; first < a.rows; first += l.piece) {
     const int live = static_cast<int>(a.rows - first < l.piece ? a.rows - first : l.piece);
     const int v_tiles = static_cast<int>(ceil_div(live, 256)), f = static_cast<int>(first);
-    PairShape g{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 0, a.stats};
-    typename GradJob<T>::Args ga{meta, reinterpret_cast<const float*>(ws + l.coef), reinterpret_cast<const float*>(ws + l.lse2), target,
-                                 dz, l.piece, N, f, live, a.scale * kLog2e};
-    if ((st = launch_pair<256, false, false, GradJob<T>>(maps[0], maps[1], g, ga, bf16, dev, s)) != TBE_OK) return st;
-    // dhidden: dz [tokens, piece] by weight [piece, dim]
-    g = PairShape{m_tiles, d_tiles, l.splits, static_cast<int>(ceil_div(live, kPairK)), 0, 0, 0, f, 0, a.stats};
-    if (bn == 128) {
-      SumJob<128>::Args sa{sums, l.dim_pad, N, first > 0};
-      st = launch_pair<128, false, true, SumJob<128>>(maps[2], maps[3], g, sa, bf16, dev, s);
-    } else {
-      SumJob<256>::Args sa{sums, l.dim_pad, N, first > 0};
-      st = launch_pair<256, false, true, SumJob<256>>(maps[2], maps[3], g, sa, bf16, dev, s);
-    }
-    if (st != TBE_OK) return st;
-    // dweight: dz^T [piece, tokens] by hidden [tokens, dim]
-    g = PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, 0, a.stats};
-    const int vec = a.dweight_stride % 8 == 0 && is_aligned(dweight, 16);
-    if (bn == 128) {
-      typename OutJob<T, 128>::Args oa{meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, a.dim, vec};
-      st = launch_pair<128, true, true, OutJob<T, 128>>(maps[4], maps[5], g, oa, bf16, dev, s);
-    } else {
-      typename OutJob<T, 256>::Args oa{meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, a.dim, vec};
-      st = launch_pair<256, true, true, OutJob<T, 256>>(maps[4], maps[5], g, oa, bf16, dev, s);
-    }
-    if (st != TBE_OK) return st;
+    typename Grad::Args ga{maps[0], maps[1], PairShape{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 0, pair_idesc(bf16, 256, false, false)},
+                           {meta, reinterpret_cast<const float*>(ws + l.coef), reinterpret_cast<const float*>(ws + l.lse2), target, dz,
+                            l.piece, N, f, live, a.scale * kLog2e}};
+    if ((st = launch_product<256, Grad>(ga, a, dev, s)) != TBE_OK) return st;
+    // dhidden += dz [tokens, piece] by weight [piece, dim];  dweight = dz^T [piece, tokens] by hidden [tokens, dim]
+    typename Sum::Args sa{maps[2], maps[3],
+                          PairShape{m_tiles, d_tiles, l.splits, static_cast<int>(ceil_div(live, kPairK)), 0, 0, 0, f, 0,
+                                    pair_idesc(bf16, BN, false, true)},
+                          {sums, l.dim_pad, N, first > 0}};
+    typename Out::Args oa{maps[4], maps[5],
+                          PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, 1, pair_idesc(bf16, BN, true, true)},
+                          {meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, a.dim, aligned}};
+    if ((st = launch_pair<BN, Sum, Out>(sa, oa, plan_two(sa.g, oa.g, a, dev), s)) != TBE_OK) return st;
   }
   FinishArgs<T> fa{sums, meta, target, static_cast<T*>(dhidden), a.tokens, l.dim_pad, a.dhidden_stride, l.splits, a.dim,
                    a.dhidden_stride % 8 == 0 && is_aligned(dhidden, 16)};
   int64_t blocks = ceil_div(a.tokens * (l.dim_pad / 8), 256);
   if (blocks > dev.sms * 8) blocks = dev.sms * 8;
-  loss_finish_kernel<T><<<static_cast<unsigned>(blocks), 256, 0, s>>>(fa);
-  note_launch();
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_after(loss_finish_kernel<T>, static_cast<unsigned>(blocks), 256, 0, s, fa));
+}
+
+template <typename T>
+tbe_status loss_backward_t(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, void* dhidden, void* dweight, char* ws,
+                           const DeviceInfo& dev, cudaStream_t s) {
+  if (gradient_bn(a.dim) == 128) return loss_backward<T, 128>(a, l, maps, dhidden, dweight, ws, dev, s);
+  return loss_backward<T, 256>(a, l, maps, dhidden, dweight, ws, dev, s);
 }
 
 }  // namespace
@@ -537,7 +628,7 @@ LossForwardLayout loss_forward_layout(const LossArgs& a) {
   LossForwardLayout l{};
   size_t at = 0;
   const int64_t dim_pad = round_up(a.dim, 8);
-  l.parts = static_cast<int>(2 * ceil_div(a.rows, 256));
+  l.parts = static_cast<int>(2 * ceil_div(a.rows, 256));  // two to a tile; fewer are used where the pairs join theirs
   l.parts_rows = round_up(a.tokens, 32);
   l.part = place(&at, l.parts * l.parts_rows * 8);
   l.target = place(&at, a.tokens * 4);
@@ -557,9 +648,12 @@ LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev
   if (most > (1 << 30)) most = 1 << 30;
   const int64_t pieces = ceil_div(a.rows, most);
   l.piece = round_up(ceil_div(a.rows, pieces), 256);
-  const int64_t tiles = ceil_div(a.tokens, kPairM) * ceil_div(a.dim, gradient_bn(a)), blocks = ceil_div(l.piece, kPairK);
-  int64_t splits = tiles > 0 ? dev.sms / 2 / tiles : 1;
-  if (splits > blocks / 4) splits = blocks / 4;
+  // Splits of dhidden's long sums: none of their tiles shall take more than half of a pair's share of a piece's blocks.
+  const int64_t d_tiles = ceil_div(a.dim, gradient_bn(a.dim)), blocks = ceil_div(l.piece, kPairK);
+  const int64_t tiles = ceil_div(a.tokens, kPairM) * d_tiles, pairs = dev.sms / 2;
+  const int64_t all = tiles * blocks + ceil_div(l.piece, 256) * d_tiles * ceil_div(a.tokens, kPairK);
+  int64_t splits = all > 0 ? ceil_div(2 * pairs * blocks, all) : 1;
+  if (splits > blocks / 2) splits = blocks / 2;
   // the last piece may be shorter: every split has to have a part of it
   const int64_t last = ceil_div(a.rows - (ceil_div(a.rows, l.piece) - 1) * l.piece, kPairK);
   if (splits > last) splits = last;
@@ -575,8 +669,8 @@ LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev
   const int64_t whole = a.tokens * round_up(a.rows, 256) * 2, least = a.tokens * 512;
   const int64_t capped = least > kPieceBytes ? least : kPieceBytes;
   l.dz = place(&at, whole < capped ? whole : capped);
-  const int64_t split = static_cast<int64_t>(dev.sms / 2) * kPairM * 256, once = a.tokens * l.dim_pad;  // splits * tiles <= sms / 2
-  l.sums = place(&at, (split > once ? split : once) * 4);
+  // splits * tiles < 2 pairs + tiles
+  l.sums = place(&at, (2 * pairs * kPairM * 256 + a.tokens * l.dim_pad) * 4);
   l.total = at;
   return l;
 }
@@ -606,16 +700,16 @@ tbe_status launch_loss_forward(const LossArgs& a, const LossForwardLayout& l, co
   uint32_t* ticket = reinterpret_cast<uint32_t*>(ws + l.ticket);
   float2* part = reinterpret_cast<float2*>(ws + l.part);
   float* target_logit = reinterpret_cast<float*>(ws + l.target);
-  const PairShape g{static_cast<int>(ceil_div(a.tokens, kPairM)), l.parts / 2, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, 0,
-                    a.stats};
-  const StatsJob::Args sa{targets, part, target_logit, ticket, l.parts_rows, a.rows, static_cast<int>(a.tokens), a.itype, a.scale,
-                          a.scale * kLog2e};
-  if ((st = launch_pair<256, false, false, StatsJob>(ma, mb, g, sa, bf16, dev, s)) != TBE_OK) return st;
+  using Stats = Product<false, false, StatsJob>;
+  const int m_tiles = static_cast<int>(ceil_div(a.tokens, kPairM)), v_tiles = l.parts / 2, pairs = dev.sms / 2;
+  const bool carry = m_tiles == 1 && v_tiles > pairs;
+  const Stats::Args sa{ma, mb, PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, 0, pair_idesc(bf16, 256, false, false)},
+                       {targets, part, target_logit, ticket, l.parts_rows, a.rows, static_cast<int>(a.tokens), a.itype, carry, a.scale,
+                        a.scale * kLog2e}};
+  if ((st = launch_product<256, Stats>(sa, a, dev, s)) != TBE_OK) return st;
   const JoinArgs ja{part, target_logit, targets, loss, lse, mean, reinterpret_cast<BlockSum*>(ws + l.ticket + 256), ticket, a.tokens,
-                    a.rows, l.parts_rows, l.parts, a.itype, a.stats};
-  loss_join_kernel<<<static_cast<unsigned>(ceil_div(a.tokens, kWarp)), kJoinThreads, 0, s>>>(ja);
-  note_launch();
-  return cuda_status(cudaGetLastError());
+                    a.rows, l.parts_rows, carry ? 2 * pairs : l.parts, a.itype, a.stats};
+  return cuda_status(launch_after(loss_join_kernel, static_cast<unsigned>(ceil_div(a.tokens, kWarp)), kJoinThreads, 0, s, ja));
 }
 
 tbe_status launch_loss_backward(const LossArgs& a, const LossBackwardLayout& l, const void* hidden, const void* weight,
@@ -644,8 +738,8 @@ tbe_status launch_loss_backward(const LossArgs& a, const LossBackwardLayout& l, 
       !encode_operand(&maps[2], dz, bf16, l.piece, a.tokens, l.piece, 128) || !encode_operand(&maps[3], weight, bf16, a.dim, a.rows, wst, 64) ||
       !encode_operand(&maps[4], dz, bf16, l.piece, a.tokens, l.piece, 64) || !encode_operand(&maps[5], h, bf16, a.dim, a.tokens, l.dim_pad, 64))
     return cuda_status(cudaErrorInvalidValue);
-  if (bf16) return loss_backward<__nv_bfloat16>(a, l, maps, h, dhidden, dweight, ws, dev, s);
-  return loss_backward<__half>(a, l, maps, h, dhidden, dweight, ws, dev, s);
+  if (bf16) return loss_backward_t<__nv_bfloat16>(a, l, maps, dhidden, dweight, ws, dev, s);
+  return loss_backward_t<__half>(a, l, maps, dhidden, dweight, ws, dev, s);
 }
 
 }  // namespace tbe

@@ -26,19 +26,30 @@ constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 32 * (kEpiWarps + 2);
 constexpr uint32_t kPairWaitLimit = 1u << 22;
 
+constexpr int kStageRow = 34;          // 16-bit elements from one row of a warp's staging area to the next: 17 words, no bank twice
+
 template <int BN>
 struct PairTile {
   static constexpr int kA = 128 * kPairK * 2;            // bytes of a CTA's part of a stage
   static constexpr int kB = BN / 2 * kPairK * 2;
   static constexpr int kStage = kA + kB;
   static constexpr int kStages = 196608 / kStage;        // 6 of 32 KB, 8 of 24 KB
-  static constexpr int kSmem = kStages * kStage + 1024;  // and room to align to the swizzle's 1024 bytes
+  static constexpr int kStaging = kEpiWarps * 32 * kStageRow * 2;       // 32 x 32 16-bit elements to a warp of the epilogue
+  static constexpr int kSmem = kStages * kStage + kStaging + 1024;      // and room to align to the swizzle's 1024 bytes
 };
 
+// A product: its tiles, and where it starts in A's and B's coordinates.
 struct PairShape {
-  int m_tiles, n_tiles, splits, k_blocks;  // k_blocks: of all splits together; splits <= k_blocks
-  int a_m0, a_k0, b_n0, b_k0;              // where the product starts in A's and B's coordinates
+  int m_tiles, n_tiles, splits, k_blocks;   // k_blocks: of all splits together; splits <= k_blocks
+  int a_m0, a_k0, b_n0, b_k0;
+  int n_first;      // tiles go along n first, else along m; splits come last
   uint32_t idesc;
+};
+
+// One or two products in a launch.  The pairs deal out the first one's tiles in turn; those that got one fewer (the lazy ones)
+// take `extra` tiles of the second before the rest is dealt out, to the lazy ones first if lazy_first.
+struct PairPlan {
+  int pairs, extra, lazy_first;
   unsigned long long* stats;
 };
 
@@ -118,22 +129,173 @@ struct Columns {
 
 }  // namespace pair
 
-// Job: `struct Args` and `tile(args, m, n, split, row, half, tmem)`: row = this thread's row of the tile (0 .. 255),
-// half = which half of the columns, tmem = the address of its first column.  All 32 lanes of a warp call it.
-template <int BN, bool AMN, bool BMN, class Job>
+// A tile, or a split's part of one: k blocks first .. last - 1.
+struct PairItem {
+  int m, n, split;
+  __device__ __forceinline__ int first(const PairShape& g) const { return static_cast<int>(static_cast<int64_t>(g.k_blocks) * split / g.splits); }
+  __device__ __forceinline__ int last(const PairShape& g) const { return static_cast<int>(static_cast<int64_t>(g.k_blocks) * (split + 1) / g.splits); }
+};
+
+// The tiles of a pair, in its order; every role of both CTAs walks them alike.
+struct PairWalk {
+  int item, end, stride;           // of the part being walked
+  int item2, end2, stride2;        // the other part, taken before
+  __device__ __forceinline__ static PairWalk first(int pair, const PairPlan& p, int items) {
+    return PairWalk{pair, items, p.pairs, 0, 0, 1};
+  }
+  __device__ __forceinline__ static PairWalk second(int pair, const PairPlan& p, int items0, int items1) {
+    const int busy = items0 % p.pairs, lazy = p.pairs - busy, taken = lazy * p.extra;
+    const int turn = p.lazy_first ? (pair + lazy) % p.pairs : pair;   // the lazy ones are busy .. pairs - 1
+    return PairWalk{taken + turn, items1, p.pairs, pair >= busy ? pair - busy : taken, taken, lazy};
+  }
+  __device__ __forceinline__ bool next(const PairShape& g, PairItem& i) {
+    int t;
+    if (item2 < end2) t = item2, item2 += stride2;
+    else if (item < end) t = item, item += stride;
+    else return false;
+    const int tiles = g.m_tiles * g.n_tiles;
+    i.split = g.splits > 1 ? t / tiles : 0;
+    t -= i.split * tiles;
+    if (g.n_first) i.m = t / g.n_tiles, i.n = t - i.m * g.n_tiles;
+    else i.n = t / g.m_tiles, i.m = t - i.n * g.m_tiles;
+    return true;
+  }
+};
+
+// A product with its epilogue.  Job:
+//   struct Args;  struct Row: what a thread needs of its row of a tile, Row::load(args, item, row) fetches it ahead;
+//   struct State: what a thread carries from tile to tile;
+//   tile(args, row_data, state, item, row, half, tmem, staging, release): row = this thread's row of the tile (0 .. 255), half =
+//     which half of the columns, tmem = the address of its first column; release() once the columns are in registers;
+//   finish(args, state, pair, row, half) after the last tile.  All 32 lanes of a warp call these together.
+template <bool A_MN, bool B_MN, class J>
+struct Product {
+  static constexpr bool kAMN = A_MN, kBMN = B_MN, kNone = false;
+  using Job = J;
+  struct Args {
+    CUtensorMap a, b;
+    PairShape g;
+    typename J::Args job;
+  };
+};
+struct NoProduct {
+  static constexpr bool kNone = true;
+  struct Args {
+    int none;
+  };
+};
+
+struct PairRole {
+  uint64_t *full, *empty, *acc_full, *acc_empty;
+  uint32_t ring, tmem, rank;
+  uint32_t it, tile;   // stages and tiles so far
+  bool failed;
+};
+
+template <int BN, class P>
+__device__ __forceinline__ void pair_copy(const typename P::Args& p, PairWalk walk, PairRole& r) {
+  using T = PairTile<BN>;
+  const PairShape& g = p.g;
+  PairItem i;
+  while (!r.failed && walk.next(g, i)) {
+    const int am = g.a_m0 + i.m * kPairM + static_cast<int>(r.rank) * 128, bn = g.b_n0 + i.n * BN + static_cast<int>(r.rank) * (BN / 2);
+    const int last = i.last(g);
+    for (int kb = i.first(g); kb < last; ++kb, ++r.it) {
+      const uint32_t st = r.it % T::kStages;
+      if (!mbar_wait_bounded(&r.empty[st], ((r.it / T::kStages) & 1) ^ 1, kPairWaitLimit)) {
+        r.failed = true;
+        return;
+      }
+      if (r.rank == 0) mbar_arrive_expect_tx(&r.full[st], 2 * T::kStage);
+      const uint32_t bar = pair::in_leader(smem_u32(&r.full[st])), a = r.ring + st * T::kStage, b = a + T::kA;
+      const int ak = g.a_k0 + kb * kPairK, bk = g.b_k0 + kb * kPairK;
+      if constexpr (P::kAMN) {
+        pair::tma_2d(a, &p.a, am, ak, bar);
+        pair::tma_2d(a + 8192, &p.a, am + 64, ak, bar);
+      } else {
+        pair::tma_2d(a, &p.a, ak, am, bar);
+      }
+      if constexpr (P::kBMN) {
+#pragma unroll
+        for (int x = 0; x < BN / 128; ++x) pair::tma_2d(b + x * 8192, &p.b, bn + x * 64, bk, bar);
+      } else {
+        pair::tma_2d(b, &p.b, bk, bn, bar);
+      }
+    }
+  }
+}
+
+template <int BN, class P>
+__device__ __forceinline__ void pair_multiply(const typename P::Args& p, PairWalk walk, PairRole& r) {
+  using T = PairTile<BN>;
+  PairItem i;
+  for (; !r.failed && walk.next(p.g, i); ++r.tile) {
+    const uint32_t buf = r.tile & 1, d = r.tmem + buf * 256;
+    if (!mbar_wait_bounded(&r.acc_empty[buf], ((r.tile >> 1) & 1) ^ 1, kPairWaitLimit)) {
+      r.failed = true;
+      return;
+    }
+    pair::fence_after();
+    const int first = i.first(p.g), last = i.last(p.g);
+    for (int kb = first; kb < last; ++kb, ++r.it) {
+      const uint32_t st = r.it % T::kStages;
+      if (!mbar_wait_bounded(&r.full[st], (r.it / T::kStages) & 1, kPairWaitLimit)) {
+        r.failed = true;
+        return;
+      }
+      pair::fence_after();
+      const uint64_t a = pair::operand_desc<P::kAMN>(r.ring + st * T::kStage), b = pair::operand_desc<P::kBMN>(r.ring + st * T::kStage + T::kA);
+#pragma unroll
+      for (int k = 0; k < kPairK / 16; ++k)  // 16 k's: 32 bytes along a row, or two groups of 8 rows
+        pair::mma(d, a + k * ((P::kAMN ? 2048 : 32) >> 4), b + k * ((P::kBMN ? 2048 : 32) >> 4), p.g.idesc, kb > first || k > 0);
+      pair::commit_both(&r.empty[st]);
+    }
+    pair::commit_both(&r.acc_full[buf]);
+  }
+}
+
+template <int BN, class P>
+__device__ __forceinline__ void pair_epilogue(const typename P::Args& p, PairWalk walk, PairRole& r, int pair, int w, int lane,
+                                              uint16_t* staging) {
+  using Job = typename P::Job;
+  const int row = static_cast<int>(r.rank) * 128 + (w % 4) * 32 + lane, half = w / 4;
+  typename Job::State state{};
+  PairItem i{}, next{};
+  bool more = walk.next(p.g, i);
+  typename Job::Row now{}, then{};
+  if (more) now.load(p.job, i, row);
+  while (more) {
+    more = walk.next(p.g, next);
+    if (more) then.load(p.job, next, row);   // the next tile's, while this one is waited for and worked on
+    const uint32_t buf = r.tile & 1;
+    r.failed = !mbar_wait_bounded(&r.acc_full[buf], (r.tile >> 1) & 1, kPairWaitLimit);
+    r.failed = __any_sync(0xffffffffu, r.failed);
+    if (r.failed) return;
+    pair::fence_after();
+    const uint32_t empty = pair::in_leader(smem_u32(&r.acc_empty[buf]));
+    Job::tile(p.job, now, state, i, row, half, r.tmem + buf * 256 + half * (BN / 2) + (static_cast<uint32_t>((w % 4) * 32) << 16), staging,
+              [&] {
+                pair::fence_before();
+                __syncwarp();
+                if (lane == 0) pair::arrive_at(empty);
+              });
+    now = then, i = next, ++r.tile;
+  }
+  Job::finish(p.job, state, pair, row, half);
+}
+
+template <int BN, class P0, class P1>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    pair_mma_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const __grid_constant__ PairShape g, const __grid_constant__ typename Job::Args args) {
+    pair_mma_kernel(const __grid_constant__ typename P0::Args p0, const __grid_constant__ typename P1::Args p1,
+                    const __grid_constant__ PairPlan plan) {
   using T = PairTile<BN>;
   constexpr int ST = T::kStages;
   extern __shared__ uint8_t s_raw[];
   __shared__ __align__(8) uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2];
   __shared__ uint32_t s_tmem;
   const uint32_t ring = (smem_u32(s_raw) + 1023u) & ~1023u;
-  const int w = threadIdx.x / kWarp, lane = lane_id();
-  const uint32_t rank = cluster_rank();
-  const int pair_id = blockIdx.x / 2, pairs = gridDim.x / 2;
-  const int items = g.m_tiles * g.n_tiles * g.splits;
+  const int w = threadIdx.x / kWarp, lane = lane_id(), pair_id = blockIdx.x / 2;
+  may_follow();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
@@ -148,100 +310,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist
   pair::fence_after();
-  const uint32_t tmem = s_tmem;
-  bool failed = false;
+  PairRole r{full, empty, acc_full, acc_empty, ring, s_tmem, cluster_rank(), 0, 0, false};
+  const int items0 = p0.g.m_tiles * p0.g.n_tiles * p0.g.splits;
+  const PairWalk walk0 = PairWalk::first(pair_id, plan, items0);
+  PairWalk walk1 = walk0;
+  if constexpr (!P1::kNone) walk1 = PairWalk::second(pair_id, plan, items0, p1.g.m_tiles * p1.g.n_tiles * p1.g.splits);
+  wait_before();  // what this kernel reads is complete from here on
 
   if (w == kEpiWarps) {
-    if (lane == 0) {  // copies
-      uint32_t it = 0;
-      for (int item = pair_id; item < items && !failed; item += pairs) {
-        const int m = item % g.m_tiles, rest = item / g.m_tiles, n = rest % g.n_tiles, s = rest / g.n_tiles;
-        const int am = g.a_m0 + m * kPairM + static_cast<int>(rank) * 128, bn = g.b_n0 + n * BN + static_cast<int>(rank) * (BN / 2);
-        const int k1 = static_cast<int>(static_cast<int64_t>(g.k_blocks) * (s + 1) / g.splits);
-        for (int kb = static_cast<int>(static_cast<int64_t>(g.k_blocks) * s / g.splits); kb < k1; ++kb, ++it) {
-          const uint32_t st = it % ST;
-          if (!mbar_wait_bounded(&empty[st], ((it / ST) & 1) ^ 1, kPairWaitLimit)) {
-            failed = true;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * T::kStage);
-          const uint32_t bar = pair::in_leader(smem_u32(&full[st])), a = ring + st * T::kStage, b = a + T::kA;
-          const int ak = g.a_k0 + kb * kPairK, bk = g.b_k0 + kb * kPairK;
-          if constexpr (AMN) {
-            pair::tma_2d(a, &map_a, am, ak, bar);
-            pair::tma_2d(a + 8192, &map_a, am + 64, ak, bar);
-          } else {
-            pair::tma_2d(a, &map_a, ak, am, bar);
-          }
-          if constexpr (BMN) {
-#pragma unroll
-            for (int x = 0; x < BN / 128; ++x) pair::tma_2d(b + x * 8192, &map_b, bn + x * 64, bk, bar);
-          } else {
-            pair::tma_2d(b, &map_b, bk, bn, bar);
-          }
-        }
-      }
+    if (lane == 0) {
+      pair_copy<BN, P0>(p0, walk0, r);
+      if constexpr (!P1::kNone) pair_copy<BN, P1>(p1, walk1, r);
       // Copies must not be in flight when a CTA ends: in the even CTA, whose barriers count both CTAs' copies, the last
       // round of every stage has landed (its products are done by then, unless a wait gave up).
-      if (rank == 0)
-        for (uint32_t k = it < ST ? 0 : it - ST; k < it; ++k)
-          failed = !mbar_wait_bounded(&full[k % ST], (k / ST) & 1, kPairWaitLimit) || failed;
+      if (r.rank == 0)
+        for (uint32_t k = r.it < ST ? 0 : r.it - ST; k < r.it; ++k)
+          r.failed = !mbar_wait_bounded(&full[k % ST], (k / ST) & 1, kPairWaitLimit) || r.failed;
     }
     __syncwarp();
   } else if (w == kEpiWarps + 1) {
-    if (rank == 0 && lane == 0) {  // products
-      uint32_t it = 0, tile = 0;
-      for (int item = pair_id; item < items && !failed; item += pairs, ++tile) {
-        const int s = item / g.m_tiles / g.n_tiles;
-        const int k0 = static_cast<int>(static_cast<int64_t>(g.k_blocks) * s / g.splits);
-        const int k1 = static_cast<int>(static_cast<int64_t>(g.k_blocks) * (s + 1) / g.splits);
-        const uint32_t buf = tile & 1, d = tmem + buf * 256;
-        if (!mbar_wait_bounded(&acc_empty[buf], ((tile >> 1) & 1) ^ 1, kPairWaitLimit)) {
-          failed = true;
-          break;
-        }
-        pair::fence_after();
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const uint32_t st = it % ST;
-          if (!mbar_wait_bounded(&full[st], (it / ST) & 1, kPairWaitLimit)) {
-            failed = true;
-            break;
-          }
-          pair::fence_after();
-          const uint64_t a = pair::operand_desc<AMN>(ring + st * T::kStage), b = pair::operand_desc<BMN>(ring + st * T::kStage + T::kA);
-#pragma unroll
-          for (int k = 0; k < kPairK / 16; ++k)  // 16 k's: 32 bytes along a row, or two groups of 8 rows
-            pair::mma(d, a + k * ((AMN ? 2048 : 32) >> 4), b + k * ((BMN ? 2048 : 32) >> 4), g.idesc, kb > k0 || k > 0);
-          pair::commit_both(&empty[st]);
-        }
-        pair::commit_both(&acc_full[buf]);
-      }
+    if (r.rank == 0 && lane == 0) {
+      pair_multiply<BN, P0>(p0, walk0, r);
+      if constexpr (!P1::kNone) pair_multiply<BN, P1>(p1, walk1, r);
     }
     __syncwarp();
   } else {
-    uint32_t tile = 0;
-    const int row = static_cast<int>(rank) * 128 + (w % 4) * 32 + lane, half = w / 4;
-    for (int item = pair_id; item < items; item += pairs, ++tile) {
-      const int m = item % g.m_tiles, rest = item / g.m_tiles, n = rest % g.n_tiles, s = rest / g.n_tiles;
-      const uint32_t buf = tile & 1;
-      failed = !mbar_wait_bounded(&acc_full[buf], (tile >> 1) & 1, kPairWaitLimit);
-      if (__any_sync(0xffffffffu, failed)) {
-        failed = true;
-        break;
-      }
-      pair::fence_after();
-      Job::tile(args, m, n, s, row, half, tmem + buf * 256 + half * (BN / 2) + (static_cast<uint32_t>((w % 4) * 32) << 16));
-      pair::fence_before();
-      __syncwarp();
-      if (lane == 0) pair::arrive_at(pair::in_leader(smem_u32(&acc_empty[buf])));
-    }
+    uint16_t* staging = reinterpret_cast<uint16_t*>(s_raw + (ring - smem_u32(s_raw)) + ST * T::kStage) + w * 32 * kStageRow;
+    pair_epilogue<BN, P0>(p0, walk0, r, pair_id, w, lane, staging);
+    if constexpr (!P1::kNone)
+      if (!r.failed) pair_epilogue<BN, P1>(p1, walk1, r, pair_id, w, lane, staging);
   }
-  if (failed && lane == 0) stat_add(g.stats, TBE_STAT_WAIT_TIMEOUT, 1);
+  if (r.failed && lane == 0) stat_add(plan.stats, TBE_STAT_WAIT_TIMEOUT, 1);
   __syncwarp();
   pair::fence_before();
   cluster_sync();  // neither CTA ends, or frees its TMEM, while the other may still reach it
   pair::fence_after();
-  if (w == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (w == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(r.tmem) : "memory");
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // NULL where the driver has none
