@@ -64,8 +64,10 @@ namespace pair {
 
 // The same place in the even CTA's shared memory.
 __device__ __forceinline__ uint32_t in_leader(uint32_t addr) { return cluster_address(addr, 0); }
+// Orders this thread's shared memory accesses of its own CTA at most: what it has read of TMEM is ordered by fence_before, and a
+// release to the cluster would wait for the epilogue's global stores (a quarter of a small product's time).
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
