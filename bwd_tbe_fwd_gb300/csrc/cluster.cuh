@@ -1,6 +1,8 @@
 // cluster.cuh -- thread-block clusters: a CTA's place in one, and its barrier.
 #pragma once
 
+#include <atomic>
+
 #include "tbe_internal.cuh"
 
 namespace tbe {
@@ -40,6 +42,20 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t addr, uint32_t cta)
 // only after wait_before, which waits until they are complete and their writes visible.
 __device__ __forceinline__ void may_follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The most dynamic shared memory that a kernel may ask for, set once for each device (a launch needs it, and the call takes as long
+// as half a launch).  `done`: a word of the caller's own for this kernel, zero at first.
+template <typename K>
+cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (f == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return f;
+}
 
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A&&... args) {

@@ -587,10 +587,11 @@ int tokens_per_warp(const LookupArgs& a, int slabs, const DeviceInfo& dev) {
 // One cluster sorts; where there is a gradient to set to zero, others do that: as many as run beside it (a cluster lies within one
 // of the GPU's processing clusters, so that 19 clusters of 8 do not fit 152 SMs at once, and each takes an equal share).
 template <int IPT>
-tbe_status launch_cluster_sort_t(const ClusterSortArgs& c, int ctas, int64_t zero, cudaStream_t s) {
+tbe_status launch_cluster_sort_t(const ClusterSortArgs& c, int ctas, int64_t zero, const DeviceInfo& dev, cudaStream_t s) {
   auto* kernel = lookup_sort_kernel<IPT>;
   const size_t smem = cluster_sort_smem(IPT);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kernel, smem, allowed);
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -603,9 +604,15 @@ tbe_status launch_cluster_sort_t(const ClusterSortArgs& c, int ctas, int64_t zer
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (zero > 0) {
-    int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
-    if (e != cudaSuccess) return cuda_status(e);
+    static std::atomic<int> known[64][4];   // by device and cluster size; 0: not asked yet
+    const int size = ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3;
+    std::atomic<int>* slot = dev.id < 64 ? &known[dev.id][size] : nullptr;
+    int clusters = slot != nullptr ? slot->load(std::memory_order_relaxed) : 0;
+    if (clusters == 0) {
+      e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+      if (e != cudaSuccess) return cuda_status(e);
+      if (slot != nullptr) slot->store(clusters, std::memory_order_relaxed);
+    }
     const int64_t others = ceil_div(zero, ctas) < clusters - 1 ? ceil_div(zero, ctas) : clusters - 1;
     cfg.gridDim.x = static_cast<unsigned>(ctas * (1 + (others > 1 ? others : 1)));
   }
@@ -628,10 +635,10 @@ tbe_status launch_cluster_sort(const LookupArgs& a, const KeyArgs& k, void* grad
   while (ctas < kMaxCluster && ctas * kClusterThreads < a.tokens) ctas *= 2;
   const int64_t per_thread = ceil_div(a.tokens, static_cast<int64_t>(ctas) * kClusterThreads);
   const int64_t zero = grad == nullptr ? 0 : ceil_div(a.rows * row_bytes, 2 * kZeroPiece);
-  if (per_thread <= 1) return launch_cluster_sort_t<1>(c, ctas, zero, s);
-  if (per_thread <= 2) return launch_cluster_sort_t<2>(c, ctas, zero, s);
-  if (per_thread <= 4) return launch_cluster_sort_t<4>(c, ctas, zero, s);
-  return launch_cluster_sort_t<kMaxPerThread>(c, ctas, zero, s);
+  if (per_thread <= 1) return launch_cluster_sort_t<1>(c, ctas, zero, dev, s);
+  if (per_thread <= 2) return launch_cluster_sort_t<2>(c, ctas, zero, dev, s);
+  if (per_thread <= 4) return launch_cluster_sort_t<4>(c, ctas, zero, dev, s);
+  return launch_cluster_sort_t<kMaxPerThread>(c, ctas, zero, dev, s);
 }
 
 }  // namespace

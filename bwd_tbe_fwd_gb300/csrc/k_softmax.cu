@@ -27,6 +27,12 @@ __device__ __forceinline__ int load_target(const void* targets, int itype, int64
   return t >= 0 && t < rows ? static_cast<int>(t) : -1;
 }
 
+// Rows of the selected tokens with those that fill up the last block of k (which are zeros), as far as there are rows at all.
+__device__ __forceinline__ int filled(int live, int64_t tokens) {
+  const int64_t n = (static_cast<int64_t>(live > 1 ? live : 1) + kPairK - 1) / kPairK * kPairK;
+  return static_cast<int>(n < tokens ? n : tokens);
+}
+
 // 32 bytes at p, which is aligned to them.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
@@ -61,6 +67,8 @@ __device__ __forceinline__ void each_columns(uint32_t tmem, R&& release, F&& f) 
 struct StatsJob {
   struct Args {
     const void* targets;
+    const int* selected;   // NULL, or the targets of the tokens that count, one after the other
+    const int* live;       // ... and how many they are
     float2* part;          // [parts][parts_rows]
     float* target_logit;   // [tokens]
     uint32_t* ticket;      // set to 0 for the kernel that joins the parts
@@ -73,7 +81,12 @@ struct StatsJob {
     int target;
     __device__ __forceinline__ void load(const Args& a, const PairItem& it, int row) {
       const int i = it.m * kPairM + row;
-      target = i < a.tokens ? load_target(a.targets, a.itype, i, a.rows) : -1;
+      target = -1;
+      if (a.selected != nullptr) {
+        if (i < *a.live) target = a.selected[i];
+      } else if (i < a.tokens) {
+        target = load_target(a.targets, a.itype, i, a.rows);
+      }
     }
   };
   struct State {
@@ -125,27 +138,31 @@ struct StatsJob {
   }
 };
 
-// dz = c (p - onehot), times the power of two that keeps it in 16 bits.
+// dz = c (p - onehot), times the power of two that keeps it in 16 bits, for the selected tokens; zeros in the rows that fill up the
+// last block of k.
 template <typename T>
 struct GradJob {
   struct Args {
     const float* meta;     // {power of two, ...}
-    const float* coef;     // [tokens]; 0 where the token does not count
-    const float* lse2;     // [tokens] lse in powers of 2
-    const int* target;     // [tokens], -1 where the token does not count
+    const int* live;       // how many tokens are selected
+    const float* coef;     // of the selected tokens
+    const float* lse2;     // lse in powers of 2
+    const int* target;     // -1 in the rows that fill up
     T* dz;                 // [tokens][ld]
     int64_t ld;
-    int tokens, first, live;   // first row of the piece, rows of the table from there on
+    int tokens, first, here;   // first row of the piece, rows of the table from there on
     float scale2;
   };
   struct Row {
     int target;
     float coef, lse2, power;
+    bool in;
     __device__ __forceinline__ void load(const Args& a, const PairItem& it, int row) {
       const int i = it.m * kPairM + row;
       target = -1, coef = 0.0f, lse2 = 0.0f;
       power = a.meta[0];
-      if (i < a.tokens) target = a.target[i], coef = a.coef[i], lse2 = a.lse2[i];
+      in = i < filled(*a.live, a.tokens);
+      if (in) target = a.target[i], coef = a.coef[i], lse2 = a.lse2[i];
     }
   };
   using State = NoState;
@@ -153,7 +170,6 @@ struct GradJob {
   static __device__ __forceinline__ void tile(const Args& a, const Row& r, State&, const PairItem& it, int row, int half, uint32_t tmem,
                                               uint16_t*, R&& release) {
     const int i = it.m * kPairM + row;
-    const bool in = i < a.tokens;
     const int col0 = it.n * 256 + half * 128, t = r.target;
     const int tl = t < 0 ? -1 : t - a.first - col0;
     const float g = r.coef * r.power, ref = r.lse2;
@@ -169,11 +185,11 @@ struct GradJob {
       }
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= g;
-      if (t < 0 || col0 + j * 32 + 32 > a.live) {  // no gradient: zeros, whatever the logits are
+      if (t < 0 || col0 + j * 32 + 32 > a.here) {  // no gradient: zeros, whatever the logits are
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = t < 0 || col0 + j * 32 + k >= a.live ? 0.0f : v[k];
+        for (int k = 0; k < 32; ++k) v[k] = t < 0 || col0 + j * 32 + k >= a.here ? 0.0f : v[k];
       }
-      if (in) {
+      if (r.in) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           float f[16];
@@ -196,18 +212,29 @@ struct OutJob {
     const float* meta;     // {.., alpha}
     T* out;
     int64_t stride, first, rows;   // first row of the product in `out`, rows of out
+    const int* place;      // NULL, or the row of out for each row of the product, of which there are *live
+    const int* live;
     int cols;
     int vec;               // bytes of a store that every row allows: 32, 16, or 0 for element by element
   };
   struct Row {
     float alpha;
-    __device__ __forceinline__ void load(const Args& a, const PairItem&, int) { alpha = a.meta[1]; }
+    int64_t out;           // row of out, or -1
+    __device__ __forceinline__ void load(const Args& a, const PairItem& it, int row) {
+      alpha = a.meta[1];
+      const int64_t i = a.first + static_cast<int64_t>(it.m) * kPairM + row;
+      out = -1;
+      if (a.place != nullptr) {
+        if (i < *a.live) out = a.place[i];
+      } else if (i < a.rows) {
+        out = i;
+      }
+    }
   };
   using State = NoState;
   template <typename R>
   static __device__ __forceinline__ void tile(const Args& a, const Row& r, State&, const PairItem& it, int row, int half, uint32_t tmem,
                                               uint16_t* staging, R&& release) {
-    const int64_t i = a.first + static_cast<int64_t>(it.m) * kPairM + row;
     const int col0 = it.n * BN + half * (BN / 2), lane = lane_id();
     each_columns<BN / 2>(tmem, release, [&](int j, pair::Columns& c) {
       const int left = a.cols - col0 - j * 32;   // columns from this block's first on; the same for the whole warp
@@ -221,8 +248,8 @@ struct OutJob {
         p[q].set(f);
       }
       if (a.vec != 0 && left >= 32) {
-        T* dst = a.out + i * a.stride + col0 + j * 32;
-        if (i < a.rows) {
+        T* dst = a.out + r.out * a.stride + col0 + j * 32;
+        if (r.out >= 0) {
           if (a.vec == 32) store32(dst, p[0].w), store32(dst + 16, p[1].w);
           else p[0].store(dst), p[1].store(dst + 16);
         }
@@ -233,11 +260,12 @@ struct OutJob {
 #pragma unroll
       for (int k = 0; k < 16; ++k) mine[k] = p[k / 8].w[k % 8];
       __syncwarp();
-      const int64_t i0 = i - lane;
-      const int rows = static_cast<int>(a.rows - i0 < 32 ? a.rows - i0 : 32);
-      uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + i0 * a.stride + col0 + j * 32 + lane;
-      if (lane < left)
-        for (int x = 0; x < rows; ++x) dst[x * a.stride] = staging[x * kStageRow + lane];
+      uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + col0 + j * 32 + lane;
+#pragma unroll 4
+      for (int x = 0; x < 32; ++x) {
+        const int64_t to = __shfl_sync(kFull, r.out, x);
+        if (to >= 0 && lane < left) dst[to * a.stride] = staging[x * kStageRow + lane];
+      }
       __syncwarp();
     });
   }
@@ -286,31 +314,124 @@ struct SumJob {
 // ------------------------------------------------------------------------------------------
 // Before and after the products
 // ------------------------------------------------------------------------------------------
-constexpr int kPrepThreads = 256;
-
-struct PrepArgs {
-  int64_t tokens, rows, hidden_stride, weight_stride;
-  int64_t hidden_rows, weight_rows;   // rows to copy: tokens or 0, rows or 0
-  const uint16_t* hidden;
-  const uint16_t* weight;
-  uint16_t* hidden_copy;              // [.][dim_pad], rows of tokens that do not count as zeros
-  uint16_t* weight_copy;
-  int dim, dim_pad, itype;
-  int backward;                       // block 0 finds the power of two; the tokens' constants are laid out
+// The tokens whose target is a row of the table, in their order, and what the products need of them: the others take no part in
+// any product, so that a batch with a third of padding costs a third less, and what their hidden rows hold is not looked at.
+struct SelectArgs {
   const void* targets;
+  int64_t tokens, rows;
+  int itype;
+  int* live;         // how many
+  int* place;        // [selected] the token
+  int* target;       // [selected] its target; -1 in the rows that fill up the last block of k
+  int* row;          // [tokens] where a token is among the selected, or -1
+  // backward
   const float* lse;
   const float* dloss;
   const float* mean;
   float scale;
-  float* meta;
-  float* coef;
-  float* lse2;
-  int* target;
+  float* meta;       // {power of two that scales dz, scale over it}
+  float* coef;       // [selected]
+  float* lse2;       // [selected] lse in powers of 2
+  unsigned long long* stats;
 };
 
-__device__ __forceinline__ float coefficient(const PrepArgs& a, int64_t i) {
-  return (a.dloss != nullptr ? a.dloss[i] : 1.0f) * (a.mean != nullptr ? a.mean[1] : 1.0f);
+__device__ __forceinline__ float coefficient(const SelectArgs& a, int64_t i, float mean) {
+  return (a.dloss != nullptr ? a.dloss[i] : 1.0f) * mean;
 }
+
+constexpr int kSelectThreads = 1024;
+constexpr int kCopyThreads = 256;
+
+// One CTA, 4 tokens to a thread at a time (8192 tokens: 4 us).
+template <bool BACKWARD>
+__global__ void __launch_bounds__(kSelectThreads) loss_select_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int kEach = 4, kWarps = kSelectThreads / kWarp;
+  __shared__ int s_count[kWarps];
+  __shared__ float s_top[kWarps];
+  const int lane = lane_id(), w = threadIdx.x / kWarp;
+  may_follow();
+  const float mean = BACKWARD && a.mean != nullptr ? a.mean[1] : 1.0f;
+  int base = 0;
+  float top = 0.0f;
+  for (int64_t i0 = 0; i0 < a.tokens; i0 += kSelectThreads * kEach) {
+    const int64_t i = i0 + threadIdx.x * kEach;
+    int t[kEach], mine = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) t[k] = i + k < a.tokens ? load_target(a.targets, a.itype, i + k, a.rows) : -1;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) mine += t[k] >= 0;
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, before, o);
+      if (lane >= o) before += y;
+    }
+    if (lane == kWarp - 1) s_count[w] = before;
+    __syncthreads();
+    int sum = s_count[lane];
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const int all = __shfl_sync(kFull, sum, kWarps - 1), warps = __shfl_sync(kFull, sum, w > 0 ? w - 1 : 0);
+    int j = base + before - mine + (w > 0 ? warps : 0);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      if (i + k < a.tokens) a.row[i + k] = t[k] >= 0 ? j : -1;
+      if (t[k] < 0) continue;
+      a.place[j] = static_cast<int>(i + k);
+      a.target[j] = t[k];
+      if (BACKWARD) {
+        const float c = coefficient(a, i + k, mean), size = fabsf(c);
+        a.coef[j] = c;
+        a.lse2[j] = a.lse[i + k] * kLog2e;
+        if (size <= FLT_MAX) top = fmaxf(top, size);
+      }
+      ++j;
+    }
+    base += all;
+    __syncthreads();
+  }
+  for (int j = base + threadIdx.x; j < filled(base, a.tokens); j += kSelectThreads) {
+    a.target[j] = -1;
+    if (BACKWARD) a.coef[j] = 0.0f, a.lse2[j] = 0.0f;
+  }
+  if (threadIdx.x == 0) *a.live = base;
+  if constexpr (BACKWARD) {
+    // The largest finite coefficient takes dz to 2^13 .. 2^14: |p - onehot| is at most 1, fp16 ends at 2^16, and what is
+    // 2^-27 of the largest is still a normal number there.
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    if (lane == 0) s_top[w] = top;
+    __syncthreads();
+    if (w != 0) return;
+    top = s_top[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    if (lane == 0) {
+      int e = top > 0.0f ? 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127) : 0;
+      e = e < -100 ? -100 : e > 100 ? 100 : e;
+      a.meta[0] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+      a.meta[1] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
+  }
+}
+
+// Rows copied to where TMA can address them (and, of hidden, those of the selected tokens one after the other, with zeros in the
+// rows that fill up the last block of k), and zeros in the rows of dhidden of the tokens that are not selected.
+struct CopyArgs {
+  const int* live;      // with place and row: of loss_select_kernel; NULL for all tokens
+  const int* place;
+  const int* row;
+  const uint16_t* hidden;
+  const uint16_t* weight;
+  uint16_t* hidden_copy;   // [.][dim_pad]
+  uint16_t* weight_copy;   // NULL: none
+  uint16_t* dhidden;       // NULL: none
+  int64_t tokens, rows, hidden_stride, weight_stride, dhidden_stride;
+  int dim, dim_pad;
+};
 
 // 8 elements of a row from column c on, zeros past its end.
 __device__ __forceinline__ uint4 row_piece(const uint16_t* src, int c, int dim, bool vec) {
@@ -321,10 +442,10 @@ __device__ __forceinline__ uint4 row_piece(const uint16_t* src, int c, int dim, 
   return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
-// Copies rows to where TMA can address them, 8 elements to a thread, two at a time; rows of tokens that do not count as zeros
-// where targets are given.
+// 8 elements to a thread, two at a time; from(r): the row of src that is row r of dst, or -1 for zeros.
+template <typename F>
 __device__ __forceinline__ void copy_rows(uint16_t* dst, const uint16_t* src, int64_t rows, int64_t stride, int dim, int dim_pad,
-                                          const PrepArgs* mask, int64_t t, int64_t n) {
+                                          int64_t t, int64_t n, F&& from) {
   const int groups = dim_pad / 8;
   const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && dim % 8 == 0 && stride % 8 == 0;
   const int64_t total = rows * groups;
@@ -336,8 +457,8 @@ __device__ __forceinline__ void copy_rows(uint16_t* dst, const uint16_t* src, in
       v[u] = make_uint4(0, 0, 0, 0);
       if (x >= total) continue;
       const int64_t r = total >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(groups) : x / groups;
-      if (mask == nullptr || load_target(mask->targets, mask->itype, r, mask->rows) >= 0)
-        v[u] = row_piece(src + r * stride, static_cast<int>(x - r * groups) * 8, dim, vec);
+      const int64_t f = from(r);
+      if (f >= 0) v[u] = row_piece(src + f * stride, static_cast<int>(x - r * groups) * 8, dim, vec);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -345,41 +466,23 @@ __device__ __forceinline__ void copy_rows(uint16_t* dst, const uint16_t* src, in
   }
 }
 
-__global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const __grid_constant__ PrepArgs a) {
-  const int lane = lane_id(), w = threadIdx.x / kWarp;
+__global__ void __launch_bounds__(kCopyThreads) loss_copy_kernel(const __grid_constant__ CopyArgs a) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, n = static_cast<int64_t>(gridDim.x) * kCopyThreads;
   may_follow();
-  const int block = static_cast<int>(blockIdx.x) - a.backward, blocks = static_cast<int>(gridDim.x) - a.backward;
-  if (block < 0) {
-    // The largest finite coefficient takes dz to 2^13 .. 2^14: |p - onehot| is at most 1, fp16 ends at 2^16, and what is
-    // 2^-38 of the largest is still a normal number there.
-    __shared__ float s_top[kPrepThreads / kWarp];
-    float top = 0.0f;
-    for (int64_t i = threadIdx.x; i < a.tokens; i += kPrepThreads) {
-      const float c = fabsf(coefficient(a, i));
-      if (load_target(a.targets, a.itype, i, a.rows) >= 0 && c <= FLT_MAX) top = fmaxf(top, c);
-    }
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    if (lane == 0) s_top[w] = top;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int k = 1; k < kPrepThreads / kWarp; ++k) top = fmaxf(top, s_top[k]);
-      int e = top > 0.0f ? 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127) : 0;
-      e = e < -100 ? -100 : e > 100 ? 100 : e;
-      a.meta[0] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      a.meta[1] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    }
+  wait_before();
+  if (a.weight_copy != nullptr)
+    copy_rows(a.weight_copy, a.weight, a.rows, a.weight_stride, a.dim, a.dim_pad, t, n, [](int64_t r) { return r; });
+  if (a.live == nullptr) {
+    copy_rows(a.hidden_copy, a.hidden, a.tokens, a.hidden_stride, a.dim, a.dim_pad, t, n, [](int64_t r) { return r; });
     return;
   }
-  const int64_t t = static_cast<int64_t>(block) * kPrepThreads + threadIdx.x, n = static_cast<int64_t>(blocks) * kPrepThreads;
-  if (a.backward)
-    for (int64_t i = t; i < a.tokens; i += n) {
-      const int target = load_target(a.targets, a.itype, i, a.rows);
-      a.target[i] = target;
-      a.coef[i] = target >= 0 ? coefficient(a, i) : 0.0f;
-      a.lse2[i] = target >= 0 ? a.lse[i] * kLog2e : 0.0f;
-    }
-  copy_rows(a.hidden_copy, a.hidden, a.hidden_rows, a.hidden_stride, a.dim, a.dim_pad, &a, t, n);
-  copy_rows(a.weight_copy, a.weight, a.weight_rows, a.weight_stride, a.dim, a.dim_pad, nullptr, t, n);
+  const int live = *a.live;
+  copy_rows(a.hidden_copy, a.hidden, filled(live, a.tokens), a.hidden_stride, a.dim, a.dim_pad, t, n,
+            [&](int64_t r) { return r < live ? static_cast<int64_t>(a.place[r]) : int64_t(-1); });
+  if (a.dhidden == nullptr || live == a.tokens) return;
+  for (int64_t i = t / kWarp; i < a.tokens; i += n / kWarp)
+    if (a.row[i] < 0)
+      for (int c = static_cast<int>(t % kWarp); c < a.dim; c += kWarp) a.dhidden[i * a.dhidden_stride + c] = 0;
 }
 
 // Joins the parts of 32 tokens' rows, a lane to a token, the parts dealt out to the warps; the last block adds up the losses.
@@ -393,6 +496,7 @@ struct JoinArgs {
   const float2* part;
   const float* target_logit;
   const void* targets;
+  const int* row;          // NULL, or where a token is among the selected
   float* loss;
   float* lse;
   float* mean;
@@ -403,6 +507,11 @@ struct JoinArgs {
   unsigned long long* stats;
 };
 
+__device__ __forceinline__ void write_mean(float* mean, double d, long long n) {
+  mean[0] = n > 0 ? static_cast<float>(d / static_cast<double>(n)) : 0.0f;
+  mean[1] = n > 0 ? static_cast<float>(1.0 / static_cast<double>(n)) : 0.0f;
+}
+
 __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_constant__ JoinArgs a) {
   constexpr int kWarps = kJoinThreads / kWarp;
   __shared__ float2 s_part[kWarps][kWarp + 1];
@@ -411,12 +520,16 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_co
   __shared__ bool s_last;
   const int lane = lane_id(), w = threadIdx.x / kWarp;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarp + lane;
-  float top = -INFINITY, sum = 0.0f;
   wait_before();
-  if (i < a.tokens) {
+  const int64_t raw = i >= a.tokens ? -1 : a.itype == TBE_I32 ? ld_int<int32_t>(a.targets, i) : ld_int<int64_t>(a.targets, i);
+  const bool counts = raw >= 0 && raw < a.rows;
+  const int64_t j = !counts ? 0 : a.row != nullptr ? a.row[i] : i;
+  const float logit = w == 0 && counts ? a.target_logit[j] : 0.0f;
+  float top = -INFINITY, sum = 0.0f;
+  if (counts) {
 #pragma unroll 8
     for (int p = w; p < a.parts; p += kWarps) {
-      const float2 v = a.part[p * a.parts_rows + i];
+      const float2 v = a.part[p * a.parts_rows + j];
       const float next = fmaxf(top, v.x), ref = next == -INFINITY ? 0.0f : next;
       sum = sum * exp2_fast(top - ref) + v.y * exp2_fast(v.x - ref);
       top = next;
@@ -429,13 +542,11 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_co
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_part[k][lane].x);
     const float ref = top == -INFINITY ? 0.0f : top;
-    sum = 0.0f;
+    float s4[4] = {};
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) sum += s_part[k][lane].y * exp2_fast(s_part[k][lane].x - ref);
-    const int64_t raw = i < a.tokens ? (a.itype == TBE_I32 ? ld_int<int32_t>(a.targets, i) : ld_int<int64_t>(a.targets, i)) : -1;
-    const bool counts = raw >= 0 && raw < a.rows;
-    const float lse = counts ? (ref + log2f(sum)) * kLn2 : 0.0f;
-    const float loss = counts ? lse - a.target_logit[i] : 0.0f;
+    for (int k = 0; k < kWarps; ++k) s4[k % 4] += s_part[k][lane].y * exp2_fast(s_part[k][lane].x - ref);
+    const float lse = counts ? (ref + log2f((s4[0] + s4[1]) + (s4[2] + s4[3]))) * kLn2 : 0.0f;
+    const float loss = counts ? lse - logit : 0.0f;
     if (i < a.tokens) a.lse[i] = lse, a.loss[i] = loss;
     const unsigned bad = __ballot_sync(kFull, raw >= a.rows);
     const unsigned live = __ballot_sync(kFull, counts);
@@ -443,11 +554,16 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_co
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFull, d, o);
     if (lane == 0) {
-      a.sums[blockIdx.x] = BlockSum{d, __popc(live)};
       stat_add(a.stats, TBE_STAT_UNREPAIRED, __popc(bad));
-      __threadfence();
-      s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
-      __threadfence();
+      s_last = false;
+      if (gridDim.x == 1) {
+        write_mean(a.mean, d, __popc(live));
+      } else {
+        a.sums[blockIdx.x] = BlockSum{d, __popc(live)};
+        __threadfence();
+        s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+        __threadfence();
+      }
     }
   }
   __syncthreads();
@@ -459,19 +575,20 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_co
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFull, d, o), n += __shfl_xor_sync(kFull, n, o);
   if (lane == 0) s_loss[w] = d, s_count[w] = n;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < kWarps; ++k) d += s_loss[k], n += s_count[k];
-    a.mean[0] = n > 0 ? static_cast<float>(d / static_cast<double>(n)) : 0.0f;
-    a.mean[1] = n > 0 ? static_cast<float>(1.0 / static_cast<double>(n)) : 0.0f;
-  }
+  if (w != 0) return;
+  d = s_loss[lane], n = s_count[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFull, d, o), n += __shfl_xor_sync(kFull, n, o);
+  if (lane == 0) write_mean(a.mean, d, n);
 }
 
-// dhidden = alpha * the sums of all splits; zeros for tokens that do not count.
+// dhidden = alpha * the sums of all splits, to the selected tokens' rows.
 template <typename T>
 struct FinishArgs {
   const float* sums;
   const float* meta;
-  const int* target;
+  const int* live;
+  const int* place;
   T* out;
   int64_t tokens, sums_stride, stride;
   int splits, cols, vec;
@@ -479,25 +596,26 @@ struct FinishArgs {
 
 template <typename T>
 __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant__ FinishArgs<T> a) {
-  const int64_t per_row = a.sums_stride / 8, total = a.tokens * per_row;
   wait_before();
+  const int per_row = static_cast<int>(a.sums_stride / 8);
+  const int64_t total = static_cast<int64_t>(*a.live) * per_row;
   const float alpha = a.meta[1];
   for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; x < total; x += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t i = x / per_row;
+    const int64_t i = total >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(per_row) : x / per_row;
     const int col = static_cast<int>(x - i * per_row) * 8;
+    const int64_t to = a.place[i];
     float f[8] = {};
-    if (a.target[i] >= 0) {
-      for (int s = 0; s < a.splits; ++s) {
-        const float4* p = reinterpret_cast<const float4*>(a.sums + (s * a.tokens + i) * a.sums_stride + col);
-        const float4 u = p[0], v = p[1];
-        f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w, f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= alpha;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(a.sums + (s * a.tokens + i) * a.sums_stride + col);
+      const float4 u = p[0], v = p[1];
+      f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w, f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] *= alpha;
     Pack<T, 8> p;
     p.set(f);
-    T* dst = a.out + i * a.stride + col;
+    T* dst = a.out + to * a.stride + col;
     if (a.vec && col + 8 <= a.cols) p.store(dst);
     else p.store_some(dst, a.cols - col);
   }
@@ -506,50 +624,35 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant_
 // ------------------------------------------------------------------------------------------
 // Host
 // ------------------------------------------------------------------------------------------
-template <int BN, class P0, class P1>
-tbe_status launch_pair(const typename P0::Args& p0, const typename P1::Args& p1, PairPlan plan, cudaStream_t s) {
-  auto* kernel = pair_mma_kernel<BN, P0, P1>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PairTile<BN>::kSmem);
+template <int BN, int AM, class P0, class P1>
+tbe_status launch_pair(const typename P0::Args& p0, const typename P1::Args& p1, int64_t items, const LossArgs& a, const DeviceInfo& dev,
+                       cudaStream_t s) {
+  auto* kernel = pair_mma_kernel<BN, AM, P0, P1>;
+  constexpr size_t smem = PairTile<BN, AM>::kSmem;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(kernel, smem, allowed);
   if (e != cudaSuccess) return cuda_status(e);
-  return cuda_status(launch_after(kernel, static_cast<unsigned>(2 * plan.pairs), kPairThreads, PairTile<BN>::kSmem, s, p0, p1, plan));
+  const int64_t pairs = items < dev.sms / 2 ? items : dev.sms / 2;
+  return cuda_status(launch_after(kernel, static_cast<unsigned>(2 * pairs), kPairThreads, smem, s, p0, p1, a.stats));
 }
 
-template <int BN, class P>
+template <int BN, int AM, class P>
 tbe_status launch_product(const typename P::Args& p, const LossArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  const int64_t items = static_cast<int64_t>(p.g.m_tiles) * p.g.n_tiles * p.g.splits;
-  const PairPlan plan{static_cast<int>(items < dev.sms / 2 ? items : dev.sms / 2), 0, 0, a.stats};
-  return launch_pair<BN, P, NoProduct>(p, NoProduct::Args{}, plan, s);
+  return launch_pair<BN, AM, P, NoProduct>(p, NoProduct::Args{}, p.g.items(), a, dev, s);
 }
 
-// Two products in one launch: the first one's tiles are long and leave some pairs a tile short; how many of the second's
-// tiles those take before the rest is dealt out, so that the last pair to end does so soonest.
-PairPlan plan_two(const PairShape& g0, const PairShape& g1, const LossArgs& a, const DeviceInfo& dev) {
-  const int64_t n0 = static_cast<int64_t>(g0.m_tiles) * g0.n_tiles * g0.splits, n1 = static_cast<int64_t>(g1.m_tiles) * g1.n_tiles * g1.splits;
-  const int64_t most = dev.sms / 2, pairs = n0 + n1 < most ? n0 + n1 : most;
-  PairPlan best{static_cast<int>(pairs), 0, 0, a.stats};
-  const int64_t c0 = g0.k_blocks / g0.splits + 3, c1 = g1.k_blocks / g1.splits + 3;  // blocks, and what a tile costs besides
-  const int64_t busy = n0 % pairs, lazy = pairs - busy, each = n0 / pairs;
-  int64_t least = INT64_MAX;
-  for (int64_t extra = busy == 0 ? 0 : c0 / c1; extra >= 0 && extra <= (busy == 0 ? 0 : c0 / c1 + 1); ++extra) {
-    const int64_t some = lazy * extra <= n1 ? extra : n1 / lazy;
-    const int64_t rest = n1 - lazy * some, round = rest / pairs, left = rest % pairs;
-    for (int first = 0; first < 2; ++first) {
-      const int64_t l = each * c0 + (some + round + (first ? left > 0 : left > busy)) * c1;
-      const int64_t b = busy == 0 ? 0 : (each + 1) * c0 + (round + (first ? left > lazy : left > 0)) * c1;
-      if ((l > b ? l : b) < least) least = l > b ? l : b, best.extra = static_cast<int>(some), best.lazy_first = first;
-    }
-  }
-  return best;
-}
-
-tbe_status launch_prep(const PrepArgs& p, const DeviceInfo& dev, cudaStream_t s) {
-  const int64_t rows = p.hidden_rows + p.weight_rows;
-  int64_t blocks = ceil_div(rows, kPrepThreads / kWarp);
-  if (blocks > dev.sms * 8) blocks = dev.sms * 8;
-  if (blocks < 1) blocks = 1;
-  loss_prep_kernel<<<static_cast<unsigned>(blocks + p.backward), kPrepThreads, 0, s>>>(p);
+template <bool BACKWARD>
+tbe_status launch_select(const SelectArgs& p, cudaStream_t s) {
+  loss_select_kernel<BACKWARD><<<1, kSelectThreads, 0, s>>>(p);
   note_launch();
   return cuda_status(cudaGetLastError());
+}
+
+tbe_status launch_copy(const CopyArgs& p, const DeviceInfo& dev, cudaStream_t s) {
+  const int64_t rows = p.tokens + (p.weight_copy != nullptr ? p.rows : 0);
+  int64_t blocks = ceil_div(rows * (p.dim_pad / 8), 2 * kCopyThreads);
+  if (blocks > dev.sms * 8) blocks = dev.sms * 8;
+  return cuda_status(launch_after(loss_copy_kernel, static_cast<unsigned>(blocks), kCopyThreads, 0, s, p));
 }
 
 size_t place(size_t* at, int64_t bytes) {
@@ -558,8 +661,23 @@ size_t place(size_t* at, int64_t bytes) {
   return here;
 }
 
+// Bytes of a store that every row allows.
+int store_bytes(const void* p, int64_t stride) {
+  return stride % 16 == 0 && is_aligned(p, 32) ? 32 : stride % 8 == 0 && is_aligned(p, 16) ? 16 : 0;
+}
+
 // Bytes of dz that a piece of the table may take.
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
+
+// The forward selects the tokens that count from here on; fewer are one to four tiles of rows, whose products take less than the
+// two launches.
+constexpr int64_t kSelectTokens = 1024;
+
+// Rows of A that a CTA copies in the forward's product of at most as many tokens.
+constexpr int kFewTokens = 32;
+
+// Blocks of k up to which one pair makes a whole tile of dhidden, with no sums to join after it.
+constexpr int kDirectBlocks = 24;
 
 // Columns of a tile of the gradients' products: 128 where tiles of 256 would be a fifth or more emptier.
 int gradient_bn(int dim) { return round_up(dim, 128) * 5 <= round_up(dim, 256) * 4 ? 128 : 256; }
@@ -571,33 +689,46 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
   const int N = static_cast<int>(a.tokens), m_tiles = static_cast<int>(ceil_div(N, kPairM));
   const int d_tiles = static_cast<int>(ceil_div(a.dim, BN)), d_blocks = static_cast<int>(ceil_div(a.dim, kPairK));
   float* meta = reinterpret_cast<float*>(ws + l.meta);
-  const int* target = reinterpret_cast<const int*>(ws + l.target);
+  const int* live = reinterpret_cast<const int*>(ws + l.live);
+  const int* placed = reinterpret_cast<const int*>(ws + l.place);
   T* dz = reinterpret_cast<T*>(ws + l.dz);
   float* sums = reinterpret_cast<float*>(ws + l.sums);
   using Grad = Product<false, false, GradJob<T>>;
   using Sum = Product<false, true, SumJob<BN>>;
+  using Direct = Product<false, true, OutJob<T, BN>>;
   using Out = Product<true, true, OutJob<T, BN>>;
-  const int aligned = a.dweight_stride % 16 == 0 && is_aligned(dweight, 32) ? 32 : a.dweight_stride % 8 == 0 && is_aligned(dweight, 16) ? 16 : 0;
   tbe_status st;
   for (int64_t first = 0; first < a.rows; first += l.piece) {
-    const int live = static_cast<int>(a.rows - first < l.piece ? a.rows - first : l.piece);
-    const int v_tiles = static_cast<int>(ceil_div(live, 256)), f = static_cast<int>(first);
-    typename Grad::Args ga{maps[0], maps[1], PairShape{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 0, pair_idesc(bf16, 256, false, false)},
-                           {meta, reinterpret_cast<const float*>(ws + l.coef), reinterpret_cast<const float*>(ws + l.lse2), target, dz,
-                            l.piece, N, f, live, a.scale * kLog2e}};
-    if ((st = launch_product<256, Grad>(ga, a, dev, s)) != TBE_OK) return st;
+    const int here = static_cast<int>(a.rows - first < l.piece ? a.rows - first : l.piece);
+    const int v_tiles = static_cast<int>(ceil_div(here, 256)), f = static_cast<int>(first);
+    typename Grad::Args ga{maps[0], maps[1],
+                           PairShape{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 0, pair_idesc(bf16, 256, false, false), live, nullptr},
+                           {meta, live, reinterpret_cast<const float*>(ws + l.coef), reinterpret_cast<const float*>(ws + l.lse2),
+                            reinterpret_cast<const int*>(ws + l.target), dz, l.piece, N, f, here, a.scale * kLog2e}};
+    if ((st = launch_product<256, 128, Grad>(ga, a, dev, s)) != TBE_OK) return st;
     // dhidden += dz [tokens, piece] by weight [piece, dim];  dweight = dz^T [piece, tokens] by hidden [tokens, dim]
-    typename Sum::Args sa{maps[2], maps[3],
-                          PairShape{m_tiles, d_tiles, l.splits, static_cast<int>(ceil_div(live, kPairK)), 0, 0, 0, f, 0,
-                                    pair_idesc(bf16, BN, false, true)},
-                          {sums, l.dim_pad, N, first > 0}};
+    const PairShape sum{m_tiles, d_tiles, l.splits, static_cast<int>(ceil_div(here, kPairK)), 0, 0, 0, f, 0, pair_idesc(bf16, BN, false, true),
+                        live, nullptr};
     typename Out::Args oa{maps[4], maps[5],
-                          PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, 1, pair_idesc(bf16, BN, true, true)},
-                          {meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, a.dim, aligned}};
-    if ((st = launch_pair<BN, Sum, Out>(sa, oa, plan_two(sa.g, oa.g, a, dev), s)) != TBE_OK) return st;
+                          PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, 1, pair_idesc(bf16, BN, true, true),
+                                    nullptr, live},
+                          {meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, nullptr, nullptr, a.dim,
+                           store_bytes(dweight, a.dweight_stride)}};
+    const int64_t items = static_cast<int64_t>(sum.items()) + oa.g.items();
+    if (l.direct) {
+      typename Direct::Args da{maps[2], maps[3], sum,
+                               {meta, static_cast<T*>(dhidden), a.dhidden_stride, 0, a.tokens, placed, live, a.dim,
+                                store_bytes(dhidden, a.dhidden_stride)}};
+      st = launch_pair<BN, 128, Direct, Out>(da, oa, items, a, dev, s);
+    } else {
+      typename Sum::Args sa{maps[2], maps[3], sum, {sums, l.dim_pad, N, first > 0}};
+      st = launch_pair<BN, 128, Sum, Out>(sa, oa, items, a, dev, s);
+    }
+    if (st != TBE_OK) return st;
   }
-  FinishArgs<T> fa{sums, meta, target, static_cast<T*>(dhidden), a.tokens, l.dim_pad, a.dhidden_stride, l.splits, a.dim,
-                   a.dhidden_stride % 8 == 0 && is_aligned(dhidden, 16)};
+  if (l.direct) return TBE_OK;
+  FinishArgs<T> fa{sums, meta, live, placed, static_cast<T*>(dhidden), a.tokens, l.dim_pad, a.dhidden_stride, l.splits, a.dim,
+                   store_bytes(dhidden, a.dhidden_stride) != 0};
   int64_t blocks = ceil_div(a.tokens * (l.dim_pad / 8), 256);
   if (blocks > dev.sms * 8) blocks = dev.sms * 8;
   return cuda_status(launch_after(loss_finish_kernel<T>, static_cast<unsigned>(blocks), 256, 0, s, fa));
@@ -631,8 +762,12 @@ LossForwardLayout loss_forward_layout(const LossArgs& a) {
   l.parts = static_cast<int>(2 * ceil_div(a.rows, 256));  // two to a tile; fewer are used where the pairs join theirs
   l.parts_rows = round_up(a.tokens, 32);
   l.part = place(&at, l.parts * l.parts_rows * 8);
-  l.target = place(&at, a.tokens * 4);
+  l.logit = place(&at, a.tokens * 4);
   l.ticket = place(&at, 256 + ceil_div(a.tokens, kWarp) * static_cast<int64_t>(sizeof(BlockSum)));  // and the blocks' sums
+  l.live = place(&at, 4);
+  l.place = place(&at, a.tokens * 4);
+  l.target = place(&at, a.tokens * 4);
+  l.row = place(&at, a.tokens * 4);
   l.hidden = place(&at, a.tokens * dim_pad * 2);
   l.weight = place(&at, a.copy_weight ? a.rows * dim_pad * 2 : 0);
   l.total = at;
@@ -648,20 +783,26 @@ LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev
   if (most > (1 << 30)) most = 1 << 30;
   const int64_t pieces = ceil_div(a.rows, most);
   l.piece = round_up(ceil_div(a.rows, pieces), 256);
-  // Splits of dhidden's long sums: none of their tiles shall take more than half of a pair's share of a piece's blocks.
   const int64_t d_tiles = ceil_div(a.dim, gradient_bn(a.dim)), blocks = ceil_div(l.piece, kPairK);
   const int64_t tiles = ceil_div(a.tokens, kPairM) * d_tiles, pairs = dev.sms / 2;
-  const int64_t all = tiles * blocks + ceil_div(l.piece, 256) * d_tiles * ceil_div(a.tokens, kPairK);
-  int64_t splits = all > 0 ? ceil_div(2 * pairs * blocks, all) : 1;
-  if (splits > blocks / 2) splits = blocks / 2;
-  // the last piece may be shorter: every split has to have a part of it
-  const int64_t last = ceil_div(a.rows - (ceil_div(a.rows, l.piece) - 1) * l.piece, kPairK);
-  if (splits > last) splits = last;
-  l.splits = splits < 1 ? 1 : static_cast<int>(splits);
+  l.direct = a.rows <= l.piece && ceil_div(a.rows, kPairK) <= kDirectBlocks;
+  l.splits = 1;
+  if (!l.direct) {  // none of the tiles of dhidden's long sums shall take more than half of a pair's share of a piece's blocks
+    const int64_t all = tiles * blocks + ceil_div(l.piece, 256) * d_tiles * ceil_div(a.tokens, kPairK);
+    int64_t splits = all > 0 ? ceil_div(2 * pairs * blocks, all) : 1;
+    if (splits > blocks / 2) splits = blocks / 2;
+    // the last piece may be shorter: every split has to have a part of it
+    const int64_t last = ceil_div(a.rows - (ceil_div(a.rows, l.piece) - 1) * l.piece, kPairK);
+    if (splits > last) splits = last;
+    if (splits > 1) l.splits = static_cast<int>(splits);
+  }
   l.meta = place(&at, 16);
+  l.live = place(&at, 4);
+  l.place = place(&at, a.tokens * 4);
+  l.target = place(&at, a.tokens * 4);
+  l.row = place(&at, a.tokens * 4);
   l.coef = place(&at, a.tokens * 4);
   l.lse2 = place(&at, a.tokens * 4);
-  l.target = place(&at, a.tokens * 4);
   l.hidden = place(&at, a.tokens * l.dim_pad * 2);
   l.weight = place(&at, a.copy_weight ? a.rows * l.dim_pad * 2 : 0);
   // What these two take varies with the number of tokens both ways: as much as any smaller number may need, so that a
@@ -679,36 +820,50 @@ tbe_status launch_loss_forward(const LossArgs& a, const LossForwardLayout& l, co
                                const void* targets, float* loss, float* lse, float* mean, char* ws, const DeviceInfo& dev,
                                cudaStream_t s) {
   if (a.tokens == 0) return cuda_status(cudaMemsetAsync(mean, 0, 8, s));
-  const bool bf16 = a.dtype == TBE_BF16;
+  const bool bf16 = a.dtype == TBE_BF16, select = a.tokens >= kSelectTokens;
   const int dim_pad = static_cast<int>(round_up(a.dim, 8));
+  int* live = reinterpret_cast<int*>(ws + l.live);
+  int* selected = reinterpret_cast<int*>(ws + l.target);
+  int* row = reinterpret_cast<int*>(ws + l.row);
   tbe_status st;
   int64_t hs = a.hidden_stride, wst = a.weight_stride;
-  if (a.copy_hidden || a.copy_weight) {
-    PrepArgs p{};
-    p.tokens = a.tokens, p.rows = a.rows, p.hidden_stride = a.hidden_stride, p.weight_stride = a.weight_stride;
-    p.hidden_rows = a.copy_hidden ? a.tokens : 0, p.weight_rows = a.copy_weight ? a.rows : 0;
+  if (select) {
+    SelectArgs p{};
+    p.targets = targets, p.tokens = a.tokens, p.rows = a.rows, p.itype = a.itype;
+    p.live = live, p.place = reinterpret_cast<int*>(ws + l.place), p.target = selected, p.row = row;
+    if ((st = launch_select<false>(p, s)) != TBE_OK) return st;
+  }
+  if (select || a.copy_hidden || a.copy_weight) {
+    CopyArgs p{};
+    if (select) p.live = live, p.place = reinterpret_cast<int*>(ws + l.place), p.row = row;
     p.hidden = static_cast<const uint16_t*>(hidden), p.weight = static_cast<const uint16_t*>(weight);
-    p.hidden_copy = reinterpret_cast<uint16_t*>(ws + l.hidden), p.weight_copy = reinterpret_cast<uint16_t*>(ws + l.weight);
-    p.dim = a.dim, p.dim_pad = dim_pad, p.itype = a.itype, p.targets = targets;
-    if ((st = launch_prep(p, dev, s)) != TBE_OK) return st;
-    if (a.copy_hidden) hidden = ws + l.hidden, hs = dim_pad;
+    p.hidden_copy = reinterpret_cast<uint16_t*>(ws + l.hidden);
+    if (a.copy_weight) p.weight_copy = reinterpret_cast<uint16_t*>(ws + l.weight);
+    p.tokens = a.tokens, p.rows = a.rows, p.hidden_stride = a.hidden_stride, p.weight_stride = a.weight_stride;
+    p.dim = a.dim, p.dim_pad = dim_pad;
+    if ((st = launch_copy(p, dev, s)) != TBE_OK) return st;
+    hidden = ws + l.hidden, hs = dim_pad;
     if (a.copy_weight) weight = ws + l.weight, wst = dim_pad;
   }
+  const bool few = a.tokens <= kFewTokens;
   CUtensorMap ma, mb;
-  if (!encode_operand(&ma, hidden, bf16, a.dim, a.tokens, hs, 128) || !encode_operand(&mb, weight, bf16, a.dim, a.rows, wst, 128))
+  if (!encode_operand(&ma, hidden, bf16, a.dim, a.tokens, hs, few ? kFewTokens : 128) || !encode_operand(&mb, weight, bf16, a.dim, a.rows, wst, 128))
     return cuda_status(cudaErrorInvalidValue);
   uint32_t* ticket = reinterpret_cast<uint32_t*>(ws + l.ticket);
   float2* part = reinterpret_cast<float2*>(ws + l.part);
-  float* target_logit = reinterpret_cast<float*>(ws + l.target);
+  float* target_logit = reinterpret_cast<float*>(ws + l.logit);
   using Stats = Product<false, false, StatsJob>;
   const int m_tiles = static_cast<int>(ceil_div(a.tokens, kPairM)), v_tiles = l.parts / 2, pairs = dev.sms / 2;
   const bool carry = m_tiles == 1 && v_tiles > pairs;
-  const Stats::Args sa{ma, mb, PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, 0, pair_idesc(bf16, 256, false, false)},
-                       {targets, part, target_logit, ticket, l.parts_rows, a.rows, static_cast<int>(a.tokens), a.itype, carry, a.scale,
-                        a.scale * kLog2e}};
-  if ((st = launch_product<256, Stats>(sa, a, dev, s)) != TBE_OK) return st;
-  const JoinArgs ja{part, target_logit, targets, loss, lse, mean, reinterpret_cast<BlockSum*>(ws + l.ticket + 256), ticket, a.tokens,
-                    a.rows, l.parts_rows, carry ? 2 * pairs : l.parts, a.itype, a.stats};
+  const Stats::Args sa{ma, mb,
+                       PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, 0, pair_idesc(bf16, 256, false, false),
+                                 select ? live : nullptr, nullptr},
+                       {targets, select ? selected : nullptr, live, part, target_logit, ticket, l.parts_rows, a.rows, static_cast<int>(a.tokens), a.itype,
+                        carry, a.scale, a.scale * kLog2e}};
+  st = few ? launch_product<256, kFewTokens, Stats>(sa, a, dev, s) : launch_product<256, 128, Stats>(sa, a, dev, s);
+  if (st != TBE_OK) return st;
+  const JoinArgs ja{part, target_logit, targets, select ? row : nullptr, loss, lse, mean, reinterpret_cast<BlockSum*>(ws + l.ticket + 256), ticket,
+                    a.tokens, a.rows, l.parts_rows, carry ? 2 * pairs : l.parts, a.itype, a.stats};
   return cuda_status(launch_after(loss_join_kernel, static_cast<unsigned>(ceil_div(a.tokens, kWarp)), kJoinThreads, 0, s, ja));
 }
 
@@ -718,17 +873,24 @@ tbe_status launch_loss_backward(const LossArgs& a, const LossBackwardLayout& l, 
   if (a.tokens == 0)  // a sum over no tokens
     return cuda_status(cudaMemset2DAsync(dweight, a.dweight_stride * 2, 0, static_cast<size_t>(a.dim) * 2, a.rows, s));
   const bool bf16 = a.dtype == TBE_BF16;
-  PrepArgs p{};
-  p.tokens = a.tokens, p.rows = a.rows, p.hidden_stride = a.hidden_stride, p.weight_stride = a.weight_stride;
-  p.hidden_rows = a.tokens, p.weight_rows = a.copy_weight ? a.rows : 0;
-  p.hidden = static_cast<const uint16_t*>(hidden), p.weight = static_cast<const uint16_t*>(weight);
-  p.hidden_copy = reinterpret_cast<uint16_t*>(ws + l.hidden), p.weight_copy = reinterpret_cast<uint16_t*>(ws + l.weight);
-  p.dim = a.dim, p.dim_pad = static_cast<int>(l.dim_pad), p.itype = a.itype, p.backward = 1, p.targets = targets, p.lse = lse;
-  p.dloss = dloss, p.mean = mean, p.scale = a.scale;
+  SelectArgs p{};
+  p.targets = targets, p.tokens = a.tokens, p.rows = a.rows, p.itype = a.itype;
+  p.live = reinterpret_cast<int*>(ws + l.live), p.place = reinterpret_cast<int*>(ws + l.place);
+  p.target = reinterpret_cast<int*>(ws + l.target), p.row = reinterpret_cast<int*>(ws + l.row);
+  p.lse = lse, p.dloss = dloss, p.mean = mean, p.scale = a.scale;
   p.meta = reinterpret_cast<float*>(ws + l.meta), p.coef = reinterpret_cast<float*>(ws + l.coef);
-  p.lse2 = reinterpret_cast<float*>(ws + l.lse2), p.target = reinterpret_cast<int*>(ws + l.target);
-  const tbe_status st = launch_prep(p, dev, s);
+  p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
+  tbe_status st = launch_select<true>(p, s);
   if (st != TBE_OK) return st;
+  CopyArgs c{};
+  c.live = p.live, c.place = p.place, c.row = p.row;
+  c.hidden = static_cast<const uint16_t*>(hidden), c.weight = static_cast<const uint16_t*>(weight);
+  c.hidden_copy = reinterpret_cast<uint16_t*>(ws + l.hidden);
+  if (a.copy_weight) c.weight_copy = reinterpret_cast<uint16_t*>(ws + l.weight);
+  c.dhidden = static_cast<uint16_t*>(dhidden);
+  c.tokens = a.tokens, c.rows = a.rows, c.hidden_stride = a.hidden_stride, c.weight_stride = a.weight_stride;
+  c.dhidden_stride = a.dhidden_stride, c.dim = a.dim, c.dim_pad = static_cast<int>(l.dim_pad);
+  if ((st = launch_copy(c, dev, s)) != TBE_OK) return st;
   const void* h = ws + l.hidden;
   const int64_t wst = a.copy_weight ? l.dim_pad : a.weight_stride;
   if (a.copy_weight) weight = ws + l.weight;

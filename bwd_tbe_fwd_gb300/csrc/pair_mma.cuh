@@ -28,29 +28,61 @@ constexpr uint32_t kPairWaitLimit = 1u << 22;
 
 constexpr int kStageRow = 34;          // 16-bit elements from one row of a warp's staging area to the next: 17 words, no bank twice
 
-template <int BN>
+// AM: rows of A that a CTA copies.  With fewer than 128 (products of few rows, bound by B's way through memory) the products
+// read what lies behind them as the others, whose results nobody looks at, and the ring has more stages.
+template <int BN, int AM = 128>
 struct PairTile {
-  static constexpr int kA = 128 * kPairK * 2;            // bytes of a CTA's part of a stage
+  static constexpr int kA = AM * kPairK * 2;             // bytes of a CTA's part of a stage
   static constexpr int kB = BN / 2 * kPairK * 2;
   static constexpr int kStage = kA + kB;
-  static constexpr int kStages = 196608 / kStage;        // 6 of 32 KB, 8 of 24 KB
+  static constexpr int kStages = 196608 / kStage;        // 6 of 32 KB, 8 of 24 KB, 9 of 20 KB
+  static_assert(kStage >= 128 * kPairK * 2, "the products read 128 rows of A from a stage's start");
   static constexpr int kStaging = kEpiWarps * 32 * kStageRow * 2;       // 32 x 32 16-bit elements to a warp of the epilogue
   static constexpr int kSmem = kStages * kStage + kStaging + 1024;      // and room to align to the swizzle's 1024 bytes
 };
 
-// A product: its tiles, and where it starts in A's and B's coordinates.
+// A product: its tiles, and where it starts in A's and B's coordinates.  With `live`, the number of rows (m) or the length of
+// the sums (k) is known on the device only: *live, taken as 1 at least; m_tiles and k_blocks are then the most they can be.
 struct PairShape {
   int m_tiles, n_tiles, splits, k_blocks;   // k_blocks: of all splits together; splits <= k_blocks
   int a_m0, a_k0, b_n0, b_k0;
   int n_first;      // tiles go along n first, else along m; splits come last
   uint32_t idesc;
+  const int* live_m;
+  const int* live_k;
+
+  __device__ __forceinline__ void settle() {
+    if (live_m != nullptr) m_tiles = (max(*live_m, 1) + kPairM - 1) / kPairM;
+    if (live_k != nullptr) k_blocks = (max(*live_k, 1) + kPairK - 1) / kPairK;
+  }
+  __host__ __device__ __forceinline__ int items() const { return m_tiles * n_tiles * splits; }
 };
 
 // One or two products in a launch.  The pairs deal out the first one's tiles in turn; those that got one fewer (the lazy ones)
 // take `extra` tiles of the second before the rest is dealt out, to the lazy ones first if lazy_first.
 struct PairPlan {
   int pairs, extra, lazy_first;
-  unsigned long long* stats;
+
+  // The choice with which the last pair ends soonest, counting blocks of k and three more for a tile's other costs.
+  __host__ __device__ static PairPlan two(const PairShape& g0, const PairShape& g1, int pairs) {
+    const int n0 = g0.items(), n1 = g1.items(), c0 = g0.k_blocks / g0.splits + 3, c1 = g1.k_blocks / g1.splits + 3;
+    const int each = n0 / pairs, busy = n0 - each * pairs, lazy = pairs - busy;
+    PairPlan best{pairs, 0, 0};
+    int64_t least = INT64_MAX;
+    const int most = busy == 0 ? 0 : n1 / lazy, even = c0 / c1;
+    for (int k = 0; k < 3; ++k) {
+      int extra = k == 0 ? 0 : even + k - 1;
+      extra = extra < most ? extra : most;
+      const int rest = n1 - lazy * extra, round = rest / pairs, left = rest - round * pairs;
+      for (int first = 0; first < 2; ++first) {
+        const int64_t l = static_cast<int64_t>(each) * c0 + static_cast<int64_t>(extra + round + (first ? left > 0 : left > busy)) * c1;
+        const int64_t b = busy == 0 ? 0 : static_cast<int64_t>(each + 1) * c0 + static_cast<int64_t>(round + (first ? left > lazy : left > 0)) * c1;
+        const int64_t end = l > b ? l : b;
+        if (end < least) least = end, best = PairPlan{pairs, extra, first};
+      }
+    }
+    return best;
+  }
 };
 
 // kind::f16 instruction descriptor: fp32 accumulator, 16-bit operands, M = 256.
@@ -96,6 +128,9 @@ __device__ __forceinline__ void commit_both(uint64_t* bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -176,7 +211,7 @@ struct Product {
   using Job = J;
   struct Args {
     CUtensorMap a, b;
-    PairShape g;
+    PairShape g;          // read by one thread of a CTA, which settles it
     typename J::Args job;
   };
 };
@@ -194,10 +229,9 @@ struct PairRole {
   bool failed;
 };
 
-template <int BN, class P>
-__device__ __forceinline__ void pair_copy(const typename P::Args& p, PairWalk walk, PairRole& r) {
-  using T = PairTile<BN>;
-  const PairShape& g = p.g;
+template <int BN, int AM, class P>
+__device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairShape& g, PairWalk walk, PairRole& r) {
+  using T = PairTile<BN, AM>;
   PairItem i;
   while (!r.failed && walk.next(g, i)) {
     const int am = g.a_m0 + i.m * kPairM + static_cast<int>(r.rank) * 128, bn = g.b_n0 + i.n * BN + static_cast<int>(r.rank) * (BN / 2);
@@ -227,18 +261,18 @@ __device__ __forceinline__ void pair_copy(const typename P::Args& p, PairWalk wa
   }
 }
 
-template <int BN, class P>
-__device__ __forceinline__ void pair_multiply(const typename P::Args& p, PairWalk walk, PairRole& r) {
-  using T = PairTile<BN>;
+template <int BN, int AM, class P>
+__device__ __forceinline__ void pair_multiply(const PairShape& g, PairWalk walk, PairRole& r) {
+  using T = PairTile<BN, AM>;
   PairItem i;
-  for (; !r.failed && walk.next(p.g, i); ++r.tile) {
+  for (; !r.failed && walk.next(g, i); ++r.tile) {
     const uint32_t buf = r.tile & 1, d = r.tmem + buf * 256;
     if (!mbar_wait_bounded(&r.acc_empty[buf], ((r.tile >> 1) & 1) ^ 1, kPairWaitLimit)) {
       r.failed = true;
       return;
     }
     pair::fence_after();
-    const int first = i.first(p.g), last = i.last(p.g);
+    const int first = i.first(g), last = i.last(g);
     for (int kb = first; kb < last; ++kb, ++r.it) {
       const uint32_t st = r.it % T::kStages;
       if (!mbar_wait_bounded(&r.full[st], (r.it / T::kStages) & 1, kPairWaitLimit)) {
@@ -249,7 +283,7 @@ __device__ __forceinline__ void pair_multiply(const typename P::Args& p, PairWal
       const uint64_t a = pair::operand_desc<P::kAMN>(r.ring + st * T::kStage), b = pair::operand_desc<P::kBMN>(r.ring + st * T::kStage + T::kA);
 #pragma unroll
       for (int k = 0; k < kPairK / 16; ++k)  // 16 k's: 32 bytes along a row, or two groups of 8 rows
-        pair::mma(d, a + k * ((P::kAMN ? 2048 : 32) >> 4), b + k * ((P::kBMN ? 2048 : 32) >> 4), p.g.idesc, kb > first || k > 0);
+        pair::mma(d, a + k * ((P::kAMN ? 2048 : 32) >> 4), b + k * ((P::kBMN ? 2048 : 32) >> 4), g.idesc, kb > first || k > 0);
       pair::commit_both(&r.empty[st]);
     }
     pair::commit_both(&r.acc_full[buf]);
@@ -257,17 +291,17 @@ __device__ __forceinline__ void pair_multiply(const typename P::Args& p, PairWal
 }
 
 template <int BN, class P>
-__device__ __forceinline__ void pair_epilogue(const typename P::Args& p, PairWalk walk, PairRole& r, int pair, int w, int lane,
-                                              uint16_t* staging) {
+__device__ __forceinline__ void pair_epilogue(const typename P::Args& p, const PairShape& g, PairWalk walk, PairRole& r, int pair, int w,
+                                              int lane, uint16_t* staging) {
   using Job = typename P::Job;
   const int row = static_cast<int>(r.rank) * 128 + (w % 4) * 32 + lane, half = w / 4;
   typename Job::State state{};
   PairItem i{}, next{};
-  bool more = walk.next(p.g, i);
+  bool more = walk.next(g, i);
   typename Job::Row now{}, then{};
   if (more) now.load(p.job, i, row);
   while (more) {
-    more = walk.next(p.g, next);
+    more = walk.next(g, next);
     if (more) then.load(p.job, next, row);   // the next tile's, while this one is waited for and worked on
     const uint32_t buf = r.tile & 1;
     r.failed = !mbar_wait_bounded(&r.acc_full[buf], (r.tile >> 1) & 1, kPairWaitLimit);
@@ -286,23 +320,28 @@ __device__ __forceinline__ void pair_epilogue(const typename P::Args& p, PairWal
   Job::finish(p.job, state, pair, row, half);
 }
 
-template <int BN, class P0, class P1>
+template <int BN, int AM, class P0, class P1>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_mma_kernel(const __grid_constant__ typename P0::Args p0, const __grid_constant__ typename P1::Args p1,
-                    const __grid_constant__ PairPlan plan) {
-  using T = PairTile<BN>;
+                    unsigned long long* stats) {
+  using T = PairTile<BN, AM>;
+  static_assert(AM == 128 || !P0::kAMN, "fewer rows of A in K-major order only");
   constexpr int ST = T::kStages;
   extern __shared__ uint8_t s_raw[];
   __shared__ __align__(8) uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2];
+  __shared__ PairShape s_shape[2];
+  __shared__ PairPlan s_plan;
   __shared__ uint32_t s_tmem;
   const uint32_t ring = (smem_u32(s_raw) + 1023u) & ~1023u;
-  const int w = threadIdx.x / kWarp, lane = lane_id(), pair_id = blockIdx.x / 2;
+  const int w = threadIdx.x / kWarp, lane = lane_id(), pair_id = blockIdx.x / 2, pairs = gridDim.x / 2;
   may_follow();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], 2 * kEpiWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pair::prefetch_map(&p0.a), pair::prefetch_map(&p0.b);
+    if constexpr (!P1::kNone) pair::prefetch_map(&p1.a), pair::prefetch_map(&p1.b);
   }
   if (w == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
@@ -312,17 +351,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist
   pair::fence_after();
+  wait_before();   // what this kernel reads is complete from here on
+  if (threadIdx.x == 32) {
+    s_shape[0] = p0.g;
+    s_shape[0].settle();
+    s_plan = PairPlan{pairs, 0, 0};
+    if constexpr (!P1::kNone) {
+      s_shape[1] = p1.g;
+      s_shape[1].settle();
+      s_plan = PairPlan::two(s_shape[0], s_shape[1], pairs);
+    }
+  }
+  __syncthreads();
   PairRole r{full, empty, acc_full, acc_empty, ring, s_tmem, cluster_rank(), 0, 0, false};
-  const int items0 = p0.g.m_tiles * p0.g.n_tiles * p0.g.splits;
-  const PairWalk walk0 = PairWalk::first(pair_id, plan, items0);
+  const PairShape g0 = s_shape[0], g1 = s_shape[P1::kNone ? 0 : 1];
+  const PairPlan plan = s_plan;
+  const PairWalk walk0 = PairWalk::first(pair_id, plan, g0.items());
   PairWalk walk1 = walk0;
-  if constexpr (!P1::kNone) walk1 = PairWalk::second(pair_id, plan, items0, p1.g.m_tiles * p1.g.n_tiles * p1.g.splits);
-  wait_before();  // what this kernel reads is complete from here on
+  if constexpr (!P1::kNone) walk1 = PairWalk::second(pair_id, plan, g0.items(), g1.items());
 
   if (w == kEpiWarps) {
     if (lane == 0) {
-      pair_copy<BN, P0>(p0, walk0, r);
-      if constexpr (!P1::kNone) pair_copy<BN, P1>(p1, walk1, r);
+      pair_copy<BN, AM, P0>(p0, g0, walk0, r);
+      if constexpr (!P1::kNone) pair_copy<BN, AM, P1>(p1, g1, walk1, r);
       // Copies must not be in flight when a CTA ends: in the even CTA, whose barriers count both CTAs' copies, the last
       // round of every stage has landed (its products are done by then, unless a wait gave up).
       if (r.rank == 0)
@@ -332,17 +383,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else if (w == kEpiWarps + 1) {
     if (r.rank == 0 && lane == 0) {
-      pair_multiply<BN, P0>(p0, walk0, r);
-      if constexpr (!P1::kNone) pair_multiply<BN, P1>(p1, walk1, r);
+      pair_multiply<BN, AM, P0>(g0, walk0, r);
+      if constexpr (!P1::kNone) pair_multiply<BN, AM, P1>(g1, walk1, r);
     }
     __syncwarp();
   } else {
     uint16_t* staging = reinterpret_cast<uint16_t*>(s_raw + (ring - smem_u32(s_raw)) + ST * T::kStage) + w * 32 * kStageRow;
-    pair_epilogue<BN, P0>(p0, walk0, r, pair_id, w, lane, staging);
+    pair_epilogue<BN, P0>(p0, g0, walk0, r, pair_id, w, lane, staging);
     if constexpr (!P1::kNone)
-      if (!r.failed) pair_epilogue<BN, P1>(p1, walk1, r, pair_id, w, lane, staging);
+      if (!r.failed) pair_epilogue<BN, P1>(p1, g1, walk1, r, pair_id, w, lane, staging);
   }
-  if (r.failed && lane == 0) stat_add(plan.stats, TBE_STAT_WAIT_TIMEOUT, 1);
+  if (r.failed && lane == 0) stat_add(stats, TBE_STAT_WAIT_TIMEOUT, 1);
   __syncwarp();
   pair::fence_before();
   cluster_sync();  // neither CTA ends, or frees its TMEM, while the other may still reach it

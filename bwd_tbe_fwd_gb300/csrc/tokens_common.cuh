@@ -27,13 +27,14 @@ struct LossArgs {
 struct LossForwardLayout {
   int64_t parts_rows;              // leading dimension of the parts: tokens, rounded up
   int parts;
-  size_t part, target, ticket, hidden, weight, total;
+  size_t part, logit, ticket, live, place, target, row, hidden, weight, total;
 };
 struct LossBackwardLayout {
   int64_t dim_pad;                 // row of the fp32 sums of dhidden
   int64_t piece;                   // rows of the table at a time
   int splits;                      // parts of the long product of dhidden
-  size_t meta, coef, lse2, target, hidden, weight, dz, sums, total;
+  bool direct;                     // it is written as it is: one piece, one split
+  size_t meta, live, place, target, row, coef, lse2, hidden, weight, dz, sums, total;
 };
 LossForwardLayout loss_forward_layout(const LossArgs& a);
 LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev);

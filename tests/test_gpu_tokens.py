@@ -223,3 +223,21 @@ def test_loss_of_no_tokens():
     assert loss.shape == lse.shape == (0,) and mean.tolist() == [0, 0]
     dh, dw = op.backward(h, w, t, lse, mean=mean)
     assert dh.shape == (0, 16) and float(dw.abs().sum()) == 0
+
+
+@pytest.mark.parametrize("tokens,kind", [(1023, "spread"), (1024, "spread"), (1500, "hot"), (4097, "none"), (4100, "run"), (1100, "full")])
+def test_loss_selects_the_tokens_that_count(tokens, kind):
+    check_loss(tokens, 290, 40, "bf16", ids=kind, seed=tokens)
+
+
+@pytest.mark.parametrize("dim", [24, 136, 200])
+@pytest.mark.parametrize("rows", [1500, 1600, 9000])
+def test_loss_sums_of_dhidden_in_one_and_in_many_splits(rows, dim):
+    check_loss(90, rows, dim, "f16", seed=rows, upstream="tokens")
+    check_loss(600, rows, dim, "bf16", seed=rows)
+
+
+@pytest.mark.parametrize("tokens", [1, 16, 31, 32, 33])
+def test_loss_of_few_tokens_over_many_rows(tokens):
+    """One tile of tokens, more tiles of the table than pairs of CTAs: the pairs join their parts."""
+    check_loss(tokens, 30_011, 72, "bf16", ids="hot", seed=tokens)
