@@ -3,9 +3,9 @@
 //
 // The two CTAs of a cluster sit on neighbouring SMs and work on one tile (tcgen05.mma.cta_group::2): each brings its
 // 128 rows of A and its half of B's rows into its shared memory, so a CTA copies BN / 2 rows of B where it would copy
-// BN alone: 64 bytes a clock at the full rate of a 256 x 256 tile, about what an SM can draw from L2.  Ten
-// warps: eight for the epilogue (warp w reads TMEM lanes 32 (w % 4) .. + 31 and half w / 4 of the columns), one thread that
-// issues the TMA copies of a ring of stages of 64 k's, one (in the even CTA) that issues the products.  The
+// BN alone: 64 bytes a clock at the full rate of a 256 x 256 tile, about what an SM can draw from L2.  Eleven
+// warps: eight for the epilogue (warp w reads TMEM lanes 32 (w % 4) .. + 31 and half w / 4 of the columns), two threads that
+// issue the TMA copies of a ring of stages of 64 k's, A's and B's, one (in the even CTA) that issues the products.  The
 // accumulator takes all 512 columns of TMEM as two buffers, so that the products of the next tile run while the epilogue
 // reads the last one.  The grid is persistent: pair p takes tiles p, p + pairs, ...
 //
@@ -23,7 +23,7 @@ namespace tbe {
 constexpr int kPairM = 256;            // rows of a tile; 128 to each CTA
 constexpr int kPairK = 64;             // k's of a stage: 128 bytes, one row of the swizzle
 constexpr int kEpiWarps = 8;
-constexpr int kPairThreads = 32 * (kEpiWarps + 2);
+constexpr int kPairThreads = 32 * (kEpiWarps + 3);
 constexpr uint32_t kPairWaitLimit = 1u << 22;
 
 constexpr int kStageRow = 34;          // 16-bit elements from one row of a warp's staging area to the next: 17 words, no bank twice
@@ -229,12 +229,14 @@ struct PairRole {
   bool failed;
 };
 
-template <int BN, int AM, class P>
+// One of the two threads that issue copies: A's or B's.  A's also tells the barrier how many bytes a stage has.
+template <int BN, int AM, class P, bool A>
 __device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairShape& g, PairWalk walk, PairRole& r) {
   using T = PairTile<BN, AM>;
+  const uint32_t leader = pair::in_leader(smem_u32(r.full));
   PairItem i;
   while (!r.failed && walk.next(g, i)) {
-    const int am = g.a_m0 + i.m * kPairM + static_cast<int>(r.rank) * 128, bn = g.b_n0 + i.n * BN + static_cast<int>(r.rank) * (BN / 2);
+    const int x = A ? g.a_m0 + i.m * kPairM + static_cast<int>(r.rank) * 128 : g.b_n0 + i.n * BN + static_cast<int>(r.rank) * (BN / 2);
     const int last = i.last(g);
     for (int kb = i.first(g); kb < last; ++kb, ++r.it) {
       const uint32_t st = r.it % T::kStages;
@@ -242,20 +244,15 @@ __device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairS
         r.failed = true;
         return;
       }
-      if (r.rank == 0) mbar_arrive_expect_tx(&r.full[st], 2 * T::kStage);
-      const uint32_t bar = pair::in_leader(smem_u32(&r.full[st])), a = r.ring + st * T::kStage, b = a + T::kA;
-      const int ak = g.a_k0 + kb * kPairK, bk = g.b_k0 + kb * kPairK;
-      if constexpr (P::kAMN) {
-        pair::tma_2d(a, &p.a, am, ak, bar);
-        pair::tma_2d(a + 8192, &p.a, am + 64, ak, bar);
-      } else {
-        pair::tma_2d(a, &p.a, ak, am, bar);
-      }
-      if constexpr (P::kBMN) {
+      if (A && r.rank == 0) mbar_arrive_expect_tx(&r.full[st], 2 * T::kStage);
+      const uint32_t bar = leader + st * 8, to = r.ring + st * T::kStage + (A ? 0 : T::kA);
+      const int k = (A ? g.a_k0 : g.b_k0) + kb * kPairK;
+      const CUtensorMap* map = A ? &p.a : &p.b;
+      if constexpr (A ? P::kAMN : P::kBMN) {
 #pragma unroll
-        for (int x = 0; x < BN / 128; ++x) pair::tma_2d(b + x * 8192, &p.b, bn + x * 64, bk, bar);
+        for (int c = 0; c < (A ? 2 : BN / 128); ++c) pair::tma_2d(to + c * 8192, map, x + c * 64, k, bar);
       } else {
-        pair::tma_2d(b, &p.b, bk, bn, bar);
+        pair::tma_2d(to, map, k, x, bar);
       }
     }
   }
@@ -372,8 +369,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (w == kEpiWarps) {
     if (lane == 0) {
-      pair_copy<BN, AM, P0>(p0, g0, walk0, r);
-      if constexpr (!P1::kNone) pair_copy<BN, AM, P1>(p1, g1, walk1, r);
+      pair_copy<BN, AM, P0, false>(p0, g0, walk0, r);
+      if constexpr (!P1::kNone) pair_copy<BN, AM, P1, false>(p1, g1, walk1, r);
+    }
+    __syncwarp();
+  } else if (w == kEpiWarps + 2) {
+    if (lane == 0) {
+      pair_copy<BN, AM, P0, true>(p0, g0, walk0, r);
+      if constexpr (!P1::kNone) pair_copy<BN, AM, P1, true>(p1, g1, walk1, r);
       // Copies must not be in flight when a CTA ends: in the even CTA, whose barriers count both CTAs' copies, the last
       // round of every stage has landed (its products are done by then, unless a wait gave up).
       if (r.rank == 0)
