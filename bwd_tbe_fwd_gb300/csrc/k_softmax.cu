@@ -27,11 +27,8 @@ __device__ __forceinline__ int load_target(const void* targets, int itype, int64
   return t >= 0 && t < rows ? static_cast<int>(t) : -1;
 }
 
-// Rows of the selected tokens with those that fill up the last block of k (which are zeros), as far as there are rows at all.
-__device__ __forceinline__ int filled(int live, int64_t tokens) {
-  const int64_t n = (static_cast<int64_t>(live > 1 ? live : 1) + kPairK - 1) / kPairK * kPairK;
-  return static_cast<int>(n < tokens ? n : tokens);
-}
+// Rows of the selected tokens with those that fill up the last block of k, which are zeros.
+__device__ __forceinline__ int filled(int live) { return (max(live, 1) + kPairK - 1) / kPairK * kPairK; }
 
 // 32 bytes at p, which is aligned to them.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
@@ -112,15 +109,16 @@ struct StatsJob {
       for (int k = 1; k < 32; ++k) most = fmaxf(most, c.get(k));
       const float next = fmaxf(top, most * a.scale2);
       const float ref = next == -INFINITY ? 0.0f : next;  // nothing but -inf so far: no inf - inf
-      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+      const F2 by(a.scale2), less(-ref);
+      F2 s0(0.0f), s1(0.0f);
 #pragma unroll
       for (int k = 0; k < 32; k += 4) {
-        s0 += exp2_fast(fmaf(c.get(k), a.scale2, -ref));
-        s1 += exp2_fast(fmaf(c.get(k + 1), a.scale2, -ref));
-        s2 += exp2_fast(fmaf(c.get(k + 2), a.scale2, -ref));
-        s3 += exp2_fast(fmaf(c.get(k + 3), a.scale2, -ref));
+        const F2 x = fma2(F2(c.get(k), c.get(k + 1)), by, less), y = fma2(F2(c.get(k + 2), c.get(k + 3)), by, less);
+        s0 = s0 + F2(exp2_fast(x.lo()), exp2_fast(x.hi()));
+        s1 = s1 + F2(exp2_fast(y.lo()), exp2_fast(y.hi()));
       }
-      sum = sum * exp2_fast(top - ref) + ((s0 + s1) + (s2 + s3));
+      s0 = s0 + s1;
+      sum = sum * exp2_fast(top - ref) + (s0.lo() + s0.hi());
       top = next;
       const int tj = tl >= j * 32 && tl < j * 32 + 32 ? static_cast<int>(tl) - j * 32 : -1;
       if (__any_sync(kFull, tj >= 0)) {
@@ -148,9 +146,9 @@ struct GradJob {
     const float* coef;     // of the selected tokens
     const float* lse2;     // lse in powers of 2
     const int* target;     // -1 in the rows that fill up
-    T* dz;                 // [tokens][ld]
-    int64_t ld;
-    int tokens, first, here;   // first row of the piece, rows of the table from there on
+    T* dz;                 // [blocks of 64 columns][dz_rows][64]
+    int64_t dz_rows;
+    int first, here;       // first row of the piece, rows of the table from there on
     float scale2;
   };
   struct Row {
@@ -161,7 +159,7 @@ struct GradJob {
       const int i = it.m * kPairM + row;
       target = -1, coef = 0.0f, lse2 = 0.0f;
       power = a.meta[0];
-      in = i < filled(*a.live, a.tokens);
+      in = i < filled(*a.live);
       if (in) target = a.target[i], coef = a.coef[i], lse2 = a.lse2[i];
     }
   };
@@ -172,20 +170,23 @@ struct GradJob {
     const int i = it.m * kPairM + row;
     const int col0 = it.n * 256 + half * 128, t = r.target;
     const int tl = t < 0 ? -1 : t - a.first - col0;
-    const float g = r.coef * r.power, ref = r.lse2;
-    T* dst = a.dz + i * a.ld + col0;
+    const F2 g(r.coef * r.power), by(a.scale2), less(-r.lse2);
+    T* dst = a.dz + (col0 / 64 * a.dz_rows + i) * 64;
     each_columns<128>(tmem, release, [&](int j, pair::Columns& c) {
       const int tj = tl >= j * 32 && tl < j * 32 + 32 ? tl - j * 32 : -1;
       float v[32];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] = exp2_fast(fmaf(c.get(k), a.scale2, -ref));
+      for (int k = 0; k < 32; k += 2) {
+        const F2 x = fma2(F2(c.get(k), c.get(k + 1)), by, less);
+        v[k] = exp2_fast(x.lo()), v[k + 1] = exp2_fast(x.hi());
+      }
       if (__any_sync(kFull, tj >= 0)) {
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] -= tj == k ? 1.0f : 0.0f;
       }
 #pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] *= g;
-      if (t < 0 || col0 + j * 32 + 32 > a.here) {  // no gradient: zeros, whatever the logits are
+      for (int k = 0; k < 32; k += 2) (F2(v[k], v[k + 1]) * g).get(v[k], v[k + 1]);
+      if (__any_sync(kFull, t < 0) || col0 + j * 32 + 32 > a.here) {  // the last tiles: zeros, whatever the logits are
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = t < 0 || col0 + j * 32 + k >= a.here ? 0.0f : v[k];
       }
@@ -197,7 +198,7 @@ struct GradJob {
           for (int k = 0; k < 16; ++k) f[k] = v[q * 16 + k];
           Pack<T, 16> p;
           p.set(f);
-          store32(dst + j * 32 + q * 16, p.w);
+          store32(dst + (j / 2 * a.dz_rows) * 64 + j % 2 * 32 + q * 16, p.w);
         }
       }
     });
@@ -219,7 +220,7 @@ struct OutJob {
   };
   struct Row {
     float alpha;
-    int64_t out;           // row of out, or -1
+    int out;               // row of out, or -1
     __device__ __forceinline__ void load(const Args& a, const PairItem& it, int row) {
       alpha = a.meta[1];
       const int64_t i = a.first + static_cast<int64_t>(it.m) * kPairM + row;
@@ -227,7 +228,7 @@ struct OutJob {
       if (a.place != nullptr) {
         if (i < *a.live) out = a.place[i];
       } else if (i < a.rows) {
-        out = i;
+        out = static_cast<int>(i);
       }
     }
   };
@@ -256,15 +257,18 @@ struct OutJob {
         return;
       }
       // Rows that begin anywhere: through shared memory, so that a warp's store lies in one row instead of 32.
-      uint32_t* mine = reinterpret_cast<uint32_t*>(staging) + lane * (kStageRow / 2);
+      const uint32_t words = smem_u32(staging) + lane * (kStageRow * 2), column = smem_u32(staging) + lane * 2;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) mine[k] = p[k / 8].w[k % 8];
+      for (int k = 0; k < 16; ++k) asm volatile("st.shared.u32 [%0], %1;" ::"r"(words + k * 4), "r"(p[k / 8].w[k % 8]) : "memory");
       __syncwarp();
+      uint16_t v[32];
+#pragma unroll
+      for (int x = 0; x < 32; ++x) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[x]) : "r"(column + x * (kStageRow * 2)) : "memory");
       uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + col0 + j * 32 + lane;
-#pragma unroll 4
+#pragma unroll
       for (int x = 0; x < 32; ++x) {
-        const int64_t to = __shfl_sync(kFull, r.out, x);
-        if (to >= 0 && lane < left) dst[to * a.stride] = staging[x * kStageRow + lane];
+        const int to = __shfl_sync(kFull, r.out, x);
+        if (to >= 0 && lane < left) dst[to * a.stride] = v[x];
       }
       __syncwarp();
     });
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(kSelectThreads) loss_select_kernel(const __gri
     base += all;
     __syncthreads();
   }
-  for (int j = base + threadIdx.x; j < filled(base, a.tokens); j += kSelectThreads) {
+  for (int j = base + threadIdx.x; j < filled(base); j += kSelectThreads) {
     a.target[j] = -1;
     if (BACKWARD) a.coef[j] = 0.0f, a.lse2[j] = 0.0f;
   }
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kCopyThreads) loss_copy_kernel(const __grid_co
     return;
   }
   const int live = *a.live;
-  copy_rows(a.hidden_copy, a.hidden, filled(live, a.tokens), a.hidden_stride, a.dim, a.dim_pad, t, n,
+  copy_rows(a.hidden_copy, a.hidden, filled(live), a.hidden_stride, a.dim, a.dim_pad, t, n,
             [&](int64_t r) { return r < live ? static_cast<int64_t>(a.place[r]) : int64_t(-1); });
   if (a.dhidden == nullptr || live == a.tokens) return;
   for (int64_t i = t / kWarp; i < a.tokens; i += n / kWarp)
@@ -679,8 +683,9 @@ constexpr int kFewTokens = 32;
 // Blocks of k up to which one pair makes a whole tile of dhidden, with no sums to join after it.
 constexpr int kDirectBlocks = 24;
 
-// Columns of a tile of the gradients' products: 128 where tiles of 256 would be a fifth or more emptier.
-int gradient_bn(int dim) { return round_up(dim, 128) * 5 <= round_up(dim, 256) * 4 ? 128 : 256; }
+// Columns of a tile of the gradients' products.  (A block of k takes as long with 128 columns as with 256, 310 against 335 ns, so
+// that the narrow tile pays only where the wide one has nothing in its other half.)
+int gradient_bn(int dim) { return dim <= 128 ? 128 : 256; }
 
 template <typename T, int BN>
 tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, void* dhidden, void* dweight, char* ws,
@@ -702,16 +707,16 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
     const int here = static_cast<int>(a.rows - first < l.piece ? a.rows - first : l.piece);
     const int v_tiles = static_cast<int>(ceil_div(here, 256)), f = static_cast<int>(first);
     typename Grad::Args ga{maps[0], maps[1],
-                           PairShape{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 0, pair_idesc(bf16, 256, false, false), live, nullptr},
+                           PairShape{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 0, pair_idesc(bf16, 256, false, false), live, nullptr, 0},
                            {meta, live, reinterpret_cast<const float*>(ws + l.coef), reinterpret_cast<const float*>(ws + l.lse2),
-                            reinterpret_cast<const int*>(ws + l.target), dz, l.piece, N, f, here, a.scale * kLog2e}};
+                            reinterpret_cast<const int*>(ws + l.target), dz, l.dz_rows, f, here, a.scale * kLog2e}};
     if ((st = launch_product<256, 128, Grad>(ga, a, dev, s)) != TBE_OK) return st;
     // dhidden += dz [tokens, piece] by weight [piece, dim];  dweight = dz^T [piece, tokens] by hidden [tokens, dim]
     const PairShape sum{m_tiles, d_tiles, l.splits, static_cast<int>(ceil_div(here, kPairK)), 0, 0, 0, f, 0, pair_idesc(bf16, BN, false, true),
-                        live, nullptr};
+                        live, nullptr, static_cast<int>(l.dz_rows)};
     typename Out::Args oa{maps[4], maps[5],
                           PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, 1, pair_idesc(bf16, BN, true, true),
-                                    nullptr, live},
+                                    nullptr, live, static_cast<int>(l.dz_rows)},
                           {meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, nullptr, nullptr, a.dim,
                            store_bytes(dweight, a.dweight_stride)}};
     const int64_t items = static_cast<int64_t>(sum.items()) + oa.g.items();
@@ -766,9 +771,9 @@ LossForwardLayout loss_forward_layout(const LossArgs& a) {
   l.ticket = place(&at, 256 + ceil_div(a.tokens, kWarp) * static_cast<int64_t>(sizeof(BlockSum)));  // and the blocks' sums
   l.live = place(&at, 4);
   l.place = place(&at, a.tokens * 4);
-  l.target = place(&at, a.tokens * 4);
+  l.target = place(&at, round_up(a.tokens, kPairM) * 4);
   l.row = place(&at, a.tokens * 4);
-  l.hidden = place(&at, a.tokens * dim_pad * 2);
+  l.hidden = place(&at, round_up(a.tokens, kPairM) * dim_pad * 2);
   l.weight = place(&at, a.copy_weight ? a.rows * dim_pad * 2 : 0);
   l.total = at;
   return l;
@@ -778,7 +783,7 @@ LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev
   LossBackwardLayout l{};
   size_t at = 0;
   l.dim_pad = round_up(a.dim, 8);
-  int64_t most = kPieceBytes / 2 / (a.tokens > 0 ? a.tokens : 1) / 256 * 256;
+  int64_t most = kPieceBytes / 2 / round_up(a.tokens > 0 ? a.tokens : 1, kPairM) / 256 * 256;
   if (most < 256) most = 256;
   if (most > (1 << 30)) most = 1 << 30;
   const int64_t pieces = ceil_div(a.rows, most);
@@ -799,15 +804,16 @@ LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev
   l.meta = place(&at, 16);
   l.live = place(&at, 4);
   l.place = place(&at, a.tokens * 4);
-  l.target = place(&at, a.tokens * 4);
+  l.dz_rows = round_up(a.tokens, kPairM);
+  l.target = place(&at, l.dz_rows * 4);
   l.row = place(&at, a.tokens * 4);
-  l.coef = place(&at, a.tokens * 4);
-  l.lse2 = place(&at, a.tokens * 4);
-  l.hidden = place(&at, a.tokens * l.dim_pad * 2);
+  l.coef = place(&at, l.dz_rows * 4);
+  l.lse2 = place(&at, l.dz_rows * 4);
+  l.hidden = place(&at, l.dz_rows * l.dim_pad * 2);
   l.weight = place(&at, a.copy_weight ? a.rows * l.dim_pad * 2 : 0);
   // What these two take varies with the number of tokens both ways: as much as any smaller number may need, so that a
   // workspace for the largest call serves every call.
-  const int64_t whole = a.tokens * round_up(a.rows, 256) * 2, least = a.tokens * 512;
+  const int64_t whole = l.dz_rows * round_up(a.rows, 256) * 2, least = l.dz_rows * 512;
   const int64_t capped = least > kPieceBytes ? least : kPieceBytes;
   l.dz = place(&at, whole < capped ? whole : capped);
   // splits * tiles < 2 pairs + tiles
@@ -857,7 +863,7 @@ tbe_status launch_loss_forward(const LossArgs& a, const LossForwardLayout& l, co
   const bool carry = m_tiles == 1 && v_tiles > pairs;
   const Stats::Args sa{ma, mb,
                        PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, 0, pair_idesc(bf16, 256, false, false),
-                                 select ? live : nullptr, nullptr},
+                                 select ? live : nullptr, nullptr, 0},
                        {targets, select ? selected : nullptr, live, part, target_logit, ticket, l.parts_rows, a.rows, static_cast<int>(a.tokens), a.itype,
                         carry, a.scale, a.scale * kLog2e}};
   st = few ? launch_product<256, kFewTokens, Stats>(sa, a, dev, s) : launch_product<256, 128, Stats>(sa, a, dev, s);
@@ -897,8 +903,8 @@ tbe_status launch_loss_backward(const LossArgs& a, const LossBackwardLayout& l, 
   const void* dz = ws + l.dz;
   CUtensorMap maps[6];
   if (!encode_operand(&maps[0], h, bf16, a.dim, a.tokens, l.dim_pad, 128) || !encode_operand(&maps[1], weight, bf16, a.dim, a.rows, wst, 128) ||
-      !encode_operand(&maps[2], dz, bf16, l.piece, a.tokens, l.piece, 128) || !encode_operand(&maps[3], weight, bf16, a.dim, a.rows, wst, 64) ||
-      !encode_operand(&maps[4], dz, bf16, l.piece, a.tokens, l.piece, 64) || !encode_operand(&maps[5], h, bf16, a.dim, a.tokens, l.dim_pad, 64))
+      !encode_operand(&maps[2], dz, bf16, 64, l.piece / 64 * l.dz_rows, 64, 128) || !encode_operand(&maps[3], weight, bf16, a.dim, a.rows, wst, 64) ||
+      !encode_operand(&maps[4], dz, bf16, 64, l.piece / 64 * l.dz_rows, 64, 64) || !encode_operand(&maps[5], h, bf16, a.dim, a.tokens, l.dim_pad, 64))
     return cuda_status(cudaErrorInvalidValue);
   if (bf16) return loss_backward_t<__nv_bfloat16>(a, l, maps, dhidden, dweight, ws, dev, s);
   return loss_backward_t<__half>(a, l, maps, dhidden, dweight, ws, dev, s);

@@ -50,6 +50,7 @@ struct PairShape {
   uint32_t idesc;
   const int* live_m;
   const int* live_k;
+  int a_rows;       // 0, or A lies in blocks of 64 columns, each a_rows rows of 128 bytes: what a copy takes is contiguous then
 
   __device__ __forceinline__ void settle() {
     if (live_m != nullptr) m_tiles = (max(*live_m, 1) + kPairM - 1) / kPairM;
@@ -250,9 +251,13 @@ __device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairS
       const CUtensorMap* map = A ? &p.a : &p.b;
       if constexpr (A ? P::kAMN : P::kBMN) {
 #pragma unroll
-        for (int c = 0; c < (A ? 2 : BN / 128); ++c) pair::tma_2d(to + c * 8192, map, x + c * 64, k, bar);
+        for (int c = 0; c < (A ? 2 : BN / 128); ++c) {
+          if (A && g.a_rows > 0) pair::tma_2d(to + c * 8192, map, 0, (x / 64 + c) * g.a_rows + k, bar);
+          else pair::tma_2d(to + c * 8192, map, x + c * 64, k, bar);
+        }
       } else {
-        pair::tma_2d(to, map, k, x, bar);
+        if (A && g.a_rows > 0) pair::tma_2d(to, map, 0, k / 64 * g.a_rows + x, bar);
+        else pair::tma_2d(to, map, k, x, bar);
       }
     }
   }

@@ -32,6 +32,7 @@ struct LossForwardLayout {
 struct LossBackwardLayout {
   int64_t dim_pad;                 // row of the fp32 sums of dhidden
   int64_t piece;                   // rows of the table at a time
+  int64_t dz_rows;                 // of a block of 64 columns of dz
   int splits;                      // parts of the long product of dhidden
   bool direct;                     // it is written as it is: one piece, one split
   size_t meta, live, place, target, row, coef, lse2, hidden, weight, dz, sums, total;
