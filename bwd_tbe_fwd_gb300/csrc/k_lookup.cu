@@ -41,10 +41,11 @@ __device__ __forceinline__ int64_t split(int64_t x, int groups) {
   return x >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(groups)) : x / groups;
 }
 
-// A thread takes V elements of U tokens at a time, U rows in flight.
+// A thread takes V elements of U tokens at a time, U rows in flight.  (131072 rows of 128 fp16 to fp32, 2 at a time: 18.4 us; 4: 20.4,
+// 8: 22.6; 82 MB, at the copy rate 12.1.)
 template <typename TT, typename OT, int V>
 __global__ void __launch_bounds__(kFwdThreads) lookup_forward_kernel(const __grid_constant__ ForwardArgs a) {
-  constexpr int U = 4;
+  constexpr int U = 2;
   const int64_t total = a.tokens * a.groups, step = static_cast<int64_t>(gridDim.x) * kFwdThreads;
   unsigned bad = 0;  // counted at the end: an atomic between the loads would hold them apart
   for (int64_t x0 = static_cast<int64_t>(blockIdx.x) * kFwdThreads + threadIdx.x; x0 < total; x0 += U * step) {

@@ -60,6 +60,33 @@ __device__ __forceinline__ void each_columns(uint32_t tmem, R&& release, F&& f) 
   }
 }
 
+// A warp's 32 rows of 64 16-bit elements by way of shared memory, so that a store has whole 128-byte lines of 4 rows instead of a
+// sector of each of 32: a thread puts 32 elements of its row (the `half`-th) there, and all of them store together; the
+// pieces of 16 bytes are exchanged within a row by its number, so that no 8 rows meet in the same banks.
+template <typename T>
+__device__ __forceinline__ void stage_half(uint32_t staging, int lane, int half, const Pack<T, 16> (&p)[2]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t at = staging + lane * 128 + (((half * 4 + q) ^ (lane & 7)) << 4);
+    const uint32_t* w = p[q / 2].w + q % 2 * 4;
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+  }
+}
+// f(row, c, piece): the 8 elements from column 8 c on of the warp's row `row`.
+template <typename F>
+__device__ __forceinline__ void unstage(uint32_t staging, int lane, F&& f) {
+  __syncwarp();
+  uint4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = i * 4 + lane / 8;
+    shared_words<16>(staging + row * 128 + (((lane & 7) ^ (row & 7)) << 4), reinterpret_cast<uint32_t*>(&v[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f(i * 4 + lane / 8, lane & 7, v[i]);
+  __syncwarp();
+}
+
 // A row's part of the softmax over half a tile's columns: {maximum of z in powers of 2, sum of 2^(z - maximum)}.
 struct StatsJob {
   struct Args {
@@ -91,7 +118,7 @@ struct StatsJob {
   };
   template <typename R>
   static __device__ __forceinline__ void tile(const Args& a, const Row& r, State& s, const PairItem& it, int row, int half, uint32_t tmem,
-                                              uint16_t*, R&& release) {
+                                              uint32_t, R&& release) {
     const int i = it.m * kPairM + row;
     const int64_t col0 = static_cast<int64_t>(it.n) * 256 + half * 128;
     if (it.m == 0 && it.n == 0 && row == 0 && half == 0) *a.ticket = 0;
@@ -152,26 +179,25 @@ struct GradJob {
     float scale2;
   };
   struct Row {
-    int target;
+    int target, rows;        // rows: of the warp's 32, how many there are
     float coef, lse2, power;
-    bool in;
     __device__ __forceinline__ void load(const Args& a, const PairItem& it, int row) {
       const int i = it.m * kPairM + row;
       target = -1, coef = 0.0f, lse2 = 0.0f;
       power = a.meta[0];
-      in = i < filled(*a.live);
-      if (in) target = a.target[i], coef = a.coef[i], lse2 = a.lse2[i];
+      rows = filled(*a.live) - i + lane_id();
+      if (i < filled(*a.live)) target = a.target[i], coef = a.coef[i], lse2 = a.lse2[i];
     }
   };
   using State = NoState;
   template <typename R>
   static __device__ __forceinline__ void tile(const Args& a, const Row& r, State&, const PairItem& it, int row, int half, uint32_t tmem,
-                                              uint16_t*, R&& release) {
-    const int i = it.m * kPairM + row;
+                                              uint32_t staging, R&& release) {
+    const int i = it.m * kPairM + row, lane = lane_id();
     const int col0 = it.n * 256 + half * 128, t = r.target;
     const int tl = t < 0 ? -1 : t - a.first - col0;
     const F2 g(r.coef * r.power), by(a.scale2), less(-r.lse2);
-    T* dst = a.dz + (col0 / 64 * a.dz_rows + i) * 64;
+    T* first = a.dz + (col0 / 64 * a.dz_rows + i - lane) * 64;   // the warp's first row
     each_columns<128>(tmem, release, [&](int j, pair::Columns& c) {
       const int tj = tl >= j * 32 && tl < j * 32 + 32 ? tl - j * 32 : -1;
       float v[32];
@@ -190,21 +216,27 @@ struct GradJob {
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = t < 0 || col0 + j * 32 + k >= a.here ? 0.0f : v[k];
       }
-      if (r.in) {
+      Pack<T, 16> p[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float f[16];
+      for (int q = 0; q < 2; ++q) {
+        float f[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] = v[q * 16 + k];
-          Pack<T, 16> p;
-          p.set(f);
-          store32(dst + (j / 2 * a.dz_rows) * 64 + j % 2 * 32 + q * 16, p.w);
-        }
+        for (int k = 0; k < 16; ++k) f[k] = v[q * 16 + k];
+        p[q].set(f);
+      }
+      stage_half<T>(staging, lane, j & 1, p);
+      if (j & 1) {
+        T* dst = first + j / 2 * a.dz_rows * 64;
+        unstage(staging, lane, [&](int x, int c, const uint4& piece) {
+          if (x < r.rows) *reinterpret_cast<uint4*>(dst + x * 64 + c * 8) = piece;
+        });
       }
     });
   }
   static __device__ __forceinline__ void finish(const Args&, const State&, int, int, int) {}
 };
+
+constexpr int kStageRow = 34;  // elements from one row to the next of rows that begin anywhere: 17 words, no bank twice
 
 // A gradient's rows: the product times alpha, rounded.
 template <typename T, int BN>
@@ -216,7 +248,7 @@ struct OutJob {
     const int* place;      // NULL, or the row of out for each row of the product, of which there are *live
     const int* live;
     int cols;
-    int vec;               // bytes of a store that every row allows: 32, 16, or 0 for element by element
+    int vec;               // rows allow 16-byte stores
   };
   struct Row {
     float alpha;
@@ -235,7 +267,7 @@ struct OutJob {
   using State = NoState;
   template <typename R>
   static __device__ __forceinline__ void tile(const Args& a, const Row& r, State&, const PairItem& it, int row, int half, uint32_t tmem,
-                                              uint16_t* staging, R&& release) {
+                                              uint32_t staging, R&& release) {
     const int col0 = it.n * BN + half * (BN / 2), lane = lane_id();
     each_columns<BN / 2>(tmem, release, [&](int j, pair::Columns& c) {
       const int left = a.cols - col0 - j * 32;   // columns from this block's first on; the same for the whole warp
@@ -248,16 +280,22 @@ struct OutJob {
         for (int k = 0; k < 16; ++k) f[k] = c.get(q * 16 + k) * r.alpha;
         p[q].set(f);
       }
-      if (a.vec != 0 && left >= 32) {
-        T* dst = a.out + r.out * a.stride + col0 + j * 32;
-        if (r.out >= 0) {
-          if (a.vec == 32) store32(dst, p[0].w), store32(dst + 16, p[1].w);
-          else p[0].store(dst), p[1].store(dst + 16);
+      if (a.vec) {
+        stage_half<T>(staging, lane, j & 1, p);
+        if ((j & 1) || left <= 32) {
+          T* dst = a.out + col0 + j / 2 * 64;
+          const int cols = a.cols - col0 - j / 2 * 64;
+          unstage(staging, lane, [&](int x, int c, const uint4& piece) {
+            const int to = __shfl_sync(kFull, r.out, x);
+            if (to < 0 || c * 8 >= cols) return;
+            if (c * 8 + 8 <= cols) *reinterpret_cast<uint4*>(dst + to * a.stride + c * 8) = piece;
+            else reinterpret_cast<const Pack<T, 8>&>(piece).store_some(dst + to * a.stride + c * 8, cols - c * 8);
+          });
         }
         return;
       }
-      // Rows that begin anywhere: through shared memory, so that a warp's store lies in one row instead of 32.
-      const uint32_t words = smem_u32(staging) + lane * (kStageRow * 2), column = smem_u32(staging) + lane * 2;
+      // Rows that begin anywhere: 32 elements of a row to a store.
+      const uint32_t words = staging + lane * (kStageRow * 2), column = staging + lane * 2;
 #pragma unroll
       for (int k = 0; k < 16; ++k) asm volatile("st.shared.u32 [%0], %1;" ::"r"(words + k * 4), "r"(p[k / 8].w[k % 8]) : "memory");
       __syncwarp();
@@ -288,7 +326,7 @@ struct SumJob {
   using Row = NoRow;
   using State = NoState;
   template <typename R>
-  static __device__ __forceinline__ void tile(const Args& a, const Row&, State&, const PairItem& it, int row, int half, uint32_t tmem, uint16_t*,
+  static __device__ __forceinline__ void tile(const Args& a, const Row&, State&, const PairItem& it, int row, int half, uint32_t tmem, uint32_t,
                                               R&& release) {
     const int i = it.m * kPairM + row;
     const int col0 = it.n * BN + half * (BN / 2);
@@ -318,6 +356,65 @@ struct SumJob {
 // ------------------------------------------------------------------------------------------
 // Before and after the products
 // ------------------------------------------------------------------------------------------
+// Rows copied to where TMA can address them (and, of hidden, those of the selected tokens one after the other, with zeros in the
+// rows that fill up the last block of k), and zeros in the rows of dhidden of the tokens that are not selected.
+struct CopyArgs {
+  const int* live;      // with place and row: of loss_select_kernel; NULL for all tokens
+  const int* place;
+  const int* row;
+  const uint16_t* hidden;
+  const uint16_t* weight;
+  uint16_t* hidden_copy;   // [.][dim_pad]
+  uint16_t* weight_copy;   // NULL: none
+  uint16_t* dhidden;       // NULL: none
+  int64_t tokens, rows, hidden_stride, weight_stride, dhidden_stride;
+  int dim, dim_pad;
+  int at_once;             // the CTA that selects gathers the rows too
+};
+
+// 8 elements of a row from column c on, zeros past its end.
+__device__ __forceinline__ uint4 row_piece(const uint16_t* src, int c, int dim, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(src + c);
+  uint32_t h[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) h[k] = c + k < dim ? src[c + k] : 0;
+  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+
+// 8 elements to a thread, two at a time; from(r): the row of src that is row r of dst, or -1 for zeros.
+template <typename F>
+__device__ __forceinline__ void copy_rows(uint16_t* dst, const uint16_t* src, int64_t rows, int64_t stride, int dim, int dim_pad,
+                                          int64_t t, int64_t n, F&& from) {
+  const int groups = dim_pad / 8;
+  const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && dim % 8 == 0 && stride % 8 == 0;
+  const int64_t total = rows * groups;
+  for (int64_t x0 = t; x0 < total; x0 += 2 * n) {
+    uint4 v[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t x = x0 + u * n;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (x >= total) continue;
+      const int64_t r = total >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(groups) : x / groups;
+      const int64_t f = from(r);
+      if (f >= 0) v[u] = row_piece(src + f * stride, static_cast<int>(x - r * groups) * 8, dim, vec);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (x0 + u * n < total) *reinterpret_cast<uint4*>(dst + (x0 + u * n) * 8) = v[u];
+  }
+}
+
+// The selected tokens' rows by n threads of which this is number t; place and row are written.
+__device__ __forceinline__ void gather_rows(const CopyArgs& a, int live, int64_t t, int64_t n) {
+  copy_rows(a.hidden_copy, a.hidden, filled(live), a.hidden_stride, a.dim, a.dim_pad, t, n,
+            [&](int64_t r) { return r < live ? static_cast<int64_t>(a.place[r]) : int64_t(-1); });
+  if (a.dhidden == nullptr || live == a.tokens) return;
+  for (int64_t i = t / kWarp; i < a.tokens; i += n / kWarp)
+    if (a.row[i] < 0)
+      for (int c = static_cast<int>(t % kWarp); c < a.dim; c += kWarp) a.dhidden[i * a.dhidden_stride + c] = 0;
+}
+
 // The tokens whose target is a row of the table, in their order, and what the products need of them: the others take no part in
 // any product, so that a batch with a third of padding costs a third less, and what their hidden rows hold is not looked at.
 struct SelectArgs {
@@ -346,14 +443,20 @@ __device__ __forceinline__ float coefficient(const SelectArgs& a, int64_t i, flo
 constexpr int kSelectThreads = 1024;
 constexpr int kCopyThreads = 256;
 
-// One CTA, 4 tokens to a thread at a time (8192 tokens: 4 us).
+// One CTA, 4 tokens to a thread at a time (8192 tokens: 4 us); the others, where there are any, copy the table meanwhile.
 template <bool BACKWARD>
-__global__ void __launch_bounds__(kSelectThreads) loss_select_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kSelectThreads) loss_select_kernel(const __grid_constant__ SelectArgs a, const __grid_constant__ CopyArgs c) {
   constexpr int kEach = 4, kWarps = kSelectThreads / kWarp;
   __shared__ int s_count[kWarps];
   __shared__ float s_top[kWarps];
   const int lane = lane_id(), w = threadIdx.x / kWarp;
   may_follow();
+  if (blockIdx.x > 0) {
+    copy_rows(c.weight_copy, c.weight, c.rows, c.weight_stride, c.dim, c.dim_pad,
+              static_cast<int64_t>(blockIdx.x - 1) * kSelectThreads + threadIdx.x, static_cast<int64_t>(gridDim.x - 1) * kSelectThreads,
+              [](int64_t r) { return r; });
+    return;
+  }
   const float mean = BACKWARD && a.mean != nullptr ? a.mean[1] : 1.0f;
   int base = 0;
   float top = 0.0f;
@@ -402,6 +505,10 @@ __global__ void __launch_bounds__(kSelectThreads) loss_select_kernel(const __gri
     if (BACKWARD) a.coef[j] = 0.0f, a.lse2[j] = 0.0f;
   }
   if (threadIdx.x == 0) *a.live = base;
+  if (c.at_once) {
+    __syncthreads();
+    gather_rows(c, base, threadIdx.x, kSelectThreads);
+  }
   if constexpr (BACKWARD) {
     // The largest finite coefficient takes dz to 2^13 .. 2^14: |p - onehot| is at most 1, fp16 ends at 2^16, and what is
     // 2^-27 of the largest is still a normal number there.
@@ -422,71 +529,14 @@ __global__ void __launch_bounds__(kSelectThreads) loss_select_kernel(const __gri
   }
 }
 
-// Rows copied to where TMA can address them (and, of hidden, those of the selected tokens one after the other, with zeros in the
-// rows that fill up the last block of k), and zeros in the rows of dhidden of the tokens that are not selected.
-struct CopyArgs {
-  const int* live;      // with place and row: of loss_select_kernel; NULL for all tokens
-  const int* place;
-  const int* row;
-  const uint16_t* hidden;
-  const uint16_t* weight;
-  uint16_t* hidden_copy;   // [.][dim_pad]
-  uint16_t* weight_copy;   // NULL: none
-  uint16_t* dhidden;       // NULL: none
-  int64_t tokens, rows, hidden_stride, weight_stride, dhidden_stride;
-  int dim, dim_pad;
-};
-
-// 8 elements of a row from column c on, zeros past its end.
-__device__ __forceinline__ uint4 row_piece(const uint16_t* src, int c, int dim, bool vec) {
-  if (vec) return *reinterpret_cast<const uint4*>(src + c);
-  uint32_t h[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) h[k] = c + k < dim ? src[c + k] : 0;
-  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-}
-
-// 8 elements to a thread, two at a time; from(r): the row of src that is row r of dst, or -1 for zeros.
-template <typename F>
-__device__ __forceinline__ void copy_rows(uint16_t* dst, const uint16_t* src, int64_t rows, int64_t stride, int dim, int dim_pad,
-                                          int64_t t, int64_t n, F&& from) {
-  const int groups = dim_pad / 8;
-  const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && dim % 8 == 0 && stride % 8 == 0;
-  const int64_t total = rows * groups;
-  for (int64_t x0 = t; x0 < total; x0 += 2 * n) {
-    uint4 v[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t x = x0 + u * n;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (x >= total) continue;
-      const int64_t r = total >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(groups) : x / groups;
-      const int64_t f = from(r);
-      if (f >= 0) v[u] = row_piece(src + f * stride, static_cast<int>(x - r * groups) * 8, dim, vec);
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      if (x0 + u * n < total) *reinterpret_cast<uint4*>(dst + (x0 + u * n) * 8) = v[u];
-  }
-}
-
 __global__ void __launch_bounds__(kCopyThreads) loss_copy_kernel(const __grid_constant__ CopyArgs a) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, n = static_cast<int64_t>(gridDim.x) * kCopyThreads;
   may_follow();
   wait_before();
   if (a.weight_copy != nullptr)
     copy_rows(a.weight_copy, a.weight, a.rows, a.weight_stride, a.dim, a.dim_pad, t, n, [](int64_t r) { return r; });
-  if (a.live == nullptr) {
-    copy_rows(a.hidden_copy, a.hidden, a.tokens, a.hidden_stride, a.dim, a.dim_pad, t, n, [](int64_t r) { return r; });
-    return;
-  }
-  const int live = *a.live;
-  copy_rows(a.hidden_copy, a.hidden, filled(live), a.hidden_stride, a.dim, a.dim_pad, t, n,
-            [&](int64_t r) { return r < live ? static_cast<int64_t>(a.place[r]) : int64_t(-1); });
-  if (a.dhidden == nullptr || live == a.tokens) return;
-  for (int64_t i = t / kWarp; i < a.tokens; i += n / kWarp)
-    if (a.row[i] < 0)
-      for (int c = static_cast<int>(t % kWarp); c < a.dim; c += kWarp) a.dhidden[i * a.dhidden_stride + c] = 0;
+  if (a.live != nullptr) gather_rows(a, *a.live, t, n);
+  else copy_rows(a.hidden_copy, a.hidden, a.tokens, a.hidden_stride, a.dim, a.dim_pad, t, n, [](int64_t r) { return r; });
 }
 
 // Joins the parts of 32 tokens' rows, a lane to a token, the parts dealt out to the warps; the last block adds up the losses.
@@ -645,18 +695,28 @@ tbe_status launch_product(const typename P::Args& p, const LossArgs& a, const De
   return launch_pair<BN, AM, P, NoProduct>(p, NoProduct::Args{}, p.g.items(), a, dev, s);
 }
 
-template <bool BACKWARD>
-tbe_status launch_select(const SelectArgs& p, cudaStream_t s) {
-  loss_select_kernel<BACKWARD><<<1, kSelectThreads, 0, s>>>(p);
-  note_launch();
-  return cuda_status(cudaGetLastError());
-}
-
 tbe_status launch_copy(const CopyArgs& p, const DeviceInfo& dev, cudaStream_t s) {
   const int64_t rows = p.tokens + (p.weight_copy != nullptr ? p.rows : 0);
   int64_t blocks = ceil_div(rows * (p.dim_pad / 8), 2 * kCopyThreads);
   if (blocks > dev.sms * 8) blocks = dev.sms * 8;
   return cuda_status(launch_after(loss_copy_kernel, static_cast<unsigned>(blocks), kCopyThreads, 0, s, p));
+}
+
+// Elements of hidden up to which the CTA that selects gathers them as well: 16 to a thread, which takes less than a launch.
+constexpr int64_t kAtOnce = 16 * kSelectThreads;
+
+// Selects the tokens and gathers their rows.  The table's copy, where c has one, is made beside the selection.
+template <bool BACKWARD>
+tbe_status launch_select(const SelectArgs& p, CopyArgs& c, const DeviceInfo& dev, cudaStream_t s) {
+  c.live = p.live, c.place = p.place, c.row = p.row;
+  c.at_once = c.tokens * c.dim_pad <= kAtOnce;
+  int64_t blocks = c.weight_copy == nullptr ? 0 : ceil_div(c.rows * (c.dim_pad / 8), 2 * kSelectThreads);
+  if (blocks > dev.sms * 2 - 1) blocks = dev.sms * 2 - 1;
+  loss_select_kernel<BACKWARD><<<static_cast<unsigned>(1 + blocks), kSelectThreads, 0, s>>>(p, c);
+  note_launch();
+  const tbe_status st = cuda_status(cudaGetLastError());
+  c.weight_copy = nullptr;
+  return st != TBE_OK || c.at_once ? st : launch_copy(c, dev, s);
 }
 
 size_t place(size_t* at, int64_t bytes) {
@@ -665,10 +725,8 @@ size_t place(size_t* at, int64_t bytes) {
   return here;
 }
 
-// Bytes of a store that every row allows.
-int store_bytes(const void* p, int64_t stride) {
-  return stride % 16 == 0 && is_aligned(p, 32) ? 32 : stride % 8 == 0 && is_aligned(p, 16) ? 16 : 0;
-}
+// Rows that allow 16-byte stores.
+int whole_stores(const void* p, int64_t stride) { return stride % 8 == 0 && is_aligned(p, 16); }
 
 // Bytes of dz that a piece of the table may take.
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
@@ -683,9 +741,9 @@ constexpr int kFewTokens = 32;
 // Blocks of k up to which one pair makes a whole tile of dhidden, with no sums to join after it.
 constexpr int kDirectBlocks = 24;
 
-// Columns of a tile of the gradients' products.  (A block of k takes as long with 128 columns as with 256, 310 against 335 ns, so
-// that the narrow tile pays only where the wide one has nothing in its other half.)
-int gradient_bn(int dim) { return dim <= 128 ? 128 : 256; }
+// Columns of a tile of the gradients' products: 128 where tiles of 256 would be a fifth or more emptier (301 columns: 188 us a call
+// with 128, 198 with 256; a block of k of a tile of 128 takes nearly as long, 310 against 335 ns, but the clock holds up).
+int gradient_bn(int dim) { return round_up(dim, 128) * 5 <= round_up(dim, 256) * 4 ? 128 : 256; }
 
 template <typename T, int BN>
 tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, void* dhidden, void* dweight, char* ws,
@@ -718,12 +776,12 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
                           PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, 1, pair_idesc(bf16, BN, true, true),
                                     nullptr, live, static_cast<int>(l.dz_rows)},
                           {meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, nullptr, nullptr, a.dim,
-                           store_bytes(dweight, a.dweight_stride)}};
+                           whole_stores(dweight, a.dweight_stride)}};
     const int64_t items = static_cast<int64_t>(sum.items()) + oa.g.items();
     if (l.direct) {
       typename Direct::Args da{maps[2], maps[3], sum,
                                {meta, static_cast<T*>(dhidden), a.dhidden_stride, 0, a.tokens, placed, live, a.dim,
-                                store_bytes(dhidden, a.dhidden_stride)}};
+                                whole_stores(dhidden, a.dhidden_stride)}};
       st = launch_pair<BN, 128, Direct, Out>(da, oa, items, a, dev, s);
     } else {
       typename Sum::Args sa{maps[2], maps[3], sum, {sums, l.dim_pad, N, first > 0}};
@@ -733,7 +791,7 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
   }
   if (l.direct) return TBE_OK;
   FinishArgs<T> fa{sums, meta, live, placed, static_cast<T*>(dhidden), a.tokens, l.dim_pad, a.dhidden_stride, l.splits, a.dim,
-                   store_bytes(dhidden, a.dhidden_stride) != 0};
+                   whole_stores(dhidden, a.dhidden_stride)};
   int64_t blocks = ceil_div(a.tokens * (l.dim_pad / 8), 256);
   if (blocks > dev.sms * 8) blocks = dev.sms * 8;
   return cuda_status(launch_after(loss_finish_kernel<T>, static_cast<unsigned>(blocks), 256, 0, s, fa));
@@ -833,21 +891,22 @@ tbe_status launch_loss_forward(const LossArgs& a, const LossForwardLayout& l, co
   int* row = reinterpret_cast<int*>(ws + l.row);
   tbe_status st;
   int64_t hs = a.hidden_stride, wst = a.weight_stride;
-  if (select) {
-    SelectArgs p{};
-    p.targets = targets, p.tokens = a.tokens, p.rows = a.rows, p.itype = a.itype;
-    p.live = live, p.place = reinterpret_cast<int*>(ws + l.place), p.target = selected, p.row = row;
-    if ((st = launch_select<false>(p, s)) != TBE_OK) return st;
-  }
   if (select || a.copy_hidden || a.copy_weight) {
-    CopyArgs p{};
-    if (select) p.live = live, p.place = reinterpret_cast<int*>(ws + l.place), p.row = row;
-    p.hidden = static_cast<const uint16_t*>(hidden), p.weight = static_cast<const uint16_t*>(weight);
-    p.hidden_copy = reinterpret_cast<uint16_t*>(ws + l.hidden);
-    if (a.copy_weight) p.weight_copy = reinterpret_cast<uint16_t*>(ws + l.weight);
-    p.tokens = a.tokens, p.rows = a.rows, p.hidden_stride = a.hidden_stride, p.weight_stride = a.weight_stride;
-    p.dim = a.dim, p.dim_pad = dim_pad;
-    if ((st = launch_copy(p, dev, s)) != TBE_OK) return st;
+    CopyArgs c{};
+    c.hidden = static_cast<const uint16_t*>(hidden), c.weight = static_cast<const uint16_t*>(weight);
+    c.hidden_copy = reinterpret_cast<uint16_t*>(ws + l.hidden);
+    if (a.copy_weight) c.weight_copy = reinterpret_cast<uint16_t*>(ws + l.weight);
+    c.tokens = a.tokens, c.rows = a.rows, c.hidden_stride = a.hidden_stride, c.weight_stride = a.weight_stride;
+    c.dim = a.dim, c.dim_pad = dim_pad;
+    if (select) {
+      SelectArgs p{};
+      p.targets = targets, p.tokens = a.tokens, p.rows = a.rows, p.itype = a.itype;
+      p.live = live, p.place = reinterpret_cast<int*>(ws + l.place), p.target = selected, p.row = row;
+      st = launch_select<false>(p, c, dev, s);
+    } else {
+      st = launch_copy(c, dev, s);
+    }
+    if (st != TBE_OK) return st;
     hidden = ws + l.hidden, hs = dim_pad;
     if (a.copy_weight) weight = ws + l.weight, wst = dim_pad;
   }
@@ -886,17 +945,15 @@ tbe_status launch_loss_backward(const LossArgs& a, const LossBackwardLayout& l, 
   p.lse = lse, p.dloss = dloss, p.mean = mean, p.scale = a.scale;
   p.meta = reinterpret_cast<float*>(ws + l.meta), p.coef = reinterpret_cast<float*>(ws + l.coef);
   p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
-  tbe_status st = launch_select<true>(p, s);
-  if (st != TBE_OK) return st;
   CopyArgs c{};
-  c.live = p.live, c.place = p.place, c.row = p.row;
   c.hidden = static_cast<const uint16_t*>(hidden), c.weight = static_cast<const uint16_t*>(weight);
   c.hidden_copy = reinterpret_cast<uint16_t*>(ws + l.hidden);
   if (a.copy_weight) c.weight_copy = reinterpret_cast<uint16_t*>(ws + l.weight);
   c.dhidden = static_cast<uint16_t*>(dhidden);
   c.tokens = a.tokens, c.rows = a.rows, c.hidden_stride = a.hidden_stride, c.weight_stride = a.weight_stride;
   c.dhidden_stride = a.dhidden_stride, c.dim = a.dim, c.dim_pad = static_cast<int>(l.dim_pad);
-  if ((st = launch_copy(c, dev, s)) != TBE_OK) return st;
+  const tbe_status st = launch_select<true>(p, c, dev, s);
+  if (st != TBE_OK) return st;
   const void* h = ws + l.hidden;
   const int64_t wst = a.copy_weight ? l.dim_pad : a.weight_stride;
   if (a.copy_weight) weight = ws + l.weight;

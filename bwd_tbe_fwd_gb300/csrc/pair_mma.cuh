@@ -26,7 +26,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 32 * (kEpiWarps + 3);
 constexpr uint32_t kPairWaitLimit = 1u << 22;
 
-constexpr int kStageRow = 34;          // 16-bit elements from one row of a warp's staging area to the next: 17 words, no bank twice
+constexpr int kStagingBytes = 4096;    // of a warp of the epilogue: 32 rows of 64 16-bit elements
 
 // AM: rows of A that a CTA copies.  With fewer than 128 (products of few rows, bound by B's way through memory) the products
 // read what lies behind them as the others, whose results nobody looks at, and the ring has more stages.
@@ -37,8 +37,7 @@ struct PairTile {
   static constexpr int kStage = kA + kB;
   static constexpr int kStages = 196608 / kStage;        // 6 of 32 KB, 8 of 24 KB, 9 of 20 KB
   static_assert(kStage >= 128 * kPairK * 2, "the products read 128 rows of A from a stage's start");
-  static constexpr int kStaging = kEpiWarps * 32 * kStageRow * 2;       // 32 x 32 16-bit elements to a warp of the epilogue
-  static constexpr int kSmem = kStages * kStage + kStaging + 1024;      // and room to align to the swizzle's 1024 bytes
+  static constexpr int kSmem = kStages * kStage + kEpiWarps * kStagingBytes + 1024;  // and room to align to the swizzle's 1024 bytes
 };
 
 // A product: its tiles, and where it starts in A's and B's coordinates.  With `live`, the number of rows (m) or the length of
@@ -294,7 +293,7 @@ __device__ __forceinline__ void pair_multiply(const PairShape& g, PairWalk walk,
 
 template <int BN, class P>
 __device__ __forceinline__ void pair_epilogue(const typename P::Args& p, const PairShape& g, PairWalk walk, PairRole& r, int pair, int w,
-                                              int lane, uint16_t* staging) {
+                                              int lane, uint32_t staging) {
   using Job = typename P::Job;
   const int row = static_cast<int>(r.rank) * 128 + (w % 4) * 32 + lane, half = w / 4;
   typename Job::State state{};
@@ -396,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     __syncwarp();
   } else {
-    uint16_t* staging = reinterpret_cast<uint16_t*>(s_raw + (ring - smem_u32(s_raw)) + ST * T::kStage) + w * 32 * kStageRow;
+    const uint32_t staging = ring + ST * T::kStage + w * kStagingBytes;
     pair_epilogue<BN, P0>(p0, g0, walk0, r, pair_id, w, lane, staging);
     if constexpr (!P1::kNone)
       if (!r.failed) pair_epilogue<BN, P1>(p1, g1, walk1, r, pair_id, w, lane, staging);
