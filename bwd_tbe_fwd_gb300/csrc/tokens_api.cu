@@ -120,7 +120,8 @@ tbe_status tbe_softmax_loss_forward(const tbe_softmax_problem* prob, const void*
   tbe_status st = make_loss(prob, d_stats, false, &a);
   if (st != TBE_OK) return st;
   if (!buffer_ok(mean, 4)) return TBE_ERR_INVALID_ARG;
-  if (a.tokens > 0 && (!buffer_ok(hidden, a.copy_hidden ? 2 : 16) || !buffer_ok(weight, a.copy_weight ? 2 : 16) ||
+  if (!is_aligned(hidden, 16)) a.copy_hidden = true;
+  if (a.tokens > 0 && (!buffer_ok(hidden, 2) || !buffer_ok(weight, a.copy_weight ? 2 : 16) ||
                        !buffer_ok(targets, itype_bytes(a.itype)) || !buffer_ok(loss, 4) || !buffer_ok(lse, 4)))
     return TBE_ERR_INVALID_ARG;
   const LossForwardLayout l = loss_forward_layout(a);
@@ -145,7 +146,7 @@ tbe_status tbe_softmax_loss_backward(const tbe_softmax_problem* prob, const void
   tbe_status st = make_loss(prob, d_stats, true, &a);
   if (st != TBE_OK) return st;
   if (!buffer_ok(dweight, 2) || !is_aligned(dloss, 4) || !is_aligned(mean, 4)) return TBE_ERR_INVALID_ARG;
-  if (a.tokens > 0 && (!buffer_ok(hidden, a.copy_hidden ? 2 : 16) || !buffer_ok(weight, a.copy_weight ? 2 : 16) ||
+  if (a.tokens > 0 && (!buffer_ok(hidden, 2) || !buffer_ok(weight, a.copy_weight ? 2 : 16) ||
                        !buffer_ok(targets, itype_bytes(a.itype)) || !buffer_ok(lse, 4) || !buffer_ok(dhidden, 2)))
     return TBE_ERR_INVALID_ARG;
   DeviceInfo dev;
