@@ -239,7 +239,7 @@ struct GradJob {
 constexpr int kStageRow = 34;  // elements from one row to the next of rows that begin anywhere: 17 words, no bank twice
 
 // A gradient's rows: the product times alpha, rounded.
-template <typename T, int BN>
+template <typename T>
 struct OutJob {
   struct Args {
     const float* meta;     // {.., alpha}
@@ -247,7 +247,7 @@ struct OutJob {
     int64_t stride, first, rows;   // first row of the product in `out`, rows of out
     const int* place;      // NULL, or the row of out for each row of the product, of which there are *live
     const int* live;
-    int cols;
+    int cols, width;       // width: of a tile
     int vec;               // rows allow 16-byte stores
   };
   struct Row {
@@ -268,9 +268,10 @@ struct OutJob {
   template <typename R>
   static __device__ __forceinline__ void tile(const Args& a, const Row& r, State&, const PairItem& it, int row, int half, uint32_t tmem,
                                               uint32_t staging, R&& release) {
-    const int col0 = it.n * BN + half * (BN / 2), lane = lane_id();
-    each_columns<BN / 2>(tmem, release, [&](int j, pair::Columns& c) {
-      const int left = a.cols - col0 - j * 32;   // columns from this block's first on; the same for the whole warp
+    const int col0 = it.n * a.width + half * 128, lane = lane_id();
+    const int here = min(a.cols - col0, a.width - half * 128);   // columns of this half; the same for the whole warp
+    each_columns<128>(tmem, release, [&](int j, pair::Columns& c) {
+      const int left = here - j * 32;
       if (left <= 0) return;
       Pack<T, 16> p[2];
 #pragma unroll
@@ -284,7 +285,7 @@ struct OutJob {
         stage_half<T>(staging, lane, j & 1, p);
         if ((j & 1) || left <= 32) {
           T* dst = a.out + col0 + j / 2 * 64;
-          const int cols = a.cols - col0 - j / 2 * 64;
+          const int cols = here - j / 2 * 64;
           unstage(staging, lane, [&](int x, int c, const uint4& piece) {
             const int to = __shfl_sync(kFull, r.out, x);
             if (to < 0 || c * 8 >= cols) return;
@@ -316,12 +317,11 @@ struct OutJob {
 
 // Sums in fp32, [split][tokens][stride]: stored by the first piece, added to by the others (each by one thread, so that the order is
 // the pieces').
-template <int BN>
 struct SumJob {
   struct Args {
     float* sums;
     int64_t stride;        // a multiple of 8
-    int tokens, add;
+    int tokens, add, width;
   };
   using Row = NoRow;
   using State = NoState;
@@ -329,9 +329,10 @@ struct SumJob {
   static __device__ __forceinline__ void tile(const Args& a, const Row&, State&, const PairItem& it, int row, int half, uint32_t tmem, uint32_t,
                                               R&& release) {
     const int i = it.m * kPairM + row;
-    const int col0 = it.n * BN + half * (BN / 2);
+    const int col0 = it.n * a.width + half * 128;
     float* dst = a.sums + (static_cast<int64_t>(it.split) * a.tokens + i) * a.stride + col0;
-    each_columns<BN / 2>(tmem, release, [&](int j, pair::Columns& c) {
+    each_columns<128>(tmem, release, [&](int j, pair::Columns& c) {
+      if (half * 128 + j * 32 >= a.width) return;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (i >= a.tokens || col0 + j * 32 + q * 8 >= a.stride) continue;
@@ -678,11 +679,11 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant_
 // ------------------------------------------------------------------------------------------
 // Host
 // ------------------------------------------------------------------------------------------
-template <int BN, int AM, class P0, class P1>
+template <int AM, class P0, class P1>
 tbe_status launch_pair(const typename P0::Args& p0, const typename P1::Args& p1, int64_t items, const LossArgs& a, const DeviceInfo& dev,
                        cudaStream_t s) {
-  auto* kernel = pair_mma_kernel<BN, AM, P0, P1>;
-  constexpr size_t smem = PairTile<BN, AM>::kSmem;
+  auto* kernel = pair_mma_kernel<AM, P0, P1>;
+  constexpr size_t smem = PairTile<AM>::kSmem;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem(kernel, smem, allowed);
   if (e != cudaSuccess) return cuda_status(e);
@@ -690,9 +691,9 @@ tbe_status launch_pair(const typename P0::Args& p0, const typename P1::Args& p1,
   return cuda_status(launch_after(kernel, static_cast<unsigned>(2 * pairs), kPairThreads, smem, s, p0, p1, a.stats));
 }
 
-template <int BN, int AM, class P>
+template <int AM, class P>
 tbe_status launch_product(const typename P::Args& p, const LossArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  return launch_pair<BN, AM, P, NoProduct>(p, NoProduct::Args{}, p.g.items(), a, dev, s);
+  return launch_pair<AM, P, NoProduct>(p, NoProduct::Args{}, p.g.items(), a, dev, s);
 }
 
 tbe_status launch_copy(const CopyArgs& p, const DeviceInfo& dev, cudaStream_t s) {
@@ -741,51 +742,51 @@ constexpr int kFewTokens = 32;
 // Blocks of k up to which one pair makes a whole tile of dhidden, with no sums to join after it.
 constexpr int kDirectBlocks = 24;
 
-// Columns of a tile of the gradients' products: 128 where tiles of 256 would be a fifth or more emptier (301 columns: 188 us a call
-// with 128, 198 with 256; a block of k of a tile of 128 takes nearly as long, 310 against 335 ns, but the clock holds up).
-int gradient_bn(int dim) { return round_up(dim, 128) * 5 <= round_up(dim, 256) * 4 ? 128 : 256; }
+// Columns of a tile of the gradients' products: as many tiles as 256 columns each would be, no wider than the rows need.
+int gradient_width(int dim) { return static_cast<int>(round_up(ceil_div(dim, ceil_div(dim, 256)), 32)); }
 
-template <typename T, int BN>
+template <typename T>
 tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, void* dhidden, void* dweight, char* ws,
                          const DeviceInfo& dev, cudaStream_t s) {
   const bool bf16 = a.dtype == TBE_BF16;
   const int N = static_cast<int>(a.tokens), m_tiles = static_cast<int>(ceil_div(N, kPairM));
-  const int d_tiles = static_cast<int>(ceil_div(a.dim, BN)), d_blocks = static_cast<int>(ceil_div(a.dim, kPairK));
+  const int width = gradient_width(a.dim);
+  const int d_tiles = static_cast<int>(ceil_div(a.dim, width)), d_blocks = static_cast<int>(ceil_div(a.dim, kPairK));
   float* meta = reinterpret_cast<float*>(ws + l.meta);
   const int* live = reinterpret_cast<const int*>(ws + l.live);
   const int* placed = reinterpret_cast<const int*>(ws + l.place);
   T* dz = reinterpret_cast<T*>(ws + l.dz);
   float* sums = reinterpret_cast<float*>(ws + l.sums);
   using Grad = Product<false, false, GradJob<T>>;
-  using Sum = Product<false, true, SumJob<BN>>;
-  using Direct = Product<false, true, OutJob<T, BN>>;
-  using Out = Product<true, true, OutJob<T, BN>>;
+  using Sum = Product<false, true, SumJob>;
+  using Direct = Product<false, true, OutJob<T>>;
+  using Out = Product<true, true, OutJob<T>>;
   tbe_status st;
   for (int64_t first = 0; first < a.rows; first += l.piece) {
     const int here = static_cast<int>(a.rows - first < l.piece ? a.rows - first : l.piece);
     const int v_tiles = static_cast<int>(ceil_div(here, 256)), f = static_cast<int>(first);
     typename Grad::Args ga{maps[0], maps[1],
-                           PairShape{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 0, pair_idesc(bf16, 256, false, false), live, nullptr, 0},
+                           PairShape{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 256, 0, pair_idesc(bf16, 256, false, false), live, nullptr, 0},
                            {meta, live, reinterpret_cast<const float*>(ws + l.coef), reinterpret_cast<const float*>(ws + l.lse2),
                             reinterpret_cast<const int*>(ws + l.target), dz, l.dz_rows, f, here, a.scale * kLog2e}};
-    if ((st = launch_product<256, 128, Grad>(ga, a, dev, s)) != TBE_OK) return st;
+    if ((st = launch_product<128, Grad>(ga, a, dev, s)) != TBE_OK) return st;
     // dhidden += dz [tokens, piece] by weight [piece, dim];  dweight = dz^T [piece, tokens] by hidden [tokens, dim]
-    const PairShape sum{m_tiles, d_tiles, l.splits, static_cast<int>(ceil_div(here, kPairK)), 0, 0, 0, f, 0, pair_idesc(bf16, BN, false, true),
+    const PairShape sum{m_tiles, d_tiles, l.splits, static_cast<int>(ceil_div(here, kPairK)), 0, 0, 0, f, width, 0, pair_idesc(bf16, width, false, true),
                         live, nullptr, static_cast<int>(l.dz_rows)};
     typename Out::Args oa{maps[4], maps[5],
-                          PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, 1, pair_idesc(bf16, BN, true, true),
+                          PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, width, 1, pair_idesc(bf16, width, true, true),
                                     nullptr, live, static_cast<int>(l.dz_rows)},
-                          {meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, nullptr, nullptr, a.dim,
+                          {meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, nullptr, nullptr, a.dim, width,
                            whole_stores(dweight, a.dweight_stride)}};
     const int64_t items = static_cast<int64_t>(sum.items()) + oa.g.items();
     if (l.direct) {
       typename Direct::Args da{maps[2], maps[3], sum,
-                               {meta, static_cast<T*>(dhidden), a.dhidden_stride, 0, a.tokens, placed, live, a.dim,
+                               {meta, static_cast<T*>(dhidden), a.dhidden_stride, 0, a.tokens, placed, live, a.dim, width,
                                 whole_stores(dhidden, a.dhidden_stride)}};
-      st = launch_pair<BN, 128, Direct, Out>(da, oa, items, a, dev, s);
+      st = launch_pair<128, Direct, Out>(da, oa, items, a, dev, s);
     } else {
-      typename Sum::Args sa{maps[2], maps[3], sum, {sums, l.dim_pad, N, first > 0}};
-      st = launch_pair<BN, 128, Sum, Out>(sa, oa, items, a, dev, s);
+      typename Sum::Args sa{maps[2], maps[3], sum, {sums, l.dim_pad, N, first > 0, width}};
+      st = launch_pair<128, Sum, Out>(sa, oa, items, a, dev, s);
     }
     if (st != TBE_OK) return st;
   }
@@ -795,13 +796,6 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
   int64_t blocks = ceil_div(a.tokens * (l.dim_pad / 8), 256);
   if (blocks > dev.sms * 8) blocks = dev.sms * 8;
   return cuda_status(launch_after(loss_finish_kernel<T>, static_cast<unsigned>(blocks), 256, 0, s, fa));
-}
-
-template <typename T>
-tbe_status loss_backward_t(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, void* dhidden, void* dweight, char* ws,
-                           const DeviceInfo& dev, cudaStream_t s) {
-  if (gradient_bn(a.dim) == 128) return loss_backward<T, 128>(a, l, maps, dhidden, dweight, ws, dev, s);
-  return loss_backward<T, 256>(a, l, maps, dhidden, dweight, ws, dev, s);
 }
 
 }  // namespace
@@ -846,7 +840,7 @@ LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev
   if (most > (1 << 30)) most = 1 << 30;
   const int64_t pieces = ceil_div(a.rows, most);
   l.piece = round_up(ceil_div(a.rows, pieces), 256);
-  const int64_t d_tiles = ceil_div(a.dim, gradient_bn(a.dim)), blocks = ceil_div(l.piece, kPairK);
+  const int64_t d_tiles = ceil_div(a.dim, gradient_width(a.dim)), blocks = ceil_div(l.piece, kPairK);
   const int64_t tiles = ceil_div(a.tokens, kPairM) * d_tiles, pairs = dev.sms / 2;
   l.direct = a.rows <= l.piece && ceil_div(a.rows, kPairK) <= kDirectBlocks;
   l.splits = 1;
@@ -921,11 +915,11 @@ tbe_status launch_loss_forward(const LossArgs& a, const LossForwardLayout& l, co
   const int m_tiles = static_cast<int>(ceil_div(a.tokens, kPairM)), v_tiles = l.parts / 2, pairs = dev.sms / 2;
   const bool carry = m_tiles == 1 && v_tiles > pairs;
   const Stats::Args sa{ma, mb,
-                       PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, 0, pair_idesc(bf16, 256, false, false),
+                       PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, 256, 0, pair_idesc(bf16, 256, false, false),
                                  select ? live : nullptr, nullptr, 0},
                        {targets, select ? selected : nullptr, live, part, target_logit, ticket, l.parts_rows, a.rows, static_cast<int>(a.tokens), a.itype,
                         carry, a.scale, a.scale * kLog2e}};
-  st = few ? launch_product<256, kFewTokens, Stats>(sa, a, dev, s) : launch_product<256, 128, Stats>(sa, a, dev, s);
+  st = few ? launch_product<kFewTokens, Stats>(sa, a, dev, s) : launch_product<128, Stats>(sa, a, dev, s);
   if (st != TBE_OK) return st;
   const JoinArgs ja{part, target_logit, targets, select ? row : nullptr, loss, lse, mean, reinterpret_cast<BlockSum*>(ws + l.ticket + 256), ticket,
                     a.tokens, a.rows, l.parts_rows, carry ? 2 * pairs : l.parts, a.itype, a.stats};
@@ -963,8 +957,8 @@ tbe_status launch_loss_backward(const LossArgs& a, const LossBackwardLayout& l, 
       !encode_operand(&maps[2], dz, bf16, 64, l.piece / 64 * l.dz_rows, 64, 128) || !encode_operand(&maps[3], weight, bf16, a.dim, a.rows, wst, 64) ||
       !encode_operand(&maps[4], dz, bf16, 64, l.piece / 64 * l.dz_rows, 64, 64) || !encode_operand(&maps[5], h, bf16, a.dim, a.tokens, l.dim_pad, 64))
     return cuda_status(cudaErrorInvalidValue);
-  if (bf16) return loss_backward_t<__nv_bfloat16>(a, l, maps, dhidden, dweight, ws, dev, s);
-  return loss_backward_t<__half>(a, l, maps, dhidden, dweight, ws, dev, s);
+  if (bf16) return loss_backward<__nv_bfloat16>(a, l, maps, dhidden, dweight, ws, dev, s);
+  return loss_backward<__half>(a, l, maps, dhidden, dweight, ws, dev, s);
 }
 
 }  // namespace tbe

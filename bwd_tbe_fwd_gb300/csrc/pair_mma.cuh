@@ -1,9 +1,9 @@
-// pair_mma.cuh -- matrix products on the fifth-generation tensor cores by pairs of CTAs: C tile of 256 x BN =
-// sum over k of A[256][k] B[BN][k], 16-bit operands, fp32 accumulators, with an epilogue of the caller's.
+// pair_mma.cuh -- matrix products on the fifth-generation tensor cores by pairs of CTAs: C tile of 256 x 256 =
+// sum over k of A[256][k] B[256][k], 16-bit operands, fp32 accumulators, with an epilogue of the caller's.
 //
 // The two CTAs of a cluster sit on neighbouring SMs and work on one tile (tcgen05.mma.cta_group::2): each brings its
-// 128 rows of A and its half of B's rows into its shared memory, so a CTA copies BN / 2 rows of B where it would copy
-// BN alone: 64 bytes a clock at the full rate of a 256 x 256 tile, about what an SM can draw from L2.  Eleven
+// 128 rows of A and its half of B's rows into its shared memory, so a CTA copies 128 rows of B where it would copy
+// 256 alone: 64 bytes a clock at the full rate of a 256 x 256 tile, about what an SM can draw from L2.  Eleven
 // warps: eight for the epilogue (warp w reads TMEM lanes 32 (w % 4) .. + 31 and half w / 4 of the columns), two threads that
 // issue the TMA copies of a ring of stages of 64 k's, A's and B's, one (in the even CTA) that issues the products.  The
 // accumulator takes all 512 columns of TMEM as two buffers, so that the products of the next tile run while the epilogue
@@ -30,12 +30,12 @@ constexpr int kStagingBytes = 4096;    // of a warp of the epilogue: 32 rows of 
 
 // AM: rows of A that a CTA copies.  With fewer than 128 (products of few rows, bound by B's way through memory) the products
 // read what lies behind them as the others, whose results nobody looks at, and the ring has more stages.
-template <int BN, int AM = 128>
+template <int AM = 128>
 struct PairTile {
   static constexpr int kA = AM * kPairK * 2;             // bytes of a CTA's part of a stage
-  static constexpr int kB = BN / 2 * kPairK * 2;
+  static constexpr int kB = 128 * kPairK * 2;
   static constexpr int kStage = kA + kB;
-  static constexpr int kStages = 196608 / kStage;        // 6 of 32 KB, 8 of 24 KB, 9 of 20 KB
+  static constexpr int kStages = 196608 / kStage;        // 6 of 32 KB, 9 of 20 KB
   static_assert(kStage >= 128 * kPairK * 2, "the products read 128 rows of A from a stage's start");
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kStagingBytes + 1024;  // and room to align to the swizzle's 1024 bytes
 };
@@ -45,6 +45,7 @@ struct PairTile {
 struct PairShape {
   int m_tiles, n_tiles, splits, k_blocks;   // k_blocks: of all splits together; splits <= k_blocks
   int a_m0, a_k0, b_n0, b_k0;
+  int width;        // columns of a tile: a multiple of 32 up to 256 (256 where B is K-major)
   int n_first;      // tiles go along n first, else along m; splits come last
   uint32_t idesc;
   const int* live_m;
@@ -86,10 +87,10 @@ struct PairPlan {
 };
 
 // kind::f16 instruction descriptor: fp32 accumulator, 16-bit operands, M = 256.
-inline uint32_t pair_idesc(bool bf16, int bn, bool a_mn, bool b_mn) {
+inline uint32_t pair_idesc(bool bf16, int width, bool a_mn, bool b_mn) {
   const uint32_t t = bf16 ? 1 : 0;
   return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-         (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(kPairM >> 4) << 24);
+         (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kPairM >> 4) << 24);
 }
 
 namespace pair {
@@ -203,7 +204,7 @@ struct PairWalk {
 //   struct Args;  struct Row: what a thread needs of its row of a tile, Row::load(args, item, row) fetches it ahead;
 //   struct State: what a thread carries from tile to tile;
 //   tile(args, row_data, state, item, row, half, tmem, staging, release): row = this thread's row of the tile (0 .. 255), half =
-//     which half of the columns, tmem = the address of its first column; release() once the columns are in registers;
+//     which 128 of the columns, tmem = the address of its first column; release() once the columns are in registers;
 //   finish(args, state, pair, row, half) after the last tile.  All 32 lanes of a warp call these together.
 template <bool A_MN, bool B_MN, class J>
 struct Product {
@@ -230,13 +231,16 @@ struct PairRole {
 };
 
 // One of the two threads that issue copies: A's or B's.  A's also tells the barrier how many bytes a stage has.
-template <int BN, int AM, class P, bool A>
+template <int AM, class P, bool A>
 __device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairShape& g, PairWalk walk, PairRole& r) {
-  using T = PairTile<BN, AM>;
+  using T = PairTile<AM>;
   const uint32_t leader = pair::in_leader(smem_u32(r.full));
+  // B with k across the rows comes in blocks of 64 columns, of which a narrow tile needs one
+  const int blocks = A ? 2 : P::kBMN && g.width <= 128 ? 1 : 2;
+  const uint32_t bytes = 2 * (T::kStage - (P::kBMN && g.width <= 128 ? T::kB / 2 : 0));
   PairItem i;
   while (!r.failed && walk.next(g, i)) {
-    const int x = A ? g.a_m0 + i.m * kPairM + static_cast<int>(r.rank) * 128 : g.b_n0 + i.n * BN + static_cast<int>(r.rank) * (BN / 2);
+    const int x = A ? g.a_m0 + i.m * kPairM + static_cast<int>(r.rank) * 128 : g.b_n0 + i.n * g.width + static_cast<int>(r.rank) * (g.width / 2);
     const int last = i.last(g);
     for (int kb = i.first(g); kb < last; ++kb, ++r.it) {
       const uint32_t st = r.it % T::kStages;
@@ -244,13 +248,12 @@ __device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairS
         r.failed = true;
         return;
       }
-      if (A && r.rank == 0) mbar_arrive_expect_tx(&r.full[st], 2 * T::kStage);
+      if (A && r.rank == 0) mbar_arrive_expect_tx(&r.full[st], bytes);
       const uint32_t bar = leader + st * 8, to = r.ring + st * T::kStage + (A ? 0 : T::kA);
       const int k = (A ? g.a_k0 : g.b_k0) + kb * kPairK;
       const CUtensorMap* map = A ? &p.a : &p.b;
       if constexpr (A ? P::kAMN : P::kBMN) {
-#pragma unroll
-        for (int c = 0; c < (A ? 2 : BN / 128); ++c) {
+        for (int c = 0; c < blocks; ++c) {
           if (A && g.a_rows > 0) pair::tma_2d(to + c * 8192, map, 0, (x / 64 + c) * g.a_rows + k, bar);
           else pair::tma_2d(to + c * 8192, map, x + c * 64, k, bar);
         }
@@ -262,9 +265,9 @@ __device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairS
   }
 }
 
-template <int BN, int AM, class P>
+template <int AM, class P>
 __device__ __forceinline__ void pair_multiply(const PairShape& g, PairWalk walk, PairRole& r) {
-  using T = PairTile<BN, AM>;
+  using T = PairTile<AM>;
   PairItem i;
   for (; !r.failed && walk.next(g, i); ++r.tile) {
     const uint32_t buf = r.tile & 1, d = r.tmem + buf * 256;
@@ -291,7 +294,7 @@ __device__ __forceinline__ void pair_multiply(const PairShape& g, PairWalk walk,
   }
 }
 
-template <int BN, class P>
+template <class P>
 __device__ __forceinline__ void pair_epilogue(const typename P::Args& p, const PairShape& g, PairWalk walk, PairRole& r, int pair, int w,
                                               int lane, uint32_t staging) {
   using Job = typename P::Job;
@@ -310,7 +313,7 @@ __device__ __forceinline__ void pair_epilogue(const typename P::Args& p, const P
     if (r.failed) return;
     pair::fence_after();
     const uint32_t empty = pair::in_leader(smem_u32(&r.acc_empty[buf]));
-    Job::tile(p.job, now, state, i, row, half, r.tmem + buf * 256 + half * (BN / 2) + (static_cast<uint32_t>((w % 4) * 32) << 16), staging,
+    Job::tile(p.job, now, state, i, row, half, r.tmem + buf * 256 + half * 128 + (static_cast<uint32_t>((w % 4) * 32) << 16), staging,
               [&] {
                 pair::fence_before();
                 __syncwarp();
@@ -321,11 +324,11 @@ __device__ __forceinline__ void pair_epilogue(const typename P::Args& p, const P
   Job::finish(p.job, state, pair, row, half);
 }
 
-template <int BN, int AM, class P0, class P1>
+template <int AM, class P0, class P1>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_mma_kernel(const __grid_constant__ typename P0::Args p0, const __grid_constant__ typename P1::Args p1,
                     unsigned long long* stats) {
-  using T = PairTile<BN, AM>;
+  using T = PairTile<AM>;
   static_assert(AM == 128 || !P0::kAMN, "fewer rows of A in K-major order only");
   constexpr int ST = T::kStages;
   extern __shared__ uint8_t s_raw[];
@@ -373,14 +376,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (w == kEpiWarps) {
     if (lane == 0) {
-      pair_copy<BN, AM, P0, false>(p0, g0, walk0, r);
-      if constexpr (!P1::kNone) pair_copy<BN, AM, P1, false>(p1, g1, walk1, r);
+      pair_copy<AM, P0, false>(p0, g0, walk0, r);
+      if constexpr (!P1::kNone) pair_copy<AM, P1, false>(p1, g1, walk1, r);
     }
     __syncwarp();
   } else if (w == kEpiWarps + 2) {
     if (lane == 0) {
-      pair_copy<BN, AM, P0, true>(p0, g0, walk0, r);
-      if constexpr (!P1::kNone) pair_copy<BN, AM, P1, true>(p1, g1, walk1, r);
+      pair_copy<AM, P0, true>(p0, g0, walk0, r);
+      if constexpr (!P1::kNone) pair_copy<AM, P1, true>(p1, g1, walk1, r);
       // Copies must not be in flight when a CTA ends: in the even CTA, whose barriers count both CTAs' copies, the last
       // round of every stage has landed (its products are done by then, unless a wait gave up).
       if (r.rank == 0)
@@ -390,15 +393,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else if (w == kEpiWarps + 1) {
     if (r.rank == 0 && lane == 0) {
-      pair_multiply<BN, AM, P0>(g0, walk0, r);
-      if constexpr (!P1::kNone) pair_multiply<BN, AM, P1>(g1, walk1, r);
+      pair_multiply<AM, P0>(g0, walk0, r);
+      if constexpr (!P1::kNone) pair_multiply<AM, P1>(g1, walk1, r);
     }
     __syncwarp();
   } else {
     const uint32_t staging = ring + ST * T::kStage + w * kStagingBytes;
-    pair_epilogue<BN, P0>(p0, g0, walk0, r, pair_id, w, lane, staging);
+    pair_epilogue<P0>(p0, g0, walk0, r, pair_id, w, lane, staging);
     if constexpr (!P1::kNone)
-      if (!r.failed) pair_epilogue<BN, P1>(p1, g1, walk1, r, pair_id, w, lane, staging);
+      if (!r.failed) pair_epilogue<P1>(p1, g1, walk1, r, pair_id, w, lane, staging);
   }
   if (r.failed && lane == 0) stat_add(stats, TBE_STAT_WAIT_TIMEOUT, 1);
   __syncwarp();
