@@ -472,11 +472,20 @@ __global__ void __launch_bounds__(kSumThreads) lookup_join_kernel(const __grid_c
   const int slab = static_cast<int>(blockIdx.x - chunk * a.slabs), lane = lane_id(), w = threadIdx.x / kWarp;
   constexpr int kChunk = kSumWarps * T;
   wait_before();
-  const int64_t p0 = chunk * kChunk, p1 = p0 + kChunk;
+  const int64_t p0 = chunk * kChunk, p1 = p0 + kChunk, p2 = p1 + kChunk;
   if (p1 >= a.tokens) return;
-  const uint32_t run = a.keys[p1 - 1];
-  if (run >= a.rows || a.keys[p1] != run || (p0 > 0 && a.keys[p0 - 1] == run)) return;
-  int64_t lo = chunk + 1, hi = a.chunks;   // the last chunk that begins with the run, 32 places looked at at once
+  const uint32_t none = static_cast<uint32_t>(a.rows);   // loaded at once, not as each is asked for
+  const uint32_t run = a.keys[p1 - 1], next = a.keys[p1], before = p0 > 0 ? a.keys[p0 - 1] : none, later = p2 < a.tokens ? a.keys[p2] : none;
+  if (run == none || next != run || before == run) return;
+  const int col = (slab * kWarp + lane) * V;
+  float begun[V];
+  Pack<TT, V> old;
+  if (w == 0) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) begun[k] = a.partial[(chunk * 2 + 1) * a.dim_pad + col + k];
+    old = old_row<ACC, TT, V>(a, run, col, true);
+  }
+  int64_t lo = chunk + 1, hi = later == run ? a.chunks : lo + 1;   // the last chunk that begins with the run, 32 places looked at at once
   while (hi - lo > 1) {
     const int64_t step = (hi - lo + kWarp - 1) / kWarp, at = lo + lane * step;
     const int hits = __popc(__ballot_sync(kFull, at < hi && a.keys[at * kChunk] == run));
@@ -484,7 +493,6 @@ __global__ void __launch_bounds__(kSumThreads) lookup_join_kernel(const __grid_c
     hi = min(hi, lo + step);
   }
   const int64_t count = lo - chunk, end = chunk + 1 + count * (w + 1) / kSumWarps;
-  const int col = (slab * kWarp + lane) * V;
   float sum[V] = {};
 #pragma unroll 4
   for (int64_t c = chunk + 1 + count * w / kSumWarps; c < end; ++c) {
@@ -496,9 +504,8 @@ __global__ void __launch_bounds__(kSumThreads) lookup_join_kernel(const __grid_c
   for (int k = 0; k < V; ++k) s_sum[w][k * kWarp + lane] = sum[k];
   __syncthreads();
   if (w != 0) return;
-  const Pack<TT, V> old = old_row<ACC, TT, V>(a, run, col, true);
 #pragma unroll
-  for (int k = 0; k < V; ++k) sum[k] = a.partial[(chunk * 2 + 1) * a.dim_pad + col + k];
+  for (int k = 0; k < V; ++k) sum[k] = begun[k];
   for (int q = 0; q < kSumWarps; ++q)
 #pragma unroll
     for (int k = 0; k < V; ++k) sum[k] += s_sum[q][k * kWarp + lane];
