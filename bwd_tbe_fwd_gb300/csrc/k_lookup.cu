@@ -182,6 +182,31 @@ __device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s_wsum) {
   return x - v + (w > 0 ? y : 0);
 }
 
+// So few tokens that a thread to each counts those that come before it (32 tokens: 7.5 us by digits, 3.9 so).
+constexpr int kRankTokens = 256;
+__device__ __forceinline__ void rank_few(const KeyArgs& a, uint32_t* s_key) {
+  const int t = threadIdx.x, n = static_cast<int>(a.tokens);
+  uint32_t key = 0xffffffffu;
+  if (t < kRankTokens) {
+    if (t < n) {
+      const int64_t id = load_id(a.ids, a.itype, t);
+      key = sort_key(id, a.rows);
+      stat_add(a.stats, TBE_STAT_UNREPAIRED, id >= a.rows);
+    }
+    s_key[t] = key;
+  }
+  __syncthreads();
+  if (t >= n) return;
+  uint32_t at = 0;
+  for (int j = 0; j < n; j += 4) {
+    const uint4 k = *reinterpret_cast<const uint4*>(s_key + j);
+    at += (k.x < key || (k.x == key && j < t)) + (k.y < key || (k.y == key && j + 1 < t)) + (k.z < key || (k.z == key && j + 2 < t)) +
+          (k.w < key || (k.w == key && j + 3 < t));
+  }
+  a.keys[at] = key;
+  a.vals[at] = static_cast<uint32_t>(t);
+}
+
 // Stable radix sort of (id, token) by one cluster, up to 65536 of them: the items stay in its shared memory, each CTA
 // holding a contiguous 1024 IPT of the current order.  A pass ranks a CTA's items by ballots and counters of its
 // warps' own, joins the CTAs' digit counts through distributed shared memory, and sends each item to its place in whichever CTA
@@ -202,6 +227,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) lookup_sort_kernel(const _
     } else {
       for (int64_t r = t / kWarp; r < a.rows; r += n / kWarp) zero_range(p + r * a.pitch, a.row_bytes, a.elem, t % kWarp, kWarp);
     }
+    return;
+  }
+  if (IPT == 1 && a.k.tokens <= kRankTokens) {
+    rank_few(a.k, reinterpret_cast<uint32_t*>(s_raw));
     return;
   }
   constexpr int kPer = kClusterThreads * IPT;
