@@ -219,7 +219,7 @@ def test_a_row_that_is_not_finite_spoils_its_own_loss_alone():
 
 @pytest.mark.parametrize("size", [0.0, 1e-30, 1e-12, 1e12, 1e30])
 def test_upstream_gradients_of_any_size(size):
-    """dz is scaled by a power of two that the largest coefficient gives: bf16's gradients keep their accuracy at any size."""
+    """dz is scaled by a factor that the largest coefficient gives: bf16's gradients keep their accuracy at any size."""
     h, w, t, t_h = loss_inputs(100, 200, 64, "bf16", seed=10)
     op = SoftmaxLoss(200, 64, 100)
     lse = op.forward(h, w, t)[1]
