@@ -98,7 +98,8 @@ struct StatsJob {
     uint32_t* ticket;      // set to 0 for the kernel that joins the parts
     int64_t parts_rows, rows;
     int tokens, itype;
-    int carry;             // one tile of rows: a thread's parts are joined from tile to tile, one for each pair
+    int carry;             // one tile of rows: a thread's parts are joined from tile to tile, one for each pair (or single CTA)
+    int width;             // columns of a tile
     float scale, scale2;   // scale2 = scale * log2(e)
   };
   struct Row {
@@ -120,10 +121,11 @@ struct StatsJob {
   static __device__ __forceinline__ void tile(const Args& a, const Row& r, State& s, const PairItem& it, int row, int half, uint32_t tmem,
                                               uint32_t, R&& release) {
     const int i = it.m * kPairM + row;
-    const int64_t col0 = static_cast<int64_t>(it.n) * 256 + half * 128;
+    const int64_t col0 = static_cast<int64_t>(it.n) * a.width + half * 128;
     if (it.m == 0 && it.n == 0 && row == 0 && half == 0) *a.ticket = 0;
-    const int64_t tl = r.target < 0 ? -1 : r.target - col0;  // the target's column of this half
-    const int live = static_cast<int>(a.rows - col0 < 128 ? a.rows - col0 : 128);  // may be negative
+    const int most = min(128, a.width - half * 128);         // columns of this half, which may have none
+    const int live = static_cast<int>(a.rows - col0 < most ? a.rows - col0 : most);
+    const int64_t tl = r.target < 0 || r.target - col0 >= live ? -1 : r.target - col0;  // the target's column of this half
     float top = s.top, sum = s.sum;
     each_columns<128>(tmem, release, [&](int j, pair::Columns& c) {
       if (live < j * 32 + 32) {
@@ -681,21 +683,21 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant_
 // ------------------------------------------------------------------------------------------
 // Host
 // ------------------------------------------------------------------------------------------
-template <int AM, class P0, class P1>
+template <int AM, int CTAS, class P0, class P1>
 tbe_status launch_pair(const typename P0::Args& p0, const typename P1::Args& p1, int64_t items, const LossArgs& a, const DeviceInfo& dev,
                        cudaStream_t s) {
-  auto* kernel = pair_mma_kernel<AM, P0, P1>;
-  constexpr size_t smem = PairTile<AM>::kSmem;
+  auto* kernel = pair_mma_kernel<AM, CTAS, P0, P1>;
+  constexpr size_t smem = PairTile<AM, CTAS>::kSmem;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem(kernel, smem, allowed);
   if (e != cudaSuccess) return cuda_status(e);
-  const int64_t pairs = items < dev.sms / 2 ? items : dev.sms / 2;
-  return cuda_status(launch_after(kernel, static_cast<unsigned>(2 * pairs), kPairThreads, smem, s, p0, p1, a.stats));
+  const int64_t pairs = items < dev.sms / CTAS ? items : dev.sms / CTAS;
+  return cuda_status(launch_after(kernel, static_cast<unsigned>(CTAS * pairs), kPairThreads, smem, s, p0, p1, a.stats));
 }
 
-template <int AM, class P>
+template <int AM, int CTAS, class P>
 tbe_status launch_product(const typename P::Args& p, const LossArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  return launch_pair<AM, P, NoProduct>(p, NoProduct::Args{}, p.g.items(), a, dev, s);
+  return launch_pair<AM, CTAS, P, NoProduct>(p, NoProduct::Args{}, p.g.items(), a, dev, s);
 }
 
 tbe_status launch_copy(const CopyArgs& p, const DeviceInfo& dev, cudaStream_t s) {
@@ -744,6 +746,18 @@ constexpr int kFewTokens = 32;
 // Blocks of k up to which one pair makes a whole tile of dhidden, with no sums to join after it.
 constexpr int kDirectBlocks = 24;
 
+// Columns of a tile of few tokens' logits, which take as long as their rows of the table take through memory: the width with which
+// the CTA with the most tiles has the fewest rows (131072 rows to 152 CTAs: 4 tiles of 224 each and not 4 of 256).
+int even_width(int64_t rows, int workers) {
+  int best = 256;
+  int64_t least = INT64_MAX;
+  for (int width = 256; width >= 128; width -= 32) {
+    const int64_t most = ceil_div(ceil_div(rows, width), workers) * width;
+    if (most < least) least = most, best = width;
+  }
+  return best;
+}
+
 // Columns of a tile of the gradients' products: as many tiles as 256 columns each would be, no wider than the rows need.
 int gradient_width(int dim) { return static_cast<int>(round_up(ceil_div(dim, ceil_div(dim, 256)), 32)); }
 
@@ -771,7 +785,7 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
                            PairShape{m_tiles, v_tiles, 1, d_blocks, 0, 0, f, 0, 256, 0, pair_idesc(bf16, 256, false, false), live, nullptr, 0},
                            {meta, live, reinterpret_cast<const float*>(ws + l.coef), reinterpret_cast<const float*>(ws + l.lse2),
                             reinterpret_cast<const int*>(ws + l.target), dz, l.dz_rows, f, here, a.scale * kLog2e}};
-    if ((st = launch_product<128, Grad>(ga, a, dev, s)) != TBE_OK) return st;
+    if ((st = launch_product<128, 2, Grad>(ga, a, dev, s)) != TBE_OK) return st;
     // dhidden += dz [tokens, piece] by weight [piece, dim];  dweight = dz^T [piece, tokens] by hidden [tokens, dim]
     const PairShape sum{m_tiles, d_tiles, l.splits, static_cast<int>(ceil_div(here, kPairK)), 0, 0, 0, f, width, 0, pair_idesc(bf16, width, false, true),
                         live, nullptr, static_cast<int>(l.dz_rows)};
@@ -785,10 +799,10 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
       typename Direct::Args da{maps[2], maps[3], sum,
                                {meta, static_cast<T*>(dhidden), a.dhidden_stride, 0, a.tokens, placed, live, a.dim, width,
                                 whole_stores(dhidden, a.dhidden_stride)}};
-      st = launch_pair<128, Direct, Out>(da, oa, items, a, dev, s);
+      st = launch_pair<128, 2, Direct, Out>(da, oa, items, a, dev, s);
     } else {
       typename Sum::Args sa{maps[2], maps[3], sum, {sums, l.dim_pad, N, first > 0, width}};
-      st = launch_pair<128, Sum, Out>(sa, oa, items, a, dev, s);
+      st = launch_pair<128, 2, Sum, Out>(sa, oa, items, a, dev, s);
     }
     if (st != TBE_OK) return st;
   }
@@ -906,25 +920,28 @@ tbe_status launch_loss_forward(const LossArgs& a, const LossForwardLayout& l, co
     hidden = ws + l.hidden, hs = dim_pad;
     if (a.copy_weight) weight = ws + l.weight, wst = dim_pad;
   }
-  const bool few = a.tokens <= kFewTokens;
+  const bool few = a.tokens <= kFewTokens, solo = a.tokens <= 128;
+  const int m_tiles = static_cast<int>(ceil_div(a.tokens, kPairM)), workers = solo ? dev.sms : dev.sms / 2;
+  const bool carry = m_tiles == 1 && l.parts / 2 > workers;
+  const int width = carry && solo ? even_width(a.rows, workers) : 256, v_tiles = static_cast<int>(ceil_div(a.rows, width));
   CUtensorMap ma, mb;
-  if (!encode_operand(&ma, hidden, bf16, a.dim, a.tokens, hs, few ? kFewTokens : 128) || !encode_operand(&mb, weight, bf16, a.dim, a.rows, wst, 128))
+  if (!encode_operand(&ma, hidden, bf16, a.dim, a.tokens, hs, few ? kFewTokens : 128) || !encode_operand(&mb, weight, bf16, a.dim, a.rows, wst, solo ? width : 128))
     return cuda_status(cudaErrorInvalidValue);
   uint32_t* ticket = reinterpret_cast<uint32_t*>(ws + l.ticket);
   float2* part = reinterpret_cast<float2*>(ws + l.part);
   float* target_logit = reinterpret_cast<float*>(ws + l.logit);
   using Stats = Product<false, false, StatsJob>;
-  const int m_tiles = static_cast<int>(ceil_div(a.tokens, kPairM)), v_tiles = l.parts / 2, pairs = dev.sms / 2;
-  const bool carry = m_tiles == 1 && v_tiles > pairs;
   const Stats::Args sa{ma, mb,
-                       PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, 256, 0, pair_idesc(bf16, 256, false, false),
-                                 select ? live : nullptr, nullptr, 0},
+                       PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, width, 0,
+                                 pair_idesc(bf16, width, false, false, solo ? 1 : 2), select ? live : nullptr, nullptr, 0},
                        {targets, select ? selected : nullptr, live, part, target_logit, ticket, l.parts_rows, a.rows, static_cast<int>(a.tokens), a.itype,
-                        carry, a.scale, a.scale * kLog2e}};
-  st = few ? launch_product<kFewTokens, Stats>(sa, a, dev, s) : launch_product<128, Stats>(sa, a, dev, s);
+                        carry, width, a.scale, a.scale * kLog2e}};
+  st = few    ? launch_product<kFewTokens, 1, Stats>(sa, a, dev, s)
+       : solo ? launch_product<128, 1, Stats>(sa, a, dev, s)
+              : launch_product<128, 2, Stats>(sa, a, dev, s);
   if (st != TBE_OK) return st;
   const JoinArgs ja{part, target_logit, targets, select ? row : nullptr, loss, lse, mean, reinterpret_cast<BlockSum*>(ws + l.ticket + 256), ticket,
-                    a.tokens, a.rows, l.parts_rows, carry ? 2 * pairs : l.parts, a.itype, a.stats};
+                    a.tokens, a.rows, l.parts_rows, carry ? 2 * workers : l.parts, a.itype, a.stats};
   return cuda_status(launch_after(loss_join_kernel, static_cast<unsigned>(ceil_div(a.tokens, kWarp)), kJoinThreads, 0, s, ja));
 }
 

@@ -30,12 +30,15 @@ constexpr int kStagingBytes = 4096;    // of a warp of the epilogue: 32 rows of 
 
 // AM: rows of A that a CTA copies.  With fewer than 128 (products of few rows, bound by B's way through memory) the products
 // read what lies behind them as the others, whose results nobody looks at, and the ring has more stages.
-template <int AM = 128>
+// CTAS: 2, or 1 for products of up to 128 rows by single CTAs, each with all of a tile's B: a pair's product of 256 rows takes
+// both SMs as long as one with 128 takes one SM (16 x 131072 x 2048: 99 us by pairs,
+// 86 by single CTAs, 92% of the copy rate).
+template <int AM = 128, int CTAS = 2>
 struct PairTile {
   static constexpr int kA = AM * kPairK * 2;             // bytes of a CTA's part of a stage
-  static constexpr int kB = 128 * kPairK * 2;
+  static constexpr int kB = 256 / CTAS * kPairK * 2;
   static constexpr int kStage = kA + kB;
-  static constexpr int kStages = 196608 / kStage;        // 6 of 32 KB, 9 of 20 KB
+  static constexpr int kStages = 196608 / kStage;        // 6 of 32 KB; single CTAs: 5 of 36 KB, 4 of 48 KB
   static_assert(kStage >= 128 * kPairK * 2, "the products read 128 rows of A from a stage's start");
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kStagingBytes + 1024;  // and room to align to the swizzle's 1024 bytes
 };
@@ -45,7 +48,7 @@ struct PairTile {
 struct PairShape {
   int m_tiles, n_tiles, splits, k_blocks;   // k_blocks: of all splits together; splits <= k_blocks
   int a_m0, a_k0, b_n0, b_k0;
-  int width;        // columns of a tile: a multiple of 32 up to 256 (256 where B is K-major)
+  int width;        // columns of a tile: a multiple of 32 up to 256
   int n_first;      // tiles go along n first, else along m; splits come last
   uint32_t idesc;
   const int* live_m;
@@ -86,11 +89,11 @@ struct PairPlan {
   }
 };
 
-// kind::f16 instruction descriptor: fp32 accumulator, 16-bit operands, M = 256.
-inline uint32_t pair_idesc(bool bf16, int width, bool a_mn, bool b_mn) {
+// kind::f16 instruction descriptor: fp32 accumulator, 16-bit operands, M = 128 to a CTA.
+inline uint32_t pair_idesc(bool bf16, int width, bool a_mn, bool b_mn, int ctas = 2) {
   const uint32_t t = bf16 ? 1 : 0;
   return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-         (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kPairM >> 4) << 24);
+         (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(128 * ctas >> 4) << 24);
 }
 
 namespace pair {
@@ -102,7 +105,15 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) { return cluster_ad
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+template <int CTAS>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (CTAS == 1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+    return;
+  }
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
@@ -116,15 +127,29 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (lbo << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
          (uint64_t(2) << 61);
 }
+template <int CTAS>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  if constexpr (CTAS == 1) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+    return;
+  }
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
       : "memory");
 }
-// Arrives on the barrier at this place in both CTAs when the products issued so far are done.
-__device__ __forceinline__ void commit_both(uint64_t* bar) {
+// Arrives on the barrier at this place in each CTA when the products issued so far are done.
+template <int CTAS>
+__device__ __forceinline__ void commit_all(uint64_t* bar) {
+  if constexpr (CTAS == 1) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    return;
+  }
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
@@ -231,16 +256,16 @@ struct PairRole {
 };
 
 // One of the two threads that issue copies: A's or B's.  A's also tells the barrier how many bytes a stage has.
-template <int AM, class P, bool A>
+template <int AM, int CTAS, class P, bool A>
 __device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairShape& g, PairWalk walk, PairRole& r) {
-  using T = PairTile<AM>;
+  using T = PairTile<AM, CTAS>;
   const uint32_t leader = pair::in_leader(smem_u32(r.full));
   // B with k across the rows comes in blocks of 64 columns, of which a narrow tile needs one
   const int blocks = A ? 2 : P::kBMN && g.width <= 128 ? 1 : 2;
-  const uint32_t bytes = 2 * (T::kStage - (P::kBMN && g.width <= 128 ? T::kB / 2 : 0));
+  const uint32_t bytes = CTAS * (T::kA + (P::kBMN ? (g.width <= 128 ? T::kB / 2 : T::kB) : g.width / CTAS * kPairK * 2));
   PairItem i;
   while (!r.failed && walk.next(g, i)) {
-    const int x = A ? g.a_m0 + i.m * kPairM + static_cast<int>(r.rank) * 128 : g.b_n0 + i.n * g.width + static_cast<int>(r.rank) * (g.width / 2);
+    const int x = A ? g.a_m0 + i.m * kPairM + static_cast<int>(r.rank) * 128 : g.b_n0 + i.n * g.width + static_cast<int>(r.rank) * (g.width / CTAS);
     const int last = i.last(g);
     for (int kb = i.first(g); kb < last; ++kb, ++r.it) {
       const uint32_t st = r.it % T::kStages;
@@ -254,20 +279,20 @@ __device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairS
       const CUtensorMap* map = A ? &p.a : &p.b;
       if constexpr (A ? P::kAMN : P::kBMN) {
         for (int c = 0; c < blocks; ++c) {
-          if (A && g.a_rows > 0) pair::tma_2d(to + c * 8192, map, 0, (x / 64 + c) * g.a_rows + k, bar);
-          else pair::tma_2d(to + c * 8192, map, x + c * 64, k, bar);
+          if (A && g.a_rows > 0) pair::tma_2d<CTAS>(to + c * 8192, map, 0, (x / 64 + c) * g.a_rows + k, bar);
+          else pair::tma_2d<CTAS>(to + c * 8192, map, x + c * 64, k, bar);
         }
       } else {
-        if (A && g.a_rows > 0) pair::tma_2d(to, map, 0, k / 64 * g.a_rows + x, bar);
-        else pair::tma_2d(to, map, k, x, bar);
+        if (A && g.a_rows > 0) pair::tma_2d<CTAS>(to, map, 0, k / 64 * g.a_rows + x, bar);
+        else pair::tma_2d<CTAS>(to, map, k, x, bar);
       }
     }
   }
 }
 
-template <int AM, class P>
+template <int AM, int CTAS, class P>
 __device__ __forceinline__ void pair_multiply(const PairShape& g, PairWalk walk, PairRole& r) {
-  using T = PairTile<AM>;
+  using T = PairTile<AM, CTAS>;
   PairItem i;
   for (; !r.failed && walk.next(g, i); ++r.tile) {
     const uint32_t buf = r.tile & 1, d = r.tmem + buf * 256;
@@ -287,14 +312,14 @@ __device__ __forceinline__ void pair_multiply(const PairShape& g, PairWalk walk,
       const uint64_t a = pair::operand_desc<P::kAMN>(r.ring + st * T::kStage), b = pair::operand_desc<P::kBMN>(r.ring + st * T::kStage + T::kA);
 #pragma unroll
       for (int k = 0; k < kPairK / 16; ++k)  // 16 k's: 32 bytes along a row, or two groups of 8 rows
-        pair::mma(d, a + k * ((P::kAMN ? 2048 : 32) >> 4), b + k * ((P::kBMN ? 2048 : 32) >> 4), g.idesc, kb > first || k > 0);
-      pair::commit_both(&r.empty[st]);
+        pair::mma<CTAS>(d, a + k * ((P::kAMN ? 2048 : 32) >> 4), b + k * ((P::kBMN ? 2048 : 32) >> 4), g.idesc, kb > first || k > 0);
+      pair::commit_all<CTAS>(&r.empty[st]);
     }
-    pair::commit_both(&r.acc_full[buf]);
+    pair::commit_all<CTAS>(&r.acc_full[buf]);
   }
 }
 
-template <class P>
+template <int CTAS, class P>
 __device__ __forceinline__ void pair_epilogue(const typename P::Args& p, const PairShape& g, PairWalk walk, PairRole& r, int pair, int w,
                                               int lane, uint32_t staging) {
   using Job = typename P::Job;
@@ -324,12 +349,12 @@ __device__ __forceinline__ void pair_epilogue(const typename P::Args& p, const P
   Job::finish(p.job, state, pair, row, half);
 }
 
-template <int AM, class P0, class P1>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+template <int AM, int CTAS, class P0, class P1>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_mma_kernel(const __grid_constant__ typename P0::Args p0, const __grid_constant__ typename P1::Args p1,
                     unsigned long long* stats) {
-  using T = PairTile<AM>;
-  static_assert(AM == 128 || !P0::kAMN, "fewer rows of A in K-major order only");
+  using T = PairTile<AM, CTAS>;
+  static_assert((AM == 128 && CTAS == 2) || (!P0::kAMN && !P0::kBMN), "fewer rows of A, or single CTAs, with K-major operands only");
   constexpr int ST = T::kStages;
   extern __shared__ uint8_t s_raw[];
   __shared__ __align__(8) uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2];
@@ -337,19 +362,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ PairPlan s_plan;
   __shared__ uint32_t s_tmem;
   const uint32_t ring = (smem_u32(s_raw) + 1023u) & ~1023u;
-  const int w = threadIdx.x / kWarp, lane = lane_id(), pair_id = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int w = threadIdx.x / kWarp, lane = lane_id(), pair_id = blockIdx.x / CTAS, pairs = gridDim.x / CTAS;
   may_follow();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], 2 * kEpiWarps);
+    for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], CTAS * kEpiWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pair::prefetch_map(&p0.a), pair::prefetch_map(&p0.b);
     if constexpr (!P1::kNone) pair::prefetch_map(&p1.a), pair::prefetch_map(&p1.b);
   }
   if (w == 0) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    if constexpr (CTAS == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
   }
   pair::fence_before();
   __syncthreads();
@@ -376,14 +406,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (w == kEpiWarps) {
     if (lane == 0) {
-      pair_copy<AM, P0, false>(p0, g0, walk0, r);
-      if constexpr (!P1::kNone) pair_copy<AM, P1, false>(p1, g1, walk1, r);
+      pair_copy<AM, CTAS, P0, false>(p0, g0, walk0, r);
+      if constexpr (!P1::kNone) pair_copy<AM, CTAS, P1, false>(p1, g1, walk1, r);
     }
     __syncwarp();
   } else if (w == kEpiWarps + 2) {
     if (lane == 0) {
-      pair_copy<AM, P0, true>(p0, g0, walk0, r);
-      if constexpr (!P1::kNone) pair_copy<AM, P1, true>(p1, g1, walk1, r);
+      pair_copy<AM, CTAS, P0, true>(p0, g0, walk0, r);
+      if constexpr (!P1::kNone) pair_copy<AM, CTAS, P1, true>(p1, g1, walk1, r);
       // Copies must not be in flight when a CTA ends: in the even CTA, whose barriers count both CTAs' copies, the last
       // round of every stage has landed (its products are done by then, unless a wait gave up).
       if (r.rank == 0)
@@ -393,22 +423,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else if (w == kEpiWarps + 1) {
     if (r.rank == 0 && lane == 0) {
-      pair_multiply<AM, P0>(g0, walk0, r);
-      if constexpr (!P1::kNone) pair_multiply<AM, P1>(g1, walk1, r);
+      pair_multiply<AM, CTAS, P0>(g0, walk0, r);
+      if constexpr (!P1::kNone) pair_multiply<AM, CTAS, P1>(g1, walk1, r);
     }
     __syncwarp();
   } else {
     const uint32_t staging = ring + ST * T::kStage + w * kStagingBytes;
-    pair_epilogue<P0>(p0, g0, walk0, r, pair_id, w, lane, staging);
+    pair_epilogue<CTAS, P0>(p0, g0, walk0, r, pair_id, w, lane, staging);
     if constexpr (!P1::kNone)
-      if (!r.failed) pair_epilogue<P1>(p1, g1, walk1, r, pair_id, w, lane, staging);
+      if (!r.failed) pair_epilogue<CTAS, P1>(p1, g1, walk1, r, pair_id, w, lane, staging);
   }
   if (r.failed && lane == 0) stat_add(stats, TBE_STAT_WAIT_TIMEOUT, 1);
   __syncwarp();
   pair::fence_before();
   cluster_sync();  // neither CTA ends, or frees its TMEM, while the other may still reach it
   pair::fence_after();
-  if (w == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(r.tmem) : "memory");
+  if (w == 0) {
+    if constexpr (CTAS == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(r.tmem) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(r.tmem) : "memory");
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // NULL where the driver has none
