@@ -317,13 +317,13 @@ struct OutJob {
   static __device__ __forceinline__ void finish(const Args&, const State&, int, int, int) {}
 };
 
-// Sums in fp32, [split][tokens][stride]: stored by the first piece, added to by the others (each by one thread, so that the order is
+// Sums in fp32, [split][rows][stride]: stored by the first piece, added to by the others (each by one thread, so that the order is
 // the pieces').
 struct SumJob {
   struct Args {
     float* sums;
     int64_t stride;        // a multiple of 8
-    int tokens, add, width;
+    int rows, add, width;
   };
   using Row = NoRow;
   using State = NoState;
@@ -332,12 +332,12 @@ struct SumJob {
                                               R&& release) {
     const int i = it.m * kPairM + row;
     const int col0 = it.n * a.width + half * 128;
-    float* dst = a.sums + (static_cast<int64_t>(it.split) * a.tokens + i) * a.stride + col0;
+    float* dst = a.sums + (static_cast<int64_t>(it.split) * a.rows + i) * a.stride + col0;
     each_columns<128>(tmem, release, [&](int j, pair::Columns& c) {
       if (half * 128 + j * 32 >= a.width) return;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (i >= a.tokens || col0 + j * 32 + q * 8 >= a.stride) continue;
+        if (i >= a.rows || col0 + j * 32 + q * 8 >= a.stride) continue;
         if (a.add) {
 #pragma unroll
           for (int x = 0; x < 2; ++x)
@@ -641,15 +641,16 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_co
   if (lane == 0) write_mean(a.mean, d, n);
 }
 
-// dhidden = alpha * the sums of all splits, to the selected tokens' rows.
+// A gradient's rows = alpha * the sums of all splits: dhidden's to the selected tokens' rows, dweight's as they are.
 template <typename T>
 struct FinishArgs {
   const float* sums;
   const float* meta;
-  const int* live;
+  const int* live;         // NULL: all rows
+  const int* live_k;       // NULL, or the length of the sums, of whose blocks there may be fewer than splits
   const int* place;
   T* out;
-  int64_t tokens, sums_stride, stride;
+  int64_t rows, sums_stride, stride;
   int splits, cols, vec;
 };
 
@@ -657,16 +658,17 @@ template <typename T>
 __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant__ FinishArgs<T> a) {
   wait_before();
   const int per_row = static_cast<int>(a.sums_stride / 8);
-  const int64_t total = static_cast<int64_t>(*a.live) * per_row;
+  const int64_t total = (a.live != nullptr ? static_cast<int64_t>(*a.live) : a.rows) * per_row;
+  const int splits = a.live_k != nullptr ? min(a.splits, (max(*a.live_k, 1) + kPairK - 1) / kPairK) : a.splits;
   const float alpha = a.meta[1];
   for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; x < total; x += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t i = total >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(per_row) : x / per_row;
     const int col = static_cast<int>(x - i * per_row) * 8;
-    const int64_t to = a.place[i];
+    const int64_t to = a.live != nullptr ? a.place[i] : i;
     float f[8] = {};
-#pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-      const float4* p = reinterpret_cast<const float4*>(a.sums + (s * a.tokens + i) * a.sums_stride + col);
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(a.sums + (s * a.rows + i) * a.sums_stride + col);
       const float4 u = p[0], v = p[1];
       f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w, f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
     }
@@ -777,6 +779,7 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
   using Sum = Product<false, true, SumJob>;
   using Direct = Product<false, true, OutJob<T>>;
   using Out = Product<true, true, OutJob<T>>;
+  using SumOut = Product<true, true, SumJob>;
   tbe_status st;
   for (int64_t first = 0; first < a.rows; first += l.piece) {
     const int here = static_cast<int>(a.rows - first < l.piece ? a.rows - first : l.piece);
@@ -799,19 +802,29 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
       typename Direct::Args da{maps[2], maps[3], sum,
                                {meta, static_cast<T*>(dhidden), a.dhidden_stride, 0, a.tokens, placed, live, a.dim, width,
                                 whole_stores(dhidden, a.dhidden_stride)}};
-      st = launch_pair<128, 2, Direct, Out>(da, oa, items, a, dev, s);
+      if ((st = launch_pair<128, 2, Direct, Out>(da, oa, items, a, dev, s)) != TBE_OK) return st;
+      continue;
+    }
+    Sum::Args sa{maps[2], maps[3], sum, {sums, l.dim_pad, N, first > 0, width}};
+    if (l.out_splits > 1) {
+      SumOut::Args wa{maps[4], maps[5], oa.g, {reinterpret_cast<float*>(ws + l.out_sums), l.dim_pad, here, 0, width}};
+      wa.g.splits = l.out_splits;
+      st = launch_pair<128, 2, Sum, SumOut>(sa, wa, static_cast<int64_t>(sum.items()) + wa.g.items(), a, dev, s);
     } else {
-      typename Sum::Args sa{maps[2], maps[3], sum, {sums, l.dim_pad, N, first > 0, width}};
       st = launch_pair<128, 2, Sum, Out>(sa, oa, items, a, dev, s);
     }
     if (st != TBE_OK) return st;
   }
   if (l.direct) return TBE_OK;
-  FinishArgs<T> fa{sums, meta, live, placed, static_cast<T*>(dhidden), a.tokens, l.dim_pad, a.dhidden_stride, l.splits, a.dim,
-                   whole_stores(dhidden, a.dhidden_stride)};
-  int64_t blocks = ceil_div(a.tokens * (l.dim_pad / 8), 256);
-  if (blocks > dev.sms * 8) blocks = dev.sms * 8;
-  return cuda_status(launch_after(loss_finish_kernel<T>, static_cast<unsigned>(blocks), 256, 0, s, fa));
+  auto finish = [&](const float* from, const int* selected, void* out, int64_t rows, int64_t stride, int splits) {
+    const FinishArgs<T> fa{from, meta, selected, selected != nullptr ? nullptr : live, placed, static_cast<T*>(out), rows, l.dim_pad, stride, splits, a.dim, whole_stores(out, stride)};
+    int64_t blocks = ceil_div(rows * (l.dim_pad / 8), 256);
+    if (blocks > dev.sms * 8) blocks = dev.sms * 8;
+    return cuda_status(launch_after(loss_finish_kernel<T>, static_cast<unsigned>(blocks), 256, 0, s, fa));
+  };
+  st = finish(sums, live, dhidden, a.tokens, a.dhidden_stride, l.splits);
+  if (st != TBE_OK || l.out_splits <= 1) return st;
+  return finish(reinterpret_cast<float*>(ws + l.out_sums), nullptr, dweight, a.rows, a.dweight_stride, l.out_splits);
 }
 
 }  // namespace
@@ -858,7 +871,16 @@ LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev
   l.piece = round_up(ceil_div(a.rows, pieces), 256);
   const int64_t d_tiles = ceil_div(a.dim, gradient_width(a.dim)), blocks = ceil_div(l.piece, kPairK);
   const int64_t tiles = ceil_div(a.tokens, kPairM) * d_tiles, pairs = dev.sms / 2;
-  l.direct = a.rows <= l.piece && ceil_div(a.rows, kPairK) <= kDirectBlocks;
+  // Where the table has few tiles, the sums over the tokens of dweight are split as well: no tile shall take more than twice a pair's
+  // share (14732 x 17 x 48 bf16: 116 us by one pair's sum, 60 split).
+  const int64_t out_tiles = ceil_div(l.piece, 256) * d_tiles, out_blocks = ceil_div(a.tokens, kPairK);
+  const int64_t share = ceil_div(tiles * blocks + out_tiles * out_blocks, pairs);
+  l.out_splits = 1;
+  if (a.rows <= l.piece && out_blocks > 16 && out_blocks > 2 * share) {
+    const int64_t n = ceil_div(out_blocks, share < 4 ? 4 : share), most = ceil_div(2 * pairs, out_tiles);
+    l.out_splits = static_cast<int>(n < most ? n : most);
+  }
+  l.direct = a.rows <= l.piece && ceil_div(a.rows, kPairK) <= kDirectBlocks && l.out_splits == 1;
   l.splits = 1;
   if (!l.direct) {  // none of the tiles of dhidden's long sums shall take more than half of a pair's share of a piece's blocks
     const int64_t all = tiles * blocks + ceil_div(l.piece, 256) * d_tiles * ceil_div(a.tokens, kPairK);
@@ -884,8 +906,12 @@ LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev
   const int64_t whole = l.dz_rows * round_up(a.rows, 256) * 2, least = l.dz_rows * 512;
   const int64_t capped = least > kPieceBytes ? least : kPieceBytes;
   l.dz = place(&at, whole < capped ? whole : capped);
-  // splits * tiles < 2 pairs + tiles
-  l.sums = place(&at, (2 * pairs * kPairM * 256 + a.tokens * l.dim_pad) * 4);
+  // splits * tiles < 2 pairs + tiles; out_splits * out_tiles < 2 pairs + out_tiles, and those are at most pairs / 2 tiles, as
+  // twice their blocks are more than a share
+  const int64_t tile = int64_t(kPairM) * 256, row = (2 * pairs + 1) * l.dim_pad;
+  const int64_t split = 2 * pairs * tile + a.tokens * l.dim_pad, out_split = 3 * pairs * tile;
+  l.sums = place(&at, (split < a.tokens * row ? split : a.tokens * row) * 4);
+  l.out_sums = place(&at, (out_split < a.rows * row ? out_split : a.rows * row) * 4);
   l.total = at;
   return l;
 }

@@ -57,7 +57,10 @@ struct PairShape {
 
   __device__ __forceinline__ void settle() {
     if (live_m != nullptr) m_tiles = (max(*live_m, 1) + kPairM - 1) / kPairM;
-    if (live_k != nullptr) k_blocks = (max(*live_k, 1) + kPairK - 1) / kPairK;
+    if (live_k != nullptr) {
+      k_blocks = (max(*live_k, 1) + kPairK - 1) / kPairK;
+      splits = min(splits, k_blocks);
+    }
   }
   __host__ __device__ __forceinline__ int items() const { return m_tiles * n_tiles * splits; }
 };

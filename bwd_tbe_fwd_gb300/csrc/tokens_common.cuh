@@ -33,9 +33,10 @@ struct LossBackwardLayout {
   int64_t dim_pad;                 // row of the fp32 sums of dhidden
   int64_t piece;                   // rows of the table at a time
   int64_t dz_rows;                 // of a block of 64 columns of dz
-  int splits;                      // parts of the long product of dhidden
+  int splits;                      // parts of the long sums of dhidden
+  int out_splits;                  // parts of the sums of dweight
   bool direct;                     // it is written as it is: one piece, one split
-  size_t meta, live, place, target, row, coef, lse2, hidden, weight, dz, sums, total;
+  size_t meta, live, place, target, row, coef, lse2, hidden, weight, dz, sums, out_sums, total;
 };
 LossForwardLayout loss_forward_layout(const LossArgs& a);
 LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev);

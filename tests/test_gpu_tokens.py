@@ -241,3 +241,48 @@ def test_loss_sums_of_dhidden_in_one_and_in_many_splits(rows, dim):
 def test_loss_of_few_tokens_over_many_rows(tokens):
     """One tile of tokens, more tiles of the table than pairs of CTAs: the pairs join their parts."""
     check_loss(tokens, 30_011, 72, "bf16", ids="hot", seed=tokens)
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 8), (17, 48), (300, 40), (257, 300)])
+@pytest.mark.parametrize("kind", ["spread", "none", "one"])
+def test_loss_of_many_tokens_over_few_rows(rows, dim, kind):
+    """dweight's sums over the tokens are split, into as many parts as there are blocks of tokens that count at most."""
+    check_loss(6000, rows, dim, "bf16", ids=kind, seed=rows)
+
+
+def test_loss_of_many_tokens_of_which_few_count():
+    h, w, t, t_h = loss_inputs(8000, 20, 64, "bf16", seed=1)
+    t[130:] = -1
+    t_h[130:] = -1
+    op = SoftmaxLoss(20, 64, 8000)
+    _, lse, mean = op.forward(h, w, t)
+    grads = op.backward(h, w, t, lse, mean=mean)
+    want, bound = ref.loss_gradients(host(h), host(w), t_h, host(lse), np.full(8000, float(mean[1])), 1.0, "bf16")
+    for got, v, b, name in zip(grads, want, bound, ("dhidden", "dweight")):
+        within(got, v, b, name)
+
+
+@pytest.mark.parametrize("table,out", TYPES)
+@pytest.mark.parametrize("dim", [63, 64, 66, 127, 130, 914, 1597])
+def test_lookup_wide_rows_without_vectors(dim, table, out):
+    check_lookup(333, 50, dim, table, out, pad=1 if dim % 2 else 2, scale=0.3, seed=dim)
+    check_lookup(50, 20, dim, table, out, seed=dim + 1)
+
+
+@pytest.mark.parametrize("at", [1, 2, 4])
+def test_lookup_buffers_may_begin_anywhere(at):
+    """Tables, gradients and rows that begin at any element of a buffer, whose other elements stay as they are."""
+    g = gen(at)
+    rows, dim, tokens = 90, 64, 400
+    emb = TokenEmbedding(rows, dim, tokens, torch.float16, torch.float16)
+    ids = torch.randint(-1, rows, (tokens,), generator=g).cuda()
+    wide = [torch.full((n * dim + 8,), 7.0, dtype=torch.float16, device="cuda") for n in (rows, tokens, rows, tokens)]
+    table, out, grad, dout = (t[at:at + n * dim].view(n, dim) for t, n in zip(wide, (rows, tokens, rows, tokens)))
+    table.copy_(torch.randn(rows, dim, generator=g))
+    dout.copy_(torch.randn(tokens, dim, generator=g))
+    emb.forward(table, ids, out=out)
+    emb.backward(dout, ids, grad=grad)
+    want = emb.forward(table.clone(), ids), emb.backward(dout.clone(), ids)
+    assert torch.equal(out, want[0]) and torch.equal(grad, want[1])
+    for t, n in zip(wide, (rows, tokens, rows, tokens)):
+        assert bool((t[:at] == 7).all()) and bool((t[at + n * dim:] == 7).all())
