@@ -163,7 +163,7 @@ class SoftmaxLoss(_Tokens):
 
     hidden and dhidden are [tokens, dim], weight and dweight [rows, dim], all of ``dtype`` (float16 or bfloat16); targets hold
     at most ``tokens`` of ``index_dtype``.  Rows may be strided (those of weight by
-    multiples of 8 where dim is one); columns are contiguous."""
+    multiples of 8 where dim is one, from a multiple of 16 bytes on); columns are contiguous."""
 
     def __init__(self, rows: int, dim: int, tokens: int, dtype=torch.bfloat16, index_dtype=torch.int64, scale: float = 1.0,
                  device="cuda"):
@@ -179,6 +179,8 @@ class SoftmaxLoss(_Tokens):
         stride = _matrix(weight, "weight", self.dtype, self.rows, self.dim, self)
         if stride % 8 and self.dim % 8 == 0:  # the workspace has no room for a copy that TMA can address
             raise ValueError("the rows of weight must be a multiple of 8 elements apart")
+        if stride % 8 == 0 and weight.data_ptr() % 16:
+            raise ValueError("weight must begin at a multiple of 16 bytes")
         return stride
 
     def forward(self, hidden, weight, targets, loss=None, lse=None, mean=None, stream=None):

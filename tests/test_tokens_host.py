@@ -209,6 +209,7 @@ def test_the_binding_refuses(fake):
     h, w, lse = torch.zeros(6, 8, dtype=torch.bfloat16), torch.zeros(10, 8, dtype=torch.bfloat16), torch.zeros(6)
     for args, kw, error in (((h.float(), w, ids), {}, TypeError), ((h, w[:9], ids), {}, ValueError), ((h[:5], w, ids), {}, ValueError),
                             ((h, torch.zeros(10, 9, dtype=torch.bfloat16)[:, :8], ids), {}, ValueError),
+                            ((h, torch.zeros(84, dtype=torch.bfloat16)[4:].view(10, 8), ids), {}, ValueError),
                             ((h, w, ids), dict(loss=torch.zeros(5)), ValueError), ((h, w, ids), dict(mean=torch.zeros(2).double()), TypeError)):
         with pytest.raises(error):
             op.forward(*args, **kw)
