@@ -10,8 +10,8 @@
  * nothing and copies nothing to the host; return values report what the host can see.  Structs are read before
  * the call returns and not kept.  Sums and softmax statistics are held in fp32.  The same inputs give the same
  * bits on a given GPU.  Two calls that use the same workspace must not overlap in time.
- * d_stats: NULL, or int64 [TBE_NUM_STATS] on the device: ids outside the table other than negative ones are
- * counted in TBE_STAT_UNREPAIRED, a bounded device-side wait that gave up (its results are then not valid) in
+ * d_stats: NULL, or int64 [TBE_NUM_STATS] on the device: ids past the table are counted in TBE_STAT_UNREPAIRED (targets by
+ * the forward alone), a bounded device-side wait that gave up (its results are then not valid) in
  * TBE_STAT_WAIT_TIMEOUT.
  */
 #ifndef TBE_TOKENS_H
