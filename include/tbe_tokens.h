@@ -98,7 +98,9 @@ tbe_status tbe_softmax_loss_forward(const tbe_softmax_problem* prob, const void*
                                     const void* targets, float* loss, float* lse, float* mean, void* ws, size_t ws_bytes,
                                     int64_t* d_stats, void* stream);
 
-/* lse as the forward left it.  dhidden [tokens, dim] and dweight [rows, dim] are overwritten; they overlap nothing. */
+/* lse as the forward left it.  The workspace holds dz of a piece of the table (up to 512 MB, or 512 bytes a token where
+ * that is more), fp32 sums (dhidden's size, and up to 100 MB) and copies of hidden and of a weight that needs one.
+ * dhidden [tokens, dim] and dweight [rows, dim] are overwritten; they overlap nothing. */
 size_t tbe_softmax_loss_backward_workspace_size(const tbe_softmax_problem* prob);
 tbe_status tbe_softmax_loss_backward(const tbe_softmax_problem* prob, const void* hidden, const void* weight,
                                      const void* targets, const float* lse, const float* dloss, const float* mean,
