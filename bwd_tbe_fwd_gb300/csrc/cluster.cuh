@@ -43,16 +43,17 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t addr, uint32_t cta)
 __device__ __forceinline__ void may_follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The most dynamic shared memory that a kernel may ask for, set once for each device (a launch needs it, and the call takes as long
+// The most dynamic shared memory that a kernel may ask for (and clusters of up to 16 CTAs), set once for each device (a launch needs it, and the call takes as long
 // as half a launch).  `done`: a word of the caller's own for this kernel, zero at first.
 template <typename K>
-cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done, bool wide_clusters = false) {
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (dev < 64 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
-  const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (f == cudaSuccess && wide_clusters) f = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (f == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
   return f;
 }

@@ -148,9 +148,9 @@ __global__ void __launch_bounds__(256) lookup_keys_kernel(const __grid_constant_
 
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / kWarp;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;   // 8 where the device has no room for more
 constexpr int kMaxPerThread = 8;
-constexpr int64_t kClusterTokens = int64_t(kMaxCluster) * kClusterThreads * kMaxPerThread;
+constexpr int64_t kCtaTokens = int64_t(kClusterThreads) * kMaxPerThread;
 
 struct ClusterSortArgs {
   KeyArgs k;                 // keys, vals: the sorted ones
@@ -243,7 +243,7 @@ __device__ __forceinline__ void rank_few(const KeyArgs& a, uint32_t* s_key) {
   a.vals[at] = static_cast<uint32_t>(t);
 }
 
-// Stable radix sort of (id, token) by one cluster, up to 65536 of them: the items stay in its shared memory, each CTA
+// Stable radix sort of (id, token) by one cluster, up to 131072 of them: the items stay in its shared memory, each CTA
 // holding a contiguous 1024 IPT of the current order.  A pass ranks a CTA's items by ballots and counters of its
 // warps' own, joins the CTAs' digit counts through distributed shared memory, and sends each item to its place in whichever CTA
 // holds it.  One launch for what takes two to four passes of three launches through memory, and the other clusters of
@@ -353,17 +353,20 @@ __global__ void __launch_bounds__(kClusterThreads, 1) lookup_sort_kernel(const _
     cluster_wait();
     uint32_t total = 0, earlier = 0;
     if (d < R) {
-      uint32_t n[kMaxCluster];
+#pragma unroll 1
+      for (uint32_t c0 = 0; c0 < ctas; c0 += 8) {
+        uint32_t n[8];
 #pragma unroll
-      for (uint32_t c = 0; c < kMaxCluster; ++c) {  // all of them in flight
-        n[c] = 0;
-        if (c < ctas)
-          asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n[c]) : "r"(cluster_address(smem_u32(s_count + d), c)) : "memory");
-      }
+        for (uint32_t c = 0; c < 8; ++c) {  // all of them in flight
+          n[c] = 0;
+          if (c0 + c < ctas)
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n[c]) : "r"(cluster_address(smem_u32(s_count + d), c0 + c)) : "memory");
+        }
 #pragma unroll
-      for (uint32_t c = 0; c < kMaxCluster; ++c) {
-        total += n[c];
-        if (c < cta) earlier += n[c];
+        for (uint32_t c = 0; c < 8; ++c) {
+          total += n[c];
+          if (c0 + c < cta) earlier += n[c];
+        }
       }
     }
     const uint32_t before = block_before(total, s_wsum[1]);
@@ -657,39 +660,58 @@ int tokens_per_warp(const LookupArgs& a, int slabs, const DeviceInfo& dev) {
   return ceil_div(a.tokens, 32 * kSumWarps) * slabs * 2 < dev.sms ? 8 : 32;
 }
 
-// One cluster sorts; where there is a gradient to set to zero, others do that: as many as run beside it (a cluster lies within one
-// of the GPU's processing clusters, so that 19 clusters of 8 do not fit 152 SMs at once, and each takes an equal share).
+// How many clusters of `ctas` that sort run at once (a cluster lies within one of the GPU's processing clusters: 15 of 8 CTAs on 152
+// SMs); asked once for each device.
 template <int IPT>
-tbe_status launch_cluster_sort_t(const ClusterSortArgs& c, int ctas, int64_t zero, const DeviceInfo& dev, cudaStream_t s) {
-  auto* kernel = lookup_sort_kernel<IPT>;
-  const size_t smem = cluster_sort_smem(IPT);
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(kernel, smem, allowed);
-  if (e != cudaSuccess) return cuda_status(e);
+int clusters_at_once(int ctas, const DeviceInfo& dev) {
+  static std::atomic<int> known[64][5];   // by device and the logarithm of the size: one more than the number, 0: not asked yet
+  int log = 0;
+  while (1 << log < ctas) ++log;
+  std::atomic<int>* slot = dev.id < 64 ? &known[dev.id][log] : nullptr;
+  if (slot != nullptr && slot->load(std::memory_order_relaxed) > 0) return slot->load(std::memory_order_relaxed) - 1;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kClusterThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = cluster_sort_smem(IPT);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  static std::atomic<uint64_t> allowed{0};
+  int n = 0;
+  if (allow_smem(lookup_sort_kernel<IPT>, cluster_sort_smem(IPT), allowed, true) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, lookup_sort_kernel<IPT>, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = 0;
+  }
+  if (slot != nullptr) slot->store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+int most_ctas(const DeviceInfo& dev) { return clusters_at_once<kMaxPerThread>(kMaxCluster, dev) > 0 ? kMaxCluster : 8; }
+
+// One cluster sorts; where there is a gradient to set to zero, others do that, as many as run beside it (each takes an equal share).
+template <int IPT>
+tbe_status launch_cluster_sort_t(const ClusterSortArgs& c, int ctas, int64_t zero, const DeviceInfo& dev, cudaStream_t s) {
+  const int clusters = clusters_at_once<IPT>(ctas, dev);
+  if (clusters < 1) return cuda_status(cudaErrorInvalidConfiguration);
+  int64_t others = 0;
+  if (zero > 0) {
+    others = ceil_div(zero, ctas) < clusters - 1 ? ceil_div(zero, ctas) : clusters - 1;
+    if (others < 1) others = 1;
+  }
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas * (1 + others)));
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = cluster_sort_smem(IPT);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (zero > 0) {
-    static std::atomic<int> known[64][4];   // by device and cluster size; 0: not asked yet
-    const int size = ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3;
-    std::atomic<int>* slot = dev.id < 64 ? &known[dev.id][size] : nullptr;
-    int clusters = slot != nullptr ? slot->load(std::memory_order_relaxed) : 0;
-    if (clusters == 0) {
-      e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
-      if (e != cudaSuccess) return cuda_status(e);
-      if (slot != nullptr) slot->store(clusters, std::memory_order_relaxed);
-    }
-    const int64_t others = ceil_div(zero, ctas) < clusters - 1 ? ceil_div(zero, ctas) : clusters - 1;
-    cfg.gridDim.x = static_cast<unsigned>(ctas * (1 + (others > 1 ? others : 1)));
-  }
-  e = cudaLaunchKernelEx(&cfg, kernel, c);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, lookup_sort_kernel<IPT>, c);
   note_launch();
   return cuda_status(e);
 }
@@ -704,8 +726,12 @@ tbe_status launch_cluster_sort(const LookupArgs& a, const KeyArgs& k, void* grad
     c.bits[p] = (left + c.passes - p - 1) / (c.passes - p);
     left -= c.bits[p];
   }
+  // As many CTAs as have tokens, up to 16; but 8 where there is much to set to zero, which takes longer than the sort and has more SMs
+  // beside smaller clusters (12345 tokens, 30 MB: 24.6 us a call with 8, 23.2 with 16; 65536 tokens, 268 MB: 86 and 90).
   int ctas = 1;
-  while (ctas < kMaxCluster && ctas * kClusterThreads < a.tokens) ctas *= 2;
+  const bool long_zeros = grad != nullptr && a.rows * row_bytes > (int64_t(64) << 20);
+  const int most = long_zeros && a.tokens <= 8 * kCtaTokens ? 8 : most_ctas(dev);
+  while (ctas < most && ctas * kClusterThreads < a.tokens) ctas *= 2;
   const int64_t per_thread = ceil_div(a.tokens, static_cast<int64_t>(ctas) * kClusterThreads);
   const int64_t zero = grad == nullptr ? 0 : ceil_div(a.rows * row_bytes, 2 * kZeroPiece);
   if (per_thread <= 1) return launch_cluster_sort_t<1>(c, ctas, zero, dev, s);
@@ -741,7 +767,7 @@ tbe_status launch_lookup_backward(const LookupArgs& a, const void* dout, const v
                                   const DeviceInfo& dev, cudaStream_t s) {
   const BackwardLayout l = backward_layout(a, dev);
   const int64_t elem = dtype_bytes(a.ttype), row = a.dim * elem, pitch = a.table_stride * elem;
-  const bool in_cluster = a.tokens > 0 && a.tokens <= kClusterTokens;
+  const bool in_cluster = a.tokens > 0 && a.tokens <= most_ctas(dev) * kCtaTokens;
   if (!accumulate && !in_cluster) {
     const tbe_status st = cuda_status(row == pitch ? cudaMemsetAsync(grad, 0, row * a.rows, s)
                                                    : cudaMemset2DAsync(grad, pitch, 0, row, a.rows, s));

@@ -286,3 +286,9 @@ def test_lookup_buffers_may_begin_anywhere(at):
     assert torch.equal(out, want[0]) and torch.equal(grad, want[1])
     for t, n in zip(wide, (rows, tokens, rows, tokens)):
         assert bool((t[:at] == 7).all()) and bool((t[at + n * dim:] == 7).all())
+
+
+@pytest.mark.parametrize("tokens", [8193, 16384, 16385, 65535, 65537, 131072, 131073])
+def test_lookup_at_the_borders_of_the_sorts(tokens):
+    check_lookup(tokens, 3000, 4, "f32", "f32", ids="hot", seed=tokens, room=1000)
+    check_lookup(tokens, 1_500_000, 4, "f32", "f32", accumulate=True, seed=tokens + 1)
