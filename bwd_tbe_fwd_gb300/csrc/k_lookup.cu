@@ -247,7 +247,8 @@ __device__ __forceinline__ void rank_few(const KeyArgs& a, uint32_t* s_key) {
 // holding a contiguous 1024 IPT of the current order.  A pass ranks a CTA's items by ballots and counters of its
 // warps' own, joins the CTAs' digit counts through distributed shared memory, and sends each item to its place in whichever CTA
 // holds it.  One launch for what takes two to four passes of three launches through memory, and the other clusters of
-// the grid write the gradient's zeros at the same time.
+// the grid write the gradient's zeros at the same time.  (16384 tokens of 131072 rows: 14 us, 32768: 16; the latency of two passes
+// of eight barriers each.)
 template <int IPT>
 __global__ void __launch_bounds__(kClusterThreads, 1) lookup_sort_kernel(const __grid_constant__ ClusterSortArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
@@ -443,7 +444,7 @@ __device__ __forceinline__ Pack<TT, V> old_row(const SumArgs& a, uint32_t key, i
 // A CTA adds up 32 V columns of 8 T sorted tokens, a warp T of them, 8 rows in flight.  A warp writes the runs that
 // begin and end among its tokens; what it has of runs that reach over its first or last token meets in shared memory, and what
 // the CTA has of runs that reach over its own is left for the join.  A run's additions keep the tokens' order, warp by
-// warp and chunk by chunk.
+// warp and chunk by chunk.  (65536 x 1024 bf16: 31 us for 184 MB, 87% of the copy rate; 16384: 14 us.)
 template <typename TT, typename OT, int V, bool ACC, int T>
 __global__ void __launch_bounds__(kSumThreads) lookup_sum_kernel(const __grid_constant__ SumArgs a) {
   constexpr int U = 8;
