@@ -11,7 +11,7 @@
 // 1870 TFLOP/s, 97% of a library product of 8192^3; with no copies at all 330 us; with k = 1024 1790 TFLOP/s.)
 //
 // Every wait is bounded.  A role whose wait gives up leaves its loop, the others follow by their own limits, the copies
-// in flight are waited for once more, and TBE_STAT_WAIT_TIMEOUT is counted.
+// in flight are given time to land, and TBE_STAT_WAIT_TIMEOUT is counted.
 #pragma once
 
 #include <cuda.h>
@@ -294,6 +294,19 @@ __device__ __forceinline__ void pair_copy(const typename P::Args& p, const PairS
   }
 }
 
+// What is under way to this CTA's shared memory when its copies are all issued: the copies themselves, and the arrivals on `empty`,
+// which the even CTA's products send to both CTAs.  Neither may find that the CTA has ended, and nothing orders those arrivals
+// before the one on acc_full that the epilogue sees last.  A stage's arrival comes after both CTAs' copies of it have landed and
+// been used, so the last round of arrivals is all there is to wait for.  Where a wait gave up it may never come; the
+// copies that were issued land within microseconds all the same, and get a millisecond.
+template <int ST>
+__device__ __forceinline__ void pair_drain(PairRole& r) {
+  for (uint32_t k = r.it < ST ? 0 : r.it - ST; k < r.it && !r.failed; ++k)
+    r.failed = !mbar_wait_bounded(&r.empty[k % ST], (k / ST) & 1, kPairWaitLimit);
+  if (r.failed)
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+}
+
 template <int AM, int CTAS, class P>
 __device__ __forceinline__ void pair_multiply(const PairShape& g, PairWalk walk, PairRole& r) {
   using T = PairTile<AM, CTAS>;
@@ -412,17 +425,14 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (lane == 0) {
       pair_copy<AM, CTAS, P0, false>(p0, g0, walk0, r);
       if constexpr (!P1::kNone) pair_copy<AM, CTAS, P1, false>(p1, g1, walk1, r);
+      pair_drain<ST>(r);
     }
     __syncwarp();
   } else if (w == kEpiWarps + 2) {
     if (lane == 0) {
       pair_copy<AM, CTAS, P0, true>(p0, g0, walk0, r);
       if constexpr (!P1::kNone) pair_copy<AM, CTAS, P1, true>(p1, g1, walk1, r);
-      // Copies must not be in flight when a CTA ends: in the even CTA, whose barriers count both CTAs' copies, the last
-      // round of every stage has landed (its products are done by then, unless a wait gave up).
-      if (r.rank == 0)
-        for (uint32_t k = r.it < ST ? 0 : r.it - ST; k < r.it; ++k)
-          r.failed = !mbar_wait_bounded(&full[k % ST], (k / ST) & 1, kPairWaitLimit) || r.failed;
+      pair_drain<ST>(r);
     }
     __syncwarp();
   } else if (w == kEpiWarps + 1) {
