@@ -252,6 +252,7 @@ struct OutJob {
     int64_t stride, first, rows;   // first row of the product in `out`, rows of out
     const int* place;      // NULL, or the row of out for each row of the product, of which there are *live
     const int* live;
+    const float* down;     // NULL, or another factor for each row of the product
     int cols, width;       // width: of a tile
     int vec;               // rows allow 16-byte stores
   };
@@ -264,6 +265,7 @@ struct OutJob {
       out = -1;
       if (a.place != nullptr) {
         if (i < *a.live) out = a.place[i];
+        if (out >= 0 && a.down != nullptr) alpha *= a.down[i];
       } else if (i < a.rows) {
         out = static_cast<int>(i);
       }
@@ -376,6 +378,12 @@ struct CopyArgs {
   int64_t tokens, rows, hidden_stride, weight_stride, dhidden_stride;
   int dim, dim_pad;
   int at_once;             // the CTA that selects gathers the rows too
+  // fp16 with a coefficient for each token; NULL otherwise
+  const float* meta;       // {.., .., largest coefficient}
+  float* coef;             // of the selected tokens: times 2^e
+  float* down;             // 2^-e
+  uint16_t* hidden_low;    // hidden_copy with each row times 2^-e
+  int rows_log;            // ceil(log2(rows))
 };
 
 // 8 elements of a row from column c on, zeros past its end.
@@ -411,8 +419,60 @@ __device__ __forceinline__ void copy_rows(uint16_t* dst, const uint16_t* src, in
   }
 }
 
-// The selected tokens' rows by n threads of which this is number t; place and row are written.
-__device__ __forceinline__ void gather_rows(const CopyArgs& a, int live, int64_t t, int64_t n) {
+// dz = c (p - onehot) has one factor for all tokens, which takes the largest |c| to 2^13, so that of a token whose c is 2^-k of it
+// fp16 keeps all bits of probabilities down to 2^(k - 27) alone and nothing below 2^(k - 38): with 131072 classes a token of 10^-4
+// would keep one or two levels of its p, and one of 10^-6 the term of its target only.  So tokens of a small c have a power of
+// two of their own, 2^e: dz is that much larger, dhidden's row is divided by it again, and dweight's product takes hidden's row
+// divided by it.  e = k + log2(rows) - 24 keeps all bits of p from 1 / (8 rows) on, is no more than k (dz stays below 2^14),
+// and no more than takes the row's largest element to 2^-10: hidden's smaller ones lose what lies below 2^-25, 2^-15 of the
+// largest.  A warp to a row.  (bf16 has fp32's range; e = 0 where all coefficients are alike, as a mean's.)
+constexpr int kTopBits = 24, kLowestRow = -10, kMostUp = 25;
+__device__ __forceinline__ void scale_rows(const CopyArgs& a, int live, float size, int64_t t, int64_t n) {
+  const int lane = lane_id(), groups = a.dim_pad / 8;
+  const bool vec = reinterpret_cast<uintptr_t>(a.hidden) % 16 == 0 && a.dim % 8 == 0 && a.hidden_stride % 8 == 0;
+  for (int64_t r = t / kWarp; r < filled(live); r += n / kWarp) {
+    uint16_t* dst = a.hidden_low + r * a.dim_pad;
+    if (r >= live) {
+      for (int g = lane; g < groups; g += kWarp) *reinterpret_cast<uint4*>(dst + g * 8) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint16_t* src = a.hidden + a.place[r] * a.hidden_stride;
+    const float c = a.coef[r];
+    int e = 0;
+    if (c != 0.0f && fabsf(c) <= size) {  // and finite: size is
+      const int k = ilogbf(size) - ilogbf(c);
+      e = min(k, k + a.rows_log - kTopBits);
+    }
+    if (e > 0) {
+      float top = 0.0f;
+      for (int i = lane; i < a.dim; i += kWarp) top = fmaxf(top, fabsf(__half2float(__ushort_as_half(src[i]))));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      if (top > 0.0f && top < INFINITY) e = min(e, ilogbf(top) - kLowestRow);
+      e = max(min(e, kMostUp), 0);
+    } else {
+      e = 0;
+    }
+    const float low = ldexpf(1.0f, -e);
+    for (int g = lane; g < groups; g += kWarp) {
+      uint4 v = row_piece(src, g * 8, a.dim, vec);
+      if (e > 0) {
+        Pack<__half, 8>& p = reinterpret_cast<Pack<__half, 8>&>(v);
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = p.get(k) * low;
+        p.set(f);
+      }
+      *reinterpret_cast<uint4*>(dst + g * 8) = v;
+    }
+    __syncwarp();  // all lanes have read coef
+    if (lane == 0) a.coef[r] = c * ldexpf(1.0f, e), a.down[r] = low;
+  }
+}
+
+// The selected tokens' rows by n threads of which this is number t; place and row are written.  size: the largest coefficient.
+__device__ __forceinline__ void gather_rows(const CopyArgs& a, int live, float size, int64_t t, int64_t n) {
+  if (a.hidden_low != nullptr) scale_rows(a, live, size, t, n);
   copy_rows(a.hidden_copy, a.hidden, filled(live), a.hidden_stride, a.dim, a.dim_pad, t, n,
             [&](int64_t r) { return r < live ? static_cast<int64_t>(a.place[r]) : int64_t(-1); });
   if (a.dhidden == nullptr || live == a.tokens) return;
@@ -436,7 +496,7 @@ struct SelectArgs {
   const float* dloss;
   const float* mean;
   float scale;
-  float* meta;       // {factor of dz, scale over it}
+  float* meta;       // {factor of dz, scale over it, the coefficient that the factor is made for}
   float* coef;       // [selected]
   float* lse2;       // [selected] lse in powers of 2
   unsigned long long* stats;
@@ -512,13 +572,10 @@ __global__ void __launch_bounds__(kSelectThreads) loss_select_kernel(const __gri
     if (BACKWARD) a.coef[j] = 0.0f, a.lse2[j] = 0.0f;
   }
   if (threadIdx.x == 0) *a.live = base;
-  if (c.at_once) {
-    __syncthreads();
-    gather_rows(c, base, threadIdx.x, kSelectThreads);
-  }
+  float size = 0.0f;
   if constexpr (BACKWARD) {
     // The largest finite coefficient takes dz to 2^13: |p - onehot| is at most 1, fp16 ends at 2^16, and what is 2^-27 of the
-    // largest is still a normal number there.  Not a power of two: the terms of the targets, 1 - p of their coefficient, are what
+    // largest is still a normal number there (of tokens whose coefficients are far smaller, see scale_rows).  Not a power of two: the terms of the targets, 1 - p of their coefficient, are what
     // most of the gradients is, and where all coefficients are the same (a mean's) they would all be rounded the same way.
     // So scaled they are 2^13 (1 - p).  (8192 x 131072 x 1024 bf16, 2-norm against 64 bits: 0.0029 by a power of two, 0.0017
     // so, which is the rounding of the gradients themselves.)
@@ -526,15 +583,19 @@ __global__ void __launch_bounds__(kSelectThreads) loss_select_kernel(const __gri
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
     if (lane == 0) s_top[w] = top;
     __syncthreads();
-    if (w != 0) return;
     top = s_top[lane];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    if (lane == 0) {
-      const float size = top > 0.0f ? fmaxf(top, 0x1p-100f) : 8192.0f;
+    size = top > 0.0f ? fmaxf(top, 0x1p-100f) : 8192.0f;
+    if (threadIdx.x == 0) {
       a.meta[0] = 8192.0f / size;
       a.meta[1] = a.scale * (size / 8192.0f);
+      a.meta[2] = size;
     }
+  }
+  if (c.at_once) {
+    __syncthreads();
+    gather_rows(c, base, size, threadIdx.x, kSelectThreads);
   }
 }
 
@@ -544,7 +605,7 @@ __global__ void __launch_bounds__(kCopyThreads) loss_copy_kernel(const __grid_co
   wait_before();
   if (a.weight_copy != nullptr)
     copy_rows(a.weight_copy, a.weight, a.rows, a.weight_stride, a.dim, a.dim_pad, t, n, [](int64_t r) { return r; });
-  if (a.live != nullptr) gather_rows(a, *a.live, t, n);
+  if (a.live != nullptr) gather_rows(a, *a.live, a.meta != nullptr ? a.meta[2] : 0.0f, t, n);
   else copy_rows(a.hidden_copy, a.hidden, a.tokens, a.hidden_stride, a.dim, a.dim_pad, t, n, [](int64_t r) { return r; });
 }
 
@@ -655,6 +716,7 @@ struct FinishArgs {
   const int* live;         // NULL: all rows
   const int* live_k;       // NULL, or the length of the sums, of whose blocks there may be fewer than splits
   const int* place;
+  const float* down;       // NULL, or another factor for each selected row
   T* out;
   int64_t rows, sums_stride, stride;
   int splits, cols, vec;
@@ -679,7 +741,7 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant_
       f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w, f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] *= alpha;
+    for (int k = 0; k < 8; ++k) f[k] *= a.down != nullptr ? alpha * a.down[i] : alpha;
     Pack<T, 8> p;
     p.set(f);
     T* dst = a.out + to * a.stride + col;
@@ -711,18 +773,20 @@ tbe_status launch_product(const typename P::Args& p, const LossArgs& a, const De
 tbe_status launch_copy(const CopyArgs& p, const DeviceInfo& dev, cudaStream_t s) {
   const int64_t rows = p.tokens + (p.weight_copy != nullptr ? p.rows : 0);
   int64_t blocks = ceil_div(rows * (p.dim_pad / 8), 2 * kCopyThreads);
+  if (p.hidden_low != nullptr && blocks < ceil_div(p.tokens, kCopyThreads / kWarp)) blocks = ceil_div(p.tokens, kCopyThreads / kWarp);
   if (blocks > dev.sms * 8) blocks = dev.sms * 8;
   return cuda_status(launch_after(loss_copy_kernel, static_cast<unsigned>(blocks), kCopyThreads, 0, s, p));
 }
 
-// Elements of hidden up to which the CTA that selects gathers them as well: 16 to a thread, which takes less than a launch.
+// Elements of hidden up to which the CTA that selects gathers them as well: 16 to a thread (and 4 rows to a warp where rows have a factor
+// of their own), which takes less than a launch.
 constexpr int64_t kAtOnce = 16 * kSelectThreads;
 
 // Selects the tokens and gathers their rows.  The table's copy, where c has one, is made beside the selection.
 template <bool BACKWARD>
 tbe_status launch_select(const SelectArgs& p, CopyArgs& c, const DeviceInfo& dev, cudaStream_t s) {
   c.live = p.live, c.place = p.place, c.row = p.row;
-  c.at_once = c.tokens * c.dim_pad <= kAtOnce;
+  c.at_once = c.tokens * c.dim_pad <= kAtOnce && (c.hidden_low == nullptr || c.tokens <= 4 * (kSelectThreads / kWarp));
   int64_t blocks = c.weight_copy == nullptr ? 0 : ceil_div(c.rows * (c.dim_pad / 8), 2 * kSelectThreads);
   if (blocks > dev.sms * 2 - 1) blocks = dev.sms * 2 - 1;
   loss_select_kernel<BACKWARD><<<static_cast<unsigned>(1 + blocks), kSelectThreads, 0, s>>>(p, c);
@@ -770,8 +834,8 @@ int even_width(int64_t rows, int workers) {
 int gradient_width(int dim) { return static_cast<int>(round_up(ceil_div(dim, ceil_div(dim, 256)), 32)); }
 
 template <typename T>
-tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, void* dhidden, void* dweight, char* ws,
-                         const DeviceInfo& dev, cudaStream_t s) {
+tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const CUtensorMap* maps, const float* down, void* dhidden,
+                         void* dweight, char* ws, const DeviceInfo& dev, cudaStream_t s) {
   const bool bf16 = a.dtype == TBE_BF16;
   const int N = static_cast<int>(a.tokens), m_tiles = static_cast<int>(ceil_div(N, kPairM));
   const int width = gradient_width(a.dim);
@@ -801,12 +865,12 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
     typename Out::Args oa{maps[4], maps[5],
                           PairShape{v_tiles, d_tiles, 1, static_cast<int>(ceil_div(N, kPairK)), 0, 0, 0, 0, width, 1, pair_idesc(bf16, width, true, true),
                                     nullptr, live, static_cast<int>(l.dz_rows)},
-                          {meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, nullptr, nullptr, a.dim, width,
+                          {meta, static_cast<T*>(dweight), a.dweight_stride, first, a.rows, nullptr, nullptr, nullptr, a.dim, width,
                            whole_stores(dweight, a.dweight_stride)}};
     const int64_t items = static_cast<int64_t>(sum.items()) + oa.g.items();
     if (l.direct) {
       typename Direct::Args da{maps[2], maps[3], sum,
-                               {meta, static_cast<T*>(dhidden), a.dhidden_stride, 0, a.tokens, placed, live, a.dim, width,
+                               {meta, static_cast<T*>(dhidden), a.dhidden_stride, 0, a.tokens, placed, live, down, a.dim, width,
                                 whole_stores(dhidden, a.dhidden_stride)}};
       if ((st = launch_pair<128, 2, Direct, Out>(da, oa, items, a, dev, s)) != TBE_OK) return st;
       continue;
@@ -823,7 +887,7 @@ tbe_status loss_backward(const LossArgs& a, const LossBackwardLayout& l, const C
   }
   if (l.direct) return TBE_OK;
   auto finish = [&](const float* from, const int* selected, void* out, int64_t rows, int64_t stride, int splits) {
-    const FinishArgs<T> fa{from, meta, selected, selected != nullptr ? nullptr : live, placed, static_cast<T*>(out), rows, l.dim_pad, stride, splits, a.dim, whole_stores(out, stride)};
+    const FinishArgs<T> fa{from, meta, selected, selected != nullptr ? nullptr : live, placed, selected != nullptr ? down : nullptr, static_cast<T*>(out), rows, l.dim_pad, stride, splits, a.dim, whole_stores(out, stride)};
     int64_t blocks = ceil_div(rows * (l.dim_pad / 8), 256);
     if (blocks > dev.sms * 8) blocks = dev.sms * 8;
     return cuda_status(launch_after(loss_finish_kernel<T>, static_cast<unsigned>(blocks), 256, 0, s, fa));
@@ -904,8 +968,10 @@ LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev
   l.target = place(&at, l.dz_rows * 4);
   l.row = place(&at, a.tokens * 4);
   l.coef = place(&at, l.dz_rows * 4);
+  l.down = place(&at, l.dz_rows * 4);
   l.lse2 = place(&at, l.dz_rows * 4);
   l.hidden = place(&at, l.dz_rows * l.dim_pad * 2);
+  l.hidden_low = place(&at, a.dtype == TBE_F16 ? l.dz_rows * l.dim_pad * 2 : 0);
   l.weight = place(&at, a.copy_weight ? a.rows * l.dim_pad * 2 : 0);
   // What these two take varies with the number of tokens both ways: as much as any smaller number may need, so that a
   // workspace for the largest call serves every call.
@@ -997,19 +1063,26 @@ tbe_status launch_loss_backward(const LossArgs& a, const LossBackwardLayout& l, 
   c.dhidden = static_cast<uint16_t*>(dhidden);
   c.tokens = a.tokens, c.rows = a.rows, c.hidden_stride = a.hidden_stride, c.weight_stride = a.weight_stride;
   c.dhidden_stride = a.dhidden_stride, c.dim = a.dim, c.dim_pad = static_cast<int>(l.dim_pad);
+  const bool scaled = !bf16 && dloss != nullptr;
+  if (scaled) {
+    c.meta = p.meta, c.coef = p.coef, c.down = reinterpret_cast<float*>(ws + l.down);
+    c.hidden_low = reinterpret_cast<uint16_t*>(ws + l.hidden_low);
+    while (int64_t(1) << c.rows_log < a.rows) ++c.rows_log;
+  }
   const tbe_status st = launch_select<true>(p, c, dev, s);
   if (st != TBE_OK) return st;
   const void* h = ws + l.hidden;
+  const void* low = scaled ? ws + l.hidden_low : h;
   const int64_t wst = a.copy_weight ? l.dim_pad : a.weight_stride;
   if (a.copy_weight) weight = ws + l.weight;
   const void* dz = ws + l.dz;
   CUtensorMap maps[6];
   if (!encode_operand(&maps[0], h, bf16, a.dim, a.tokens, l.dim_pad, 128) || !encode_operand(&maps[1], weight, bf16, a.dim, a.rows, wst, 128) ||
       !encode_operand(&maps[2], dz, bf16, 64, l.piece / 64 * l.dz_rows, 64, 128) || !encode_operand(&maps[3], weight, bf16, a.dim, a.rows, wst, 64) ||
-      !encode_operand(&maps[4], dz, bf16, 64, l.piece / 64 * l.dz_rows, 64, 64) || !encode_operand(&maps[5], h, bf16, a.dim, a.tokens, l.dim_pad, 64))
+      !encode_operand(&maps[4], dz, bf16, 64, l.piece / 64 * l.dz_rows, 64, 64) || !encode_operand(&maps[5], low, bf16, a.dim, a.tokens, l.dim_pad, 64))
     return cuda_status(cudaErrorInvalidValue);
-  if (bf16) return loss_backward<__nv_bfloat16>(a, l, maps, dhidden, dweight, ws, dev, s);
-  return loss_backward<__half>(a, l, maps, dhidden, dweight, ws, dev, s);
+  if (bf16) return loss_backward<__nv_bfloat16>(a, l, maps, nullptr, dhidden, dweight, ws, dev, s);
+  return loss_backward<__half>(a, l, maps, c.down, dhidden, dweight, ws, dev, s);
 }
 
 }  // namespace tbe

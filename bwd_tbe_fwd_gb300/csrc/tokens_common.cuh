@@ -36,7 +36,7 @@ struct LossBackwardLayout {
   int splits;                      // parts of the long sums of dhidden
   int out_splits;                  // parts of the sums of dweight
   bool direct;                     // it is written as it is: one piece, one split
-  size_t meta, live, place, target, row, coef, lse2, hidden, weight, dz, sums, out_sums, total;
+  size_t meta, live, place, target, row, coef, down, lse2, hidden, hidden_low, weight, dz, sums, out_sums, total;
 };
 LossForwardLayout loss_forward_layout(const LossArgs& a);
 LossBackwardLayout loss_backward_layout(const LossArgs& a, const DeviceInfo& dev);

@@ -71,8 +71,10 @@ tbe_status tbe_lookup_backward(const tbe_lookup_problem* prob, const void* dout,
  *   dz[i][v] = c[i] * (exp(z[i][v] - lse[i]) - [v = targets[i]]),
  *   dhidden = scale * dz weight,  dweight = scale * dz^T hidden.
  * The logits are never kept: the forward holds them a tile at a time, the backward takes a piece of the table's rows
- * at a time, of which dz is held in 16 bits (type dtype, scaled by a factor that the largest c[i] gives, so that
- * nothing of it is lost below fp16's range).  Products are of 16-bit operands, summed in fp32.
+ * at a time, of which dz is held in 16 bits (type dtype, scaled by a factor that the largest |c[i]| gives).  In fp16 a
+ * token of a smaller |c[i]| has a power of two of its own: its probabilities from 1 / (8 rows) on keep all bits that
+ * the type has where |c[i]| >= 2^-34 rows / (its hidden row's largest element) of the largest; what is smaller than
+ * that product loses its last bits first.  bf16 has fp32's range.  Products are of 16-bit operands, summed in fp32.
  * Limits: 1 <= rows < 2^31 - 2^16, 1 <= dim <= 65536, tokens <= 2^24, tokens * rows <= 2^45; dtype TBE_F16 or
  * TBE_BF16; TBE_ERR_UNSUPPORTED beyond.  weight: 16-byte aligned where its stride is a multiple of 8; the other
  * buffers, and weight otherwise, are aligned to their element.

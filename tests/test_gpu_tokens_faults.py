@@ -1,9 +1,11 @@
 """The token side (include/tbe_tokens.h) where it once went wrong, or where no test had looked."""
+import numpy as np
 import pytest
 import torch
 
+import tokens_reference as ref
 from bwd_tbe_fwd_gb300 import SoftmaxLoss
-from test_gpu_tokens import check_loss, loss_inputs
+from test_gpu_tokens import check_loss, gen, host, loss_inputs, within
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +31,57 @@ def test_products_one_after_the_other():
         want = want or got
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert not op.stats.any()
+
+
+# ------------------------------------------------------------------------------------------
+# Coefficients of different sizes in fp16
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("tokens,rows,dim", [(48, 131072, 16), (100, 1500, 24), (600, 20011, 37), (1500, 900, 64)])
+def test_fp16_gradients_of_coefficients_of_different_sizes(tokens, rows, dim):
+    """Coefficients from 1 down to 10^-6, dhidden row by row against the row's own size.  The table's rows have a common part, so
+    that the probabilities' sum counts.  What dz loses to fp16's least values is, at a coefficient c, no more than 2^-13 c / rows
+    an entry: 2^-25 where the largest coefficient is 2^13 and c = 2^-k of it has a factor 2^e, e >= k + log2(rows) - 24.  That
+    holds where hidden's rows reach 2^(k + log2(rows) - 34): 8 for k = 20 and 2^17 rows.  dweight's product takes hidden's
+    rows to 2^-15 of their largest element."""
+    g = gen(rows)
+    h = torch.randn(tokens, dim, generator=g).clamp(-7, 7)
+    h[:, 0] = 8
+    w = torch.randn(rows, dim, generator=g) * 0.05 + 0.25
+    h, w = h.half().cuda(), w.half().cuda()
+    t = torch.randint(0, rows, (tokens,), generator=g).cuda()
+    t[5] = -1
+    c = 2.0 ** 10 * 10.0 ** (-6 * torch.rand(tokens, generator=g).sort().values)
+    c[::3] *= -1
+    c[0], c[-1], c[7] = 2.0 ** 10, 2.0 ** 10 * 1e-6, 0
+    op = SoftmaxLoss(rows, dim, tokens, dtype=torch.float16)
+    lse = op.forward(h, w, t)[1]
+    dh, dw = op.backward(h, w, t, lse, dloss=c.cuda())
+    hh, wh, th, lh, ch = host(h), host(w), t.cpu().numpy(), host(lse), host(c)
+    for i in range(tokens):
+        one = slice(i, i + 1)
+        (want, _), (bound, _) = ref.loss_gradients(hh[one], wh, th[one], lh[one], ch[one], 1.0, "f16")
+        within(dh[one], want, bound + (th[i] >= 0) * abs(ch[i]) * 2.0 ** -13 * np.abs(wh).mean(0), f"dhidden {i}")
+    (_, want), (_, bound) = ref.loss_gradients(hh, wh, th, lh, ch, 1.0, "f16")
+    z, _ = ref.logits(hh, wh, 1.0)
+    dz = np.exp(z - lh[:, None])
+    dz[np.arange(tokens), np.maximum(th, 0)] -= 1
+    low = np.abs(np.where(th >= 0, ch, 0.0)[:, None] * dz).T @ np.broadcast_to(2.0 ** -15 * np.abs(hh).max(1, keepdims=True), hh.shape)
+    within(dw, want, bound + low, "dweight")
+    again = op.backward(h, w, t, lse, dloss=c.cuda())
+    assert torch.equal(again[0], dh) and torch.equal(again[1], dw)
+    assert not op.stats.any()
+
+
+def test_fp16_coefficients_that_are_not_finite():
+    """They spoil their own token's gradient, and with it the table's; the other tokens' rows are as without them."""
+    h, w, t, _ = loss_inputs(60, 200, 32, "f16", ids="full", seed=2)
+    op = SoftmaxLoss(200, 32, 60, dtype=torch.float16)
+    lse = op.forward(h, w, t)[1]
+    c = torch.full((60,), 1e-5, device="cuda")
+    c[1] = 1.0
+    want = op.backward(h, w, t, lse, dloss=c)[0].clone()
+    c[10], c[20] = float("inf"), float("nan")
+    got = op.backward(h, w, t, lse, dloss=c)[0]
+    keep = torch.ones(60, dtype=torch.bool, device="cuda")
+    keep[10] = keep[20] = False
+    assert torch.equal(got[keep], want[keep]) and not bool(torch.isfinite(got[~keep]).any())
