@@ -85,3 +85,22 @@ def test_fp16_coefficients_that_are_not_finite():
     keep = torch.ones(60, dtype=torch.bool, device="cuda")
     keep[10] = keep[20] = False
     assert torch.equal(got[keep], want[keep]) and not bool(torch.isfinite(got[~keep]).any())
+
+
+# ------------------------------------------------------------------------------------------
+# Statistics that pairs of CTAs carry from tile to tile
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("tokens", [128, 129, 130, 200, 255, 256])
+def test_loss_of_one_tile_of_tokens_over_many_rows(tokens):
+    """128 tokens: single CTAs; from 129 on pairs, more tiles of 256 rows than there are pairs, each pair's statistics one part."""
+    check_loss(tokens, 30_011, 72, "bf16", ids="hot", seed=tokens)
+    check_loss(tokens, 19_457, 40, "f16", itype="i32", seed=tokens, upstream="tokens")
+
+
+def test_loss_and_its_statistics_of_256_tokens_over_70000_rows():
+    h, w, t, t_h = loss_inputs(256, 70_000, 16, "f16", seed=3)
+    op = SoftmaxLoss(70_000, 16, 256, dtype=torch.float16)
+    out = op.forward(h, w, t)
+    want, bound = ref.loss(host(h), host(w), t_h, 1.0)
+    for got, v, b, name in zip(out, want, bound, ("loss", "lse", "mean")):
+        within(got, v, b, name)
