@@ -1,5 +1,6 @@
 // k_lookup.cu -- rows of a table by token, and the table's gradient by sorted tokens (tbe_tokens.h).
 #include "cluster.cuh"
+#include "lookup_plan.cuh"
 #include "tokens_common.cuh"
 
 namespace tbe {
@@ -146,11 +147,7 @@ __global__ void __launch_bounds__(256) lookup_keys_kernel(const __grid_constant_
   stat_add(a.stats, TBE_STAT_UNREPAIRED, bad);
 }
 
-constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / kWarp;
-constexpr int kMaxCluster = 16;   // 8 where the device has no room for more
-constexpr int kMaxPerThread = 8;
-constexpr int64_t kCtaTokens = int64_t(kClusterThreads) * kMaxPerThread;
 
 struct ClusterSortArgs {
   KeyArgs k;                 // keys, vals: the sorted ones
@@ -662,10 +659,10 @@ int tokens_per_warp(const LookupArgs& a, int slabs, const DeviceInfo& dev) {
 }
 
 // How many clusters of `ctas` that sort run at once (a cluster lies within one of the GPU's processing clusters: 15 of 8 CTAs on 152
-// SMs); asked once for each device.
+// SMs); asked once for each device, and again after a question that failed.
 template <int IPT>
 int clusters_at_once(int ctas, const DeviceInfo& dev) {
-  static std::atomic<int> known[64][5];   // by device and the logarithm of the size: one more than the number, 0: not asked yet
+  static std::atomic<int> known[64][5];   // by device and the logarithm of the size: one more than the number, 0: not known
   int log = 0;
   while (1 << log < ctas) ++log;
   std::atomic<int>* slot = dev.id < 64 ? &known[dev.id][log] : nullptr;
@@ -684,41 +681,24 @@ int clusters_at_once(int ctas, const DeviceInfo& dev) {
   if (allow_smem(lookup_sort_kernel<IPT>, cluster_sort_smem(IPT), allowed, true) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, lookup_sort_kernel<IPT>, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
-    n = 0;
+    return 0;
   }
   if (slot != nullptr) slot->store(n + 1, std::memory_order_relaxed);
   return n;
 }
 
-int most_ctas(const DeviceInfo& dev) { return clusters_at_once<kMaxPerThread>(kMaxCluster, dev) > 0 ? kMaxCluster : 8; }
-
-// One cluster sorts; where there is a gradient to set to zero, others do that, as many as run beside it (each takes an equal share).
-template <int IPT>
-tbe_status launch_cluster_sort_t(const ClusterSortArgs& c, int ctas, int64_t zero, const DeviceInfo& dev, cudaStream_t s) {
-  const int clusters = clusters_at_once<IPT>(ctas, dev);
-  if (clusters < 1) return cuda_status(cudaErrorInvalidConfiguration);
-  int64_t others = 0;
-  if (zero > 0) {
-    others = ceil_div(zero, ctas) < clusters - 1 ? ceil_div(zero, ctas) : clusters - 1;
-    if (others < 1) others = 1;
-  }
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas * (1 + others)));
-  cfg.blockDim = dim3(kClusterThreads);
-  cfg.dynamicSmemBytes = cluster_sort_smem(IPT);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, lookup_sort_kernel<IPT>, c);
-  note_launch();
-  return cuda_status(e);
+// Calls f with the number of tokens to a thread.
+template <typename F>
+auto with_per_thread(int per_thread, F&& f) {
+  if (per_thread <= 1) return f(std::integral_constant<int, 1>());
+  if (per_thread <= 2) return f(std::integral_constant<int, 2>());
+  if (per_thread <= 4) return f(std::integral_constant<int, 4>());
+  return f(std::integral_constant<int, kMaxPerThread>());
 }
 
-tbe_status launch_cluster_sort(const LookupArgs& a, const KeyArgs& k, void* grad, int64_t row_bytes, int64_t pitch,
-                               const DeviceInfo& dev, cudaStream_t s) {
+// One cluster sorts; where there is a gradient to set to zero, others do that, as many as run beside it (each takes an equal share).
+tbe_status launch_cluster_sort(const LookupArgs& a, const SortPlan& plan, const KeyArgs& k, void* grad, int64_t row_bytes, int64_t pitch,
+                               cudaStream_t s) {
   ClusterSortArgs c{k, 0, {}, grad, a.rows, row_bytes, pitch, dtype_bytes(a.ttype)};
   int bits = 1;
   while (bits < 31 && (int64_t(1) << bits) <= a.rows) ++bits;  // keys 0 .. rows
@@ -727,18 +707,28 @@ tbe_status launch_cluster_sort(const LookupArgs& a, const KeyArgs& k, void* grad
     c.bits[p] = (left + c.passes - p - 1) / (c.passes - p);
     left -= c.bits[p];
   }
-  // As many CTAs as have tokens, up to 16; but 8 where there is much to set to zero, which takes longer than the sort and has more SMs
-  // beside smaller clusters (12345 tokens, 30 MB: 24.6 us a call with 8, 23.2 with 16; 65536 tokens, 268 MB: 86 and 90).
-  int ctas = 1;
-  const bool long_zeros = grad != nullptr && a.rows * row_bytes > (int64_t(64) << 20);
-  const int most = long_zeros && a.tokens <= 8 * kCtaTokens ? 8 : most_ctas(dev);
-  while (ctas < most && ctas * kClusterThreads < a.tokens) ctas *= 2;
-  const int64_t per_thread = ceil_div(a.tokens, static_cast<int64_t>(ctas) * kClusterThreads);
-  const int64_t zero = grad == nullptr ? 0 : ceil_div(a.rows * row_bytes, 2 * kZeroPiece);
-  if (per_thread <= 1) return launch_cluster_sort_t<1>(c, ctas, zero, dev, s);
-  if (per_thread <= 2) return launch_cluster_sort_t<2>(c, ctas, zero, dev, s);
-  if (per_thread <= 4) return launch_cluster_sort_t<4>(c, ctas, zero, dev, s);
-  return launch_cluster_sort_t<kMaxPerThread>(c, ctas, zero, dev, s);
+  int64_t others = 0;
+  if (grad != nullptr) {
+    others = ceil_div(ceil_div(a.rows * row_bytes, 2 * kZeroPiece), plan.ctas);
+    if (others > plan.clusters - 1) others = plan.clusters - 1;
+    if (others < 1) others = 1;
+  }
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {static_cast<unsigned>(plan.ctas), 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.ctas * (1 + others)));
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return with_per_thread(plan.per_thread, [&](auto ipt) {
+    constexpr int IPT = decltype(ipt)::value;
+    cfg.dynamicSmemBytes = cluster_sort_smem(IPT);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, lookup_sort_kernel<IPT>, c);
+    note_launch();
+    return cuda_status(e);
+  });
 }
 
 }  // namespace
@@ -768,7 +758,14 @@ tbe_status launch_lookup_backward(const LookupArgs& a, const void* dout, const v
                                   const DeviceInfo& dev, cudaStream_t s) {
   const BackwardLayout l = backward_layout(a, dev);
   const int64_t elem = dtype_bytes(a.ttype), row = a.dim * elem, pitch = a.table_stride * elem;
-  const bool in_cluster = a.tokens > 0 && a.tokens <= most_ctas(dev) * kCtaTokens;
+  SortPlan plan{0, 0, 0};
+  if (a.tokens > 0) {
+    const bool long_zeros = !accumulate && a.rows * row > (int64_t(64) << 20);
+    plan = plan_sort(a.tokens, long_zeros, [&](int ctas, int per_thread) {
+      return with_per_thread(per_thread, [&](auto ipt) { return clusters_at_once<decltype(ipt)::value>(ctas, dev); });
+    });
+  }
+  const bool in_cluster = plan.ctas > 0;
   if (!accumulate && !in_cluster) {
     const tbe_status st = cuda_status(row == pitch ? cudaMemsetAsync(grad, 0, row * a.rows, s)
                                                    : cudaMemset2DAsync(grad, pitch, 0, row, a.rows, s));
@@ -781,7 +778,7 @@ tbe_status launch_lookup_backward(const LookupArgs& a, const void* dout, const v
   const KeyArgs ka{ids, a.tokens, a.rows, a.itype, keys[0], vals[0], reinterpret_cast<uint32_t*>(ws + l.counters), a.stats};
   tbe_status st;
   if (in_cluster) {
-    st = launch_cluster_sort(a, ka, accumulate ? nullptr : grad, row, pitch, dev, s);
+    st = launch_cluster_sort(a, plan, ka, accumulate ? nullptr : grad, row, pitch, s);
   } else {
     int64_t blocks = ceil_div(a.tokens, 256);
     if (blocks > dev.sms * 8) blocks = dev.sms * 8;
