@@ -35,7 +35,7 @@ size_t itype_bytes(int itype) { return itype == TBE_I32 ? 4 : 8; }
 tbe_status make_loss(const tbe_softmax_problem* p, int64_t* stats, bool backward, LossArgs* a) {
   if (p == nullptr || p->tokens < 0 || p->rows < 1 || p->dim < 1) return TBE_ERR_INVALID_ARG;
   if (p->tokens > kMaxLossTokens || p->rows >= kMaxIndices || p->dim > kMaxDim) return TBE_ERR_UNSUPPORTED;
-  if (ceil_div(p->tokens, 256) * ceil_div(p->rows, 256) > (int64_t(1) << 30)) return TBE_ERR_UNSUPPORTED;  // tiles
+  if (p->tokens > (int64_t(1) << 45) / p->rows) return TBE_ERR_UNSUPPORTED;  // tiles of 256 x 256: below 2^30
   if ((p->dtype != TBE_F16 && p->dtype != TBE_BF16) || (p->itype != TBE_I32 && p->itype != TBE_I64)) return TBE_ERR_UNSUPPORTED;
   if (!(p->scale > 0) || std::isinf(p->scale)) return TBE_ERR_INVALID_ARG;
   if (p->hidden_stride < p->dim || p->weight_stride < p->dim) return TBE_ERR_INVALID_ARG;
