@@ -2,9 +2,9 @@
 //
 // Forward: z = scale * hidden weight^T a 256 x 256 tile at a time on the tensor cores (pair_mma.cuh); the epilogue reduces
 // a tile's row to its maximum and sum of exponentials (in powers of 2), and picks the target's logit when its column
-// comes by; a second kernel joins a row's parts.  Backward: for a piece of the table's rows at a time, the logits again,
-// whose epilogue makes dz = c (p - onehot) in 16 bits, then dhidden += dz weight (summed over the pieces in fp32)
-// and dweight = dz^T hidden, which is complete for the piece's rows.
+// comes by; a second kernel joins a row's parts (of a piece of the table's rows at a time where there are many).  Backward: for a
+// piece of the table's rows at a time, the logits again, whose epilogue makes dz = c (p - onehot) in 16 bits, then
+// dhidden += dz weight (summed over the pieces in fp32) and dweight = dz^T hidden, which is complete for the piece's rows.
 #include <cfloat>
 
 #include "pair_mma.cuh"
@@ -99,6 +99,7 @@ struct StatsJob {
     float* target_logit;   // [tokens]
     uint32_t* ticket;      // set to 0 for the kernel that joins the parts
     int64_t parts_rows, rows;
+    int64_t first, end;    // the piece's rows of the table
     int tokens, itype;
     int carry;             // one tile of rows: a thread's parts are joined from tile to tile, one for each pair (or single CTA)
     int width;             // columns of a tile
@@ -123,10 +124,10 @@ struct StatsJob {
   static __device__ __forceinline__ void tile(const Args& a, const Row& r, State& s, const PairItem& it, int row, int half, uint32_t tmem,
                                               uint32_t, R&& release) {
     const int i = it.m * kPairM + row;
-    const int64_t col0 = static_cast<int64_t>(it.n) * a.width + half * 128;
+    const int64_t col0 = a.first + static_cast<int64_t>(it.n) * a.width + half * 128;
     if (it.m == 0 && it.n == 0 && row == 0 && half == 0) *a.ticket = 0;
     const int most = min(128, a.width - half * 128);         // columns of this half, which may have none
-    const int live = static_cast<int>(a.rows - col0 < most ? a.rows - col0 : most);
+    const int live = static_cast<int>(a.end - col0 < most ? a.end - col0 : most);
     const int64_t tl = r.target < 0 || r.target - col0 >= live ? -1 : r.target - col0;  // the target's column of this half
     float top = s.top, sum = s.sum;
     each_columns<128>(tmem, release, [&](int j, pair::Columns& c) {
@@ -609,16 +610,62 @@ __global__ void __launch_bounds__(kCopyThreads) loss_copy_kernel(const __grid_co
   else copy_rows(a.hidden_copy, a.hidden, a.tokens, a.hidden_stride, a.dim, a.dim_pad, t, n, [](int64_t r) { return r; });
 }
 
-// Joins the parts of 32 tokens' rows, a lane to a token, the parts dealt out to the warps; the last block adds up the losses.  (8192 tokens
-// of 1024 parts: 22 us, 67 MB; 16 of 304: 7, latency.)
+// Joins the parts of 32 tokens' rows, a lane to a token, the parts dealt out to the warps.
 constexpr int kJoinThreads = 1024;
+
+struct PartArgs {
+  float2* part;            // [..][rows]: a token's parts, and behind them (number `before`) those of earlier pieces, joined
+  int64_t rows;
+  int parts, before;       // before: -1 for the first piece
+};
+
+// {maximum, sum of exponentials} of token j of this lane, in the first warp's threads; all of the block's call it.
+__device__ __forceinline__ float2 join_parts(const PartArgs& a, int64_t j, bool counts) {
+  constexpr int kWarps = kJoinThreads / kWarp;
+  __shared__ float2 s_part[kWarps][kWarp + 1];
+  const int lane = lane_id(), w = threadIdx.x / kWarp;
+  float top = -INFINITY, sum = 0.0f;
+  auto add = [&](const float2& v) {
+    const float next = fmaxf(top, v.x), ref = next == -INFINITY ? 0.0f : next;
+    sum = sum * exp2_fast(top - ref) + v.y * exp2_fast(v.x - ref);
+    top = next;
+  };
+  if (counts) {
+#pragma unroll 8
+    for (int p = w; p < a.parts; p += kWarps) add(a.part[p * a.rows + j]);
+    if (a.before >= 0 && w == 0) add(a.part[a.before * a.rows + j]);
+  }
+  s_part[w][lane] = make_float2(top, sum);
+  __syncthreads();
+  if (w != 0) return make_float2(0.0f, 0.0f);
+  top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_part[k][lane].x);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float s4[4] = {};
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) s4[k % 4] += s_part[k][lane].y * exp2_fast(s_part[k][lane].x - ref);
+  return make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+}
+
+// Between two pieces of the table: a token's parts to the one behind them.
+__global__ void __launch_bounds__(kJoinThreads) loss_fold_kernel(const __grid_constant__ PartArgs a, const int* live, int64_t tokens, int to) {
+  wait_before();
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * kWarp + lane_id();
+  const bool counts = j < (live != nullptr ? *live : tokens);
+  const float2 v = join_parts(a, j, counts);
+  if (threadIdx.x < kWarp && counts) a.part[to * a.rows + j] = v;
+}
+
+// A token's loss from all of its parts; the last block adds up the losses.  (8192 tokens of 1024 parts: 22 us, 67 MB; 16 of 304: 7,
+// latency.)
 struct BlockSum {
   double loss;
   long long count;
 };
 
 struct JoinArgs {
-  const float2* part;
+  PartArgs parts;
   const float* target_logit;
   const void* targets;
   const int* row;          // NULL, or where a token is among the selected
@@ -627,8 +674,8 @@ struct JoinArgs {
   float* mean;
   BlockSum* sums;
   uint32_t* ticket;
-  int64_t tokens, rows, parts_rows;
-  int parts, itype;
+  int64_t tokens, rows;
+  int itype;
   unsigned long long* stats;
 };
 
@@ -639,7 +686,6 @@ __device__ __forceinline__ void write_mean(float* mean, double d, long long n) {
 
 __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_constant__ JoinArgs a) {
   constexpr int kWarps = kJoinThreads / kWarp;
-  __shared__ float2 s_part[kWarps][kWarp + 1];
   __shared__ double s_loss[kWarps];
   __shared__ long long s_count[kWarps];
   __shared__ bool s_last;
@@ -650,27 +696,9 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_co
   const bool counts = raw >= 0 && raw < a.rows;
   const int64_t j = !counts ? 0 : a.row != nullptr ? a.row[i] : i;
   const float logit = w == 0 && counts ? a.target_logit[j] : 0.0f;
-  float top = -INFINITY, sum = 0.0f;
-  if (counts) {
-#pragma unroll 8
-    for (int p = w; p < a.parts; p += kWarps) {
-      const float2 v = a.part[p * a.parts_rows + j];
-      const float next = fmaxf(top, v.x), ref = next == -INFINITY ? 0.0f : next;
-      sum = sum * exp2_fast(top - ref) + v.y * exp2_fast(v.x - ref);
-      top = next;
-    }
-  }
-  s_part[w][lane] = make_float2(top, sum);
-  __syncthreads();
+  const float2 all = join_parts(a.parts, j, counts);
   if (w == 0) {
-    top = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_part[k][lane].x);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float s4[4] = {};
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) s4[k % 4] += s_part[k][lane].y * exp2_fast(s_part[k][lane].x - ref);
-    const float lse = counts ? (ref + log2f((s4[0] + s4[1]) + (s4[2] + s4[3]))) * kLn2 : 0.0f;
+    const float lse = counts ? ((all.x == -INFINITY ? 0.0f : all.x) + log2f(all.y)) * kLn2 : 0.0f;
     const float loss = counts ? lse - logit : 0.0f;
     if (i < a.tokens) a.lse[i] = lse, a.loss[i] = loss;
     const unsigned bad = __ballot_sync(kFull, raw >= a.rows);
@@ -805,6 +833,10 @@ size_t place(size_t* at, int64_t bytes) {
 // Rows that allow 16-byte stores.
 int whole_stores(const void* p, int64_t stride) { return stride % 8 == 0 && is_aligned(p, 16); }
 
+// Bytes of the softmax's parts that a piece of the table may take in the forward, 8 for each token and 128 rows: up to 2^32 logits are
+// one piece.  (131072 x 131072 would take 1 GB in one, where the logits are not to be kept.)
+constexpr int64_t kPartBytes = int64_t(256) << 20;
+
 // Bytes of dz that a piece of the table may take.
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
 
@@ -915,9 +947,15 @@ LossForwardLayout loss_forward_layout(const LossArgs& a) {
   LossForwardLayout l{};
   size_t at = 0;
   const int64_t dim_pad = round_up(a.dim, 8);
-  l.parts = static_cast<int>(2 * ceil_div(a.rows, 256));  // two to a tile; fewer are used where the pairs join theirs
-  l.parts_rows = round_up(a.tokens, 32);
-  l.part = place(&at, l.parts * l.parts_rows * 8);
+  l.parts_rows = round_up(a.tokens > 0 ? a.tokens : 1, 32);
+  int64_t most = kPartBytes / 16 / l.parts_rows;   // tiles of 256 rows, two parts to each; fewer are used where the pairs join theirs
+  if (most < 1) most = 1;
+  const int64_t tiles = ceil_div(a.rows, 256);
+  l.piece = ceil_div(tiles, ceil_div(tiles, most)) * 256;
+  l.parts = static_cast<int>(l.piece / 128);
+  // As much as any smaller number of tokens may need.
+  const int64_t whole = tiles * 16 * l.parts_rows, least = 16 * l.parts_rows, capped = least > kPartBytes ? least : kPartBytes;
+  l.part = place(&at, (whole < capped ? whole : capped) + 8 * l.parts_rows);
   l.logit = place(&at, a.tokens * 4);
   l.ticket = place(&at, 256 + ceil_div(a.tokens, kWarp) * static_cast<int64_t>(sizeof(BlockSum)));  // and the blocks' sums
   l.live = place(&at, 4);
@@ -1020,27 +1058,38 @@ tbe_status launch_loss_forward(const LossArgs& a, const LossForwardLayout& l, co
   }
   const bool few = a.tokens <= kFewTokens, solo = a.tokens <= 128;
   const int m_tiles = static_cast<int>(ceil_div(a.tokens, kPairM)), workers = solo ? dev.sms : dev.sms / 2;
-  const bool carry = m_tiles == 1 && l.parts / 2 > workers;
-  const int width = carry && solo ? even_width(a.rows, workers) : 256, v_tiles = static_cast<int>(ceil_div(a.rows, width));
-  CUtensorMap ma, mb;
-  if (!encode_operand(&ma, hidden, bf16, a.dim, a.tokens, hs, few ? kFewTokens : 128) || !encode_operand(&mb, weight, bf16, a.dim, a.rows, wst, solo ? width : 128))
-    return cuda_status(cudaErrorInvalidValue);
   uint32_t* ticket = reinterpret_cast<uint32_t*>(ws + l.ticket);
   float2* part = reinterpret_cast<float2*>(ws + l.part);
   float* target_logit = reinterpret_cast<float*>(ws + l.logit);
+  CUtensorMap ma, mb;
+  if (!encode_operand(&ma, hidden, bf16, a.dim, a.tokens, hs, few ? kFewTokens : 128)) return cuda_status(cudaErrorInvalidValue);
   using Stats = Product<false, false, StatsJob>;
-  const Stats::Args sa{ma, mb,
-                       PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, 0, 0, width, 0,
-                                 pair_idesc(bf16, width, false, false, solo ? 1 : 2), select ? live : nullptr, nullptr, 0},
-                       {targets, select ? selected : nullptr, live, part, target_logit, ticket, l.parts_rows, a.rows, static_cast<int>(a.tokens), a.itype,
-                        carry, width, a.scale, a.scale * kLog2e}};
-  st = few    ? launch_product<kFewTokens, 1, Stats>(sa, a, dev, s)
-       : solo ? launch_product<128, 1, Stats>(sa, a, dev, s)
-              : launch_product<128, 2, Stats>(sa, a, dev, s);
-  if (st != TBE_OK) return st;
-  const JoinArgs ja{part, target_logit, targets, select ? row : nullptr, loss, lse, mean, reinterpret_cast<BlockSum*>(ws + l.ticket + 256), ticket,
-                    a.tokens, a.rows, l.parts_rows, carry ? 2 * workers : l.parts, a.itype, a.stats};
-  return cuda_status(launch_after(loss_join_kernel, static_cast<unsigned>(ceil_div(a.tokens, kWarp)), kJoinThreads, 0, s, ja));
+  const unsigned blocks = static_cast<unsigned>(ceil_div(a.tokens, kWarp));
+  for (int64_t first = 0; first < a.rows; first += l.piece) {
+    const int64_t here = a.rows - first < l.piece ? a.rows - first : l.piece, tiles = ceil_div(here, 256);
+    const bool carry = m_tiles == 1 && tiles > workers, last = first + here == a.rows;
+    const int width = carry && solo ? even_width(here, workers) : 256, v_tiles = static_cast<int>(ceil_div(here, width));
+    if (!encode_operand(&mb, weight, bf16, a.dim, a.rows, wst, solo ? width : 128)) return cuda_status(cudaErrorInvalidValue);
+    const Stats::Args sa{ma, mb,
+                         PairShape{m_tiles, v_tiles, 1, static_cast<int>(ceil_div(a.dim, kPairK)), 0, 0, static_cast<int>(first), 0, width, 0,
+                                   pair_idesc(bf16, width, false, false, solo ? 1 : 2), select ? live : nullptr, nullptr, 0},
+                         {targets, select ? selected : nullptr, live, part, target_logit, ticket, l.parts_rows, a.rows, first, first + here,
+                          static_cast<int>(a.tokens), a.itype, carry, width, a.scale, a.scale * kLog2e}};
+    st = few    ? launch_product<kFewTokens, 1, Stats>(sa, a, dev, s)
+         : solo ? launch_product<128, 1, Stats>(sa, a, dev, s)
+                : launch_product<128, 2, Stats>(sa, a, dev, s);
+    if (st != TBE_OK) return st;
+    const PartArgs parts{part, l.parts_rows, carry ? 2 * workers : static_cast<int>(2 * tiles), first > 0 ? l.parts : -1};
+    if (!last) {
+      st = cuda_status(launch_after(loss_fold_kernel, blocks, kJoinThreads, 0, s, parts, static_cast<const int*>(select ? live : nullptr), a.tokens, l.parts));
+      if (st != TBE_OK) return st;
+      continue;
+    }
+    const JoinArgs ja{parts, target_logit, targets, select ? row : nullptr, loss, lse, mean, reinterpret_cast<BlockSum*>(ws + l.ticket + 256), ticket,
+                      a.tokens, a.rows, a.itype, a.stats};
+    st = cuda_status(launch_after(loss_join_kernel, blocks, kJoinThreads, 0, s, ja));
+  }
+  return st;
 }
 
 tbe_status launch_loss_backward(const LossArgs& a, const LossBackwardLayout& l, const void* hidden, const void* weight,

@@ -26,7 +26,8 @@ struct LossArgs {
 // Workspace of the forward: parts of the rows' softmax statistics, copies; bytes from its start.
 struct LossForwardLayout {
   int64_t parts_rows;              // leading dimension of the parts: tokens, rounded up
-  int parts;
+  int64_t piece;                   // rows of the table at a time
+  int parts;                       // of a piece; behind them, where there are several, one for the pieces before
   size_t part, logit, ticket, live, place, target, row, hidden, weight, total;
 };
 struct LossBackwardLayout {

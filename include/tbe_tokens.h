@@ -93,8 +93,9 @@ typedef struct {
 } tbe_softmax_problem;
 
 /* loss, lse: fp32 [tokens]; mean: fp32 [2].  ws: the size that the query gives (0: a problem that is refused),
- * 256-byte aligned; it serves every call of at most as many tokens, and any hidden_stride, with the same table.  (A
- * weight_stride that is no multiple of 8 takes room for a copy of the table.) */
+ * 256-byte aligned; it serves every call of at most as many tokens, and any hidden_stride, with the same table.  It holds
+ * 8 bytes for each token and 128 rows of the table, up to 256 MB of them or 16 bytes a token, some 30 bytes a token
+ * more, a copy of hidden, and one of a table whose weight_stride is no multiple of 8. */
 size_t tbe_softmax_loss_workspace_size(const tbe_softmax_problem* prob);
 tbe_status tbe_softmax_loss_forward(const tbe_softmax_problem* prob, const void* hidden, const void* weight,
                                     const void* targets, float* loss, float* lse, float* mean, void* ws, size_t ws_bytes,

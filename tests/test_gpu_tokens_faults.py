@@ -104,3 +104,65 @@ def test_loss_and_its_statistics_of_256_tokens_over_70000_rows():
     want, bound = ref.loss(host(h), host(w), t_h, 1.0)
     for got, v, b, name in zip(out, want, bound, ("loss", "lse", "mean")):
         within(got, v, b, name)
+
+
+# ------------------------------------------------------------------------------------------
+# The forward's workspace
+# ------------------------------------------------------------------------------------------
+def sampled_loss(tokens, rows, dim, dtype, seed, check):
+    """A loss over a large table, its tokens `check` against the formula; targets at the pieces' borders and in each part."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = (torch.randn(rows, dim, generator=g, device="cuda") * 2 / dim ** 0.5).to(dtype)
+    h = torch.randn(tokens, dim, generator=g, device="cuda").to(dtype)
+    t = torch.randint(0, rows, (tokens,), generator=g, device="cuda")
+    t[1::9] = -1
+    op = SoftmaxLoss(rows, dim, tokens, dtype=dtype)
+    piece = -(-(-(-rows // 256)) // 2) * 256  # of two
+    for k, at in enumerate((0, piece - 1, piece, rows - 1)):
+        t[check[k % len(check)]] = at
+        loss, lse, mean = op.forward(h, w, t)
+        if k >= len(check) - 1:
+            want, bound = ref.loss(host(h[check]), host(w), t[check].cpu().numpy(), 1.0)
+            within(loss[check], want[0], bound[0], "loss")
+            within(lse[check], want[1], bound[1], "lse")
+    live = t >= 0
+    assert not bool(loss[~live].any()) and not bool(lse[~live].any())
+    n = int(live.sum())
+    assert float(mean[1]) == pytest.approx(1 / n, rel=1e-6)
+    assert float(mean[0]) == pytest.approx(float(loss.double().sum()) / n, rel=1e-6)
+    assert not op.stats.any()
+
+
+@pytest.mark.parametrize("tokens,rows,dim,check", [
+    (1500, 3_000_001, 8, [0, 700, 1400, 1499]),        # tokens that count are gathered; several tiles of them
+    (1_050_000, 5003, 16, [0, 255, 524_288, 1_049_999]),
+    (300, 16_000_000, 8, [0, 299]),                    # two tiles, not gathered
+])
+def test_loss_in_two_pieces(tokens, rows, dim, check):
+    """More than 2^32 logits, whose statistics are joined piece by piece."""
+    sampled_loss(tokens, rows, dim, torch.bfloat16, tokens, check)
+
+
+def test_loss_of_one_tile_of_tokens_in_two_pieces():
+    """One tile of tokens over so many rows that it takes two pieces, whose statistics pairs carry (256 tokens)."""
+    sampled_loss(256, 17_000_003, 8, torch.float16, 5, [0, 255])
+
+
+def test_loss_of_few_tokens_in_two_pieces():
+    """... and single CTAs (120)."""
+    sampled_loss(120, 34_000_003, 8, torch.bfloat16, 6, [0, 119])
+
+
+def test_a_piece_of_nothing_has_no_part_in_the_next():
+    """The first piece's logits are all -inf, the second's -200: the sum of exponentials is the second's.  Its 8.5M terms are added
+    in a chain of some 25000 additions at most, each within 2^-24; the logits and their constants lose 2^-13 at this size."""
+    rows, piece = 17_000_003, -(-(-(-17_000_003 // 256)) // 2) * 256
+    w = torch.full((rows, 8), -25.0, dtype=torch.float16, device="cuda")
+    w[:piece] = float("-inf")
+    h = torch.ones(256, 8, dtype=torch.float16, device="cuda")
+    t = torch.full((256,), rows - 1, device="cuda")
+    loss, lse, mean = SoftmaxLoss(rows, 8, 256, dtype=torch.float16).forward(h, w, t)
+    n = np.log(rows - piece)
+    err = 25000 * ref.U + 2.0 ** -13
+    assert float((loss.double() - n).abs().max()) <= err and float((lse.double() - (n - 200)).abs().max()) <= err
+    assert abs(float(mean[0]) - n) <= err

@@ -33,3 +33,18 @@ def test_the_loss_refuses_what_the_header_does():
     for n, rows in ((1 << 24, (1 << 21) + 1), ((1 << 15) + 1, 1 << 30)):
         assert lib.tbe_softmax_loss_workspace_size(problem(n, rows)) == 0
         assert lib.tbe_softmax_loss_forward(problem(n, rows), A, A, A, A, A, A, A, 1 << 50, None, None) == tbe.TBE_ERR_UNSUPPORTED
+
+
+def test_the_losss_workspace_does_not_grow_with_the_logits():
+    """What the forward keeps of the logits is 256 MB or 16 bytes a token at the most, beside a copy of hidden; more tokens
+    never take less."""
+    tbe_build.build()
+    lib = tokens._bind(tbe.load())
+    for dim in (8, 64):
+        for rows in (1000, 131072, 1 << 21, 1 << 24):
+            last = 0
+            for n in (1, 100, 256, 257, 1000, 8192, 32768, 131072, 1 << 20, 1 << 21):
+                size = lib.tbe_softmax_loss_workspace_size(
+                    ctypes.byref(tokens.SoftmaxProblem(n, rows, dim, dim, dim, dim, dim, tbe.TBE_BF16, tbe.TBE_I64, 1.0)))
+                assert last <= size <= max(256 << 20, 16 * n) + (2 * dim + 64) * (n + 256) + 4096, (dim, rows, n)
+                last = size
