@@ -1,11 +1,15 @@
 """The token side (include/tbe_tokens.h) where it once went wrong, or where no test had looked."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import tokens_reference as ref
 from bwd_tbe_fwd_gb300 import SoftmaxLoss
-from test_gpu_tokens import check_loss, gen, host, loss_inputs, within
+from test_gpu_tokens import check_lookup, check_loss, gen, host, loss_inputs, within
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +170,87 @@ def test_a_piece_of_nothing_has_no_part_in_the_next():
     err = 25000 * ref.U + 2.0 ** -13
     assert float((loss.double() - n).abs().max()) <= err and float((lse.double() - (n - 200)).abs().max()) <= err
     assert abs(float(mean[0]) - n) <= err
+
+
+# ------------------------------------------------------------------------------------------
+# Calls that the header allows and no test made
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dim", [1500, 4099, 65535, 65536])
+def test_loss_of_wide_rows(dim):
+    check_loss(70, 300, dim, "bf16", seed=dim, spread=1.0)
+    check_loss(300, 40, dim, "f16", seed=dim, spread=1.0, upstream="tokens")
+
+
+@pytest.mark.parametrize("dim,pad", [(45, 3), (301, 3), (8, 8), (1, 7)])
+def test_loss_rows_of_odd_widths_at_aligned_strides(dim, pad):
+    """Rows of which the last piece of 16 bytes is not whole, read where they lie."""
+    check_loss(90, 400, dim, "bf16", pad=pad, seed=dim)
+    check_loss(1100, 300, dim, "f16", pad=pad, seed=dim, upstream="tokens")
+
+
+@pytest.mark.parametrize("dim,table,out", [(65536, "bf16", "bf16"), (65535, "f16", "f32"), (4100, "f32", "bf16")])
+def test_lookup_of_wide_rows(dim, table, out):
+    check_lookup(90, 30, dim, table, out, ids="hot", scale=0.7, seed=dim)
+    check_lookup(700, 20, dim, table, out, accumulate=True, scale=0.7, seed=dim)
+
+
+@pytest.mark.parametrize("pad", [0, 1, 8])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_lookup_gradient_of_more_than_a_cluster_sorts_into_rows_apart(pad, accumulate):
+    check_lookup(140_001, 9000, 6, "bf16", "f32", ids="hot", itype="i32", pad=pad, accumulate=accumulate, seed=pad)
+
+
+def test_the_tables_gradients_add_up_to_nothing():
+    """The sum over the table's rows of dz is (sum of p) - 1 = 0 for every token, as far as lse is that of the logits and p
+    of both.  Each entry of dz is rounded to bf16, each row of dweight too: half a step of its size; the sums over the tokens
+    lose 2 N u of them."""
+    tokens, rows, dim = 1000, 5000, 40
+    h, w, t, t_h = loss_inputs(tokens, rows, dim, "bf16", seed=8)
+    op = SoftmaxLoss(rows, dim, tokens)
+    _, lse, mean = op.forward(h, w, t)
+    dw = host(op.backward(h, w, t, lse, mean=mean)[1])
+    live, hh = ref.masked(host(h), t_h, rows)
+    l64 = host(lse)[:, None]
+    z, ez = ref.logits(hh, host(w), 1.0)
+    p = np.exp(z - l64)
+    off = (p * (ref.exponent_error(z, l64, ez) * 1.01 + 4 * ref.U)).sum(1) + ref.loss(hh, host(w), t_h, 1.0)[1][1]  # of a token's sum
+    dz = p.copy()
+    dz[np.nonzero(live)[0], t_h[live]] -= 1
+    size = np.abs(dz[live]).T @ np.abs(hh[live])
+    bound = (size * (ref.STORE["bf16"] + 2 * tokens * ref.U)).sum(0) + off[live] @ np.abs(hh[live])
+    bound = (bound * float(mean[1]) + np.abs(dw).sum(0) * ref.STORE["bf16"]) * 1.02
+    assert (np.abs(dw.sum(0)) <= bound).all()
+
+
+CAPTURE = """
+import torch
+from bwd_tbe_fwd_gb300 import SoftmaxLoss, TokenEmbedding
+g = torch.Generator().manual_seed(1)
+w = torch.randn({rows}, 72, generator=g).to(torch.bfloat16).cuda()
+t = torch.randint(-1, {rows}, ({tokens},), generator=g).cuda()
+emb = TokenEmbedding({rows}, 72, {tokens}, table_dtype=torch.bfloat16)
+op = SoftmaxLoss({rows}, 72, {tokens})
+def step():
+    h = emb.forward(w, t)
+    loss, lse, mean = op.forward(h, w, t)
+    dh, dw = op.backward(h, w, t, lse, mean=mean)
+    return [h, loss, lse, mean, dh, emb.backward(dh, t, grad=dw, accumulate=True), emb.backward(dh, t)]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in got]
+want = step()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert not emb.stats.any() and not op.stats.any()
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("tokens,rows", [(40, 500), (3000, 4000), (140_000, 300)])
+def test_a_graph_may_hold_a_process_s_first_calls(tokens, rows):
+    """Nothing is loaded, asked or set up by a first call that a capture does not allow."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE.format(tokens=tokens, rows=rows)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout == "captured\n", r.stdout[-2000:] + r.stderr[-3000:]
