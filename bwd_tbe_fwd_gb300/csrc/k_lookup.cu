@@ -81,8 +81,9 @@ __global__ void __launch_bounds__(kFwdThreads) lookup_forward_kernel(const __gri
   stat_add(a.stats, TBE_STAT_UNREPAIRED, bad);
 }
 
-// Wide rows that allow no vector of 16 bytes: a warp to a token, so that its id is read and its row found once.  (27884 rows of 1597
-// fp32 to bf16 by single elements: 134 us by the kernel above, 28 so.)
+// Rows of 64 elements or more that allow no vector of 16 bytes: a warp to a token, so that its id is read and its row found once.  (us a
+// call by the kernel above and so: 27884 rows of 1597 fp32 to bf16 134 and 28; 50000 rows of fp16 of 129 22.8 and 14.5, of 65 14.3
+// and 12.7, of 33 12.6 and 12.7.)
 template <typename TT, typename OT, int V>
 __global__ void __launch_bounds__(kFwdThreads) lookup_rows_kernel(const __grid_constant__ ForwardArgs a) {
   constexpr int U = 4;
@@ -215,7 +216,8 @@ __device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s_wsum) {
   return x - v + (w > 0 ? y : 0);
 }
 
-// So few tokens that a thread to each counts those that come before it (32 tokens: 7.5 us by digits, 3.9 so).
+// So few tokens that a thread to each counts those that come before it.  (us a call, by digits and so: 32 tokens 10.3 and 8.7, 256 tokens
+// 12.3 and 10.5, 500 tokens 12.6 and 16.6.)
 constexpr int kRankTokens = 256;
 __device__ __forceinline__ void rank_few(const KeyArgs& a, uint32_t* s_key) {
   const int t = threadIdx.x, n = static_cast<int>(a.tokens);
@@ -760,7 +762,7 @@ tbe_status launch_lookup_backward(const LookupArgs& a, const void* dout, const v
   const int64_t elem = dtype_bytes(a.ttype), row = a.dim * elem, pitch = a.table_stride * elem;
   SortPlan plan{0, 0, 0};
   if (a.tokens > 0) {
-    const bool long_zeros = !accumulate && a.rows * row > (int64_t(64) << 20);
+    const bool long_zeros = !accumulate && zeros_are_long(a.tokens, a.rows * row);
     plan = plan_sort(a.tokens, long_zeros, [&](int ctas, int per_thread) {
       return with_per_thread(per_thread, [&](auto ipt) { return clusters_at_once<decltype(ipt)::value>(ctas, dev); });
     });

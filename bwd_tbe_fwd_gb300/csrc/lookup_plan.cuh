@@ -17,8 +17,13 @@ struct SortPlan {
   int clusters;     // how many of them run at once
 };
 
-// As many CTAs as have tokens, up to 16, or up to 8 where there is much to set to zero, which takes longer than the sort and has more
-// SMs beside smaller clusters (12345 tokens, 30 MB: 24.6 us a call with 8, 23.2 with 16; 65536 tokens, 268 MB: 86 and 90).
+// Whether the zeros of a gradient of so many bytes take longer than the sort, so that they want more SMs beside a smaller cluster: past
+// 32768 tokens, eight of which a thread of 8 CTAs has to sort, that is much later.  (us a call with 8 and with 16 CTAs, by
+// gradient: 12345 tokens 40 MB 24.8 and 24.0, 64 MB 26.9 and 27.4, 128 MB 39.2 and 41.1; 32000 tokens 64 MB 33.0 and 30.0, 96 MB
+// 35.7 and 36.9; 45000 tokens 128 MB 51.5 and 44.9, 192 MB 58.0 and 55.7; 65536 tokens 128 MB 55.2 and 51.6, 192 MB 61.7 and 64.0.)
+constexpr bool zeros_are_long(int64_t tokens, int64_t bytes) { return bytes > (int64_t(tokens > 4 * kCtaTokens ? 160 : 64) << 20); }
+
+// As many CTAs as have tokens, up to 16, or up to 8 where there is much to set to zero.
 // Others, down to a single CTA, where at_once(ctas, per_thread) says that no such cluster can run (one of 16 needs that many
 // SMs in one of the GPU's processing clusters), and none where the tokens do not fit what can.
 template <typename F>

@@ -42,6 +42,8 @@ int main() {
         for (int64_t base = 1; base <= 1 << 20; base *= 2)
           for (int64_t tokens : {base - 1, base, base + 1, base + base / 2})
             if (tokens > 0 && !check(tokens, zeros, largest, per_thread)) return 1;
+  static_assert(!tbe::zeros_are_long(1, 64 << 20) && tbe::zeros_are_long(32768, (64 << 20) + 1), "");
+  static_assert(!tbe::zeros_are_long(32769, 160 << 20) && tbe::zeros_are_long(65536, (160 << 20) + 1), "");
   std::puts("plans ok");
   return 0;
 }
