@@ -807,7 +807,8 @@ tbe_status launch_copy(const CopyArgs& p, const DeviceInfo& dev, cudaStream_t s)
 }
 
 // Elements of hidden up to which the CTA that selects gathers them as well: 16 to a thread (and 4 rows to a warp where rows have a factor
-// of their own), which takes less than a launch.
+// of their own), which takes less than a launch.  (us a gradient of 1000 rows x 64, so and by a launch: 64 tokens 24.9 and 26.6, 256
+// tokens 25.3 and 26.8, 512 tokens 28.6 and 27.6, 1024 tokens 34.6 and 29.8.)
 constexpr int64_t kAtOnce = 16 * kSelectThreads;
 
 // Selects the tokens and gathers their rows.  The table's copy, where c has one, is made beside the selection.
@@ -840,14 +841,17 @@ constexpr int64_t kPartBytes = int64_t(256) << 20;
 // Bytes of dz that a piece of the table may take.
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
 
-// The forward selects the tokens that count from here on; fewer are one to four tiles of rows, whose products take less than the
-// two launches.
+// The forward selects the tokens that count from here on, which takes two launches, 7 to 10 us, and saves their share of the products;
+// fewer are one to four tiles of rows.  (us a call, 1024 tokens, all rows and the selected ones: 131072 x 1024 186 and 151 with a third
+// of padding, 175 and 185 with 2%; 50000 x 256 36.3 and 37.4, 36.2 and 43.6; 600 tokens with a third 29.9 and 33.1.)
 constexpr int64_t kSelectTokens = 1024;
 
-// Rows of A that a CTA copies in the forward's product of at most as many tokens.
+// Rows of A that a CTA copies in the forward's product of at most as many tokens.  (16 x 131072 x 1024: 56 us by 128, 47 by 32; beyond
+// that single CTAs copy 128 up to 128 tokens, against pairs: 128 x 131072 x 1024 50.8 us and 55.4.)
 constexpr int kFewTokens = 32;
 
-// Blocks of k up to which one pair makes a whole tile of dhidden, with no sums to join after it.
+// Blocks of k up to which one pair makes a whole tile of dhidden, with no sums to join after it.  (us a gradient, so and by sums: 4096 x
+// 1536 x 1024 72 and 81, 300 x 1536 x 128 31.1 and 30.8, 300 x 2000 x 128 33.3 and 31.0, 300 x 3000 x 128 38.8 and 32.)
 constexpr int kDirectBlocks = 24;
 
 // Columns of a tile of few tokens' logits, which take as long as their rows of the table take through memory: the width with which
