@@ -163,7 +163,8 @@ class SoftmaxLoss(_Tokens):
 
     hidden and dhidden are [tokens, dim], weight and dweight [rows, dim], all of ``dtype`` (float16 or bfloat16); targets hold
     at most ``tokens`` of ``index_dtype``.  Rows may be strided (those of weight by
-    multiples of 8 where dim is one, from a multiple of 16 bytes on); columns are contiguous."""
+    multiples of 8 where dim is one, from a multiple of 16 bytes on); columns are contiguous.  The workspace has room for both
+    directions: up to 512 MB of the logits' gradient (or 512 bytes a token), 100 MB and copies of hidden."""
 
     def __init__(self, rows: int, dim: int, tokens: int, dtype=torch.bfloat16, index_dtype=torch.int64, scale: float = 1.0,
                  device="cuda"):
