@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import tokens_reference as ref
-from bwd_tbe_fwd_gb300 import SoftmaxLoss
+from bwd_tbe_fwd_gb300 import SoftmaxLoss, TokenEmbedding
 from test_gpu_tokens import check_lookup, check_loss, gen, host, loss_inputs, within
 
 pytestmark = pytest.mark.gpu
@@ -254,3 +254,30 @@ def test_a_graph_may_hold_a_process_s_first_calls(tokens, rows):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", CAPTURE.format(tokens=tokens, rows=rows)], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout == "captured\n", r.stdout[-2000:] + r.stderr[-3000:]
+
+
+def test_objects_for_no_tokens_and_calls_of_none():
+    emb, op = TokenEmbedding(10, 8, 0, table_dtype=torch.float16), SoftmaxLoss(10, 8, 0, dtype=torch.float16)
+    w = torch.ones(10, 8, dtype=torch.float16, device="cuda")
+    ids = torch.zeros(0, 5, dtype=torch.int64, device="cuda")
+    out = emb.forward(w, ids)
+    assert out.shape == (0, 5, 8)
+    wide = torch.full((10, 9), 7.0, dtype=torch.float16, device="cuda")
+    assert not bool(emb.backward(out, ids, grad=wide[:, :8]).any()) and bool((wide[:, 8] == 7).all())
+    wide[:, :8] = 7
+    loss, lse, mean = op.forward(out.view(0, 8), w, ids.view(-1))
+    dh, dw = op.backward(out.view(0, 8), w, ids.view(-1), lse, dloss=loss, mean=mean, dweight=wide[:, :8])
+    assert loss.shape == lse.shape == (0,) and dh.shape == (0, 8) and mean.tolist() == [0, 0]
+    assert not bool(dw.any()) and bool((wide[:, 8] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_upstream_gradients_of_padding_are_not_looked_at(dtype):
+    h, w, t, t_h = loss_inputs(300, 200, 40, dtype, seed=11)
+    op = SoftmaxLoss(200, 40, 300, dtype=w.dtype)
+    lse = op.forward(h, w, t)[1]
+    c = torch.rand(300, generator=gen(12)).cuda() + 0.5
+    want = op.backward(h, w, t, lse, dloss=c)
+    c[t < 0], lse[t < 0] = float("inf"), float("nan")
+    assert all(torch.equal(a, b) for a, b in zip(op.backward(h, w, t, lse, dloss=c), want))
+    assert not bool(want[0][t < 0].any())
